@@ -296,6 +296,204 @@ int zero_gather_params(uint64_t psi, uint32_t nd, uint64_t lo, uint64_t len,
  */
 int zero_launch_occupancy(int kernel, int *wgs_per_cu, uint32_t *lds_bytes);
 
+/* ------------------------------------------------------------------------
+ * Residual states: activations kept for the backward pass in 8 bits, the
+ * weight gradient taken from them, and the norms around a block.
+ *
+ * The guide's third class of training memory after optimizer states, gradients
+ * and parameters (section "Como funciona": ZeRO-R treats the residual states,
+ * activations among them) and what produces the local gradient that
+ * zero_reduce_shard takes (card "ZeRO-2", "Gradient lifecycle": a layer's local
+ * gradient is made in backward, then reduced).  The entry points below follow
+ * the conventions at the top of this file.  16-bit matrices are rows x cols with
+ * a row stride in elements (stride >= cols unless there is at most one row);
+ * any stride and any base that its element size divides is accepted, and rows
+ * that start on 16 bytes (8 for codes) are read with wide loads.  Sums are fp32
+ * in a fixed order, so equal inputs give equal bits.
+ * ------------------------------------------------------------------------ */
+
+/* Element types. */
+#define ZERO_F16 0
+#define ZERO_BF16 1
+#define ZERO_F32 2
+
+/* Formats of an 8-bit checkpoint. */
+#define ZERO_CKPT_INT8 0
+#define ZERO_CKPT_E4M3 1
+#define ZERO_CKPT_BLOCK 32 /* columns that share one scale byte */
+
+/*
+ * An 8-bit checkpoint of a rows x cols matrix in device memory: the code of
+ * (r, c) is codes[r * code_stride + c], and its value is
+ *   value(code) * 2^(b - 127),  b = scales[r * scale_stride + c / 32];
+ * b = 0 stands for 0 and b = 255 for NaN.  int8 codes are two's complement
+ * (-127..127), e4m3 codes are 8-bit floats with 4 exponent and 3 mantissa bits,
+ * bias 7, no infinities.  Padding columns between rows are never touched.
+ */
+typedef struct zero_ckpt {
+  uint8_t *codes;
+  uint8_t *scales;
+  uint64_t rows, cols;
+  uint64_t code_stride;  /* bytes between rows of codes, >= cols */
+  uint64_t scale_stride; /* bytes between rows of scales, >= ceil(cols / 32) */
+  int format;            /* ZERO_CKPT_INT8 or ZERO_CKPT_E4M3 */
+} zero_ckpt_t;
+
+/*
+ * Stores x (rows x cols of c, fp16 or bf16) as an 8-bit checkpoint.  Per block of
+ * 32 columns of a row, with amax its largest magnitude:
+ *   int8: 2^e = 2^(floor(log2 amax) - 6), e >= -126;
+ *         code = the whole number nearest to x 2^-e (ties to even), held to
+ *         +-127; the held value is off by at most 2^(e-1), below 2^e where 127
+ *         holds it
+ *   e4m3: x is first held to +-1.875 2^E, E = 15 for fp16 and 127 for bf16;
+ *         e >= -117 is the least with amax 2^-e <= 448; code = the e4m3 value
+ *         nearest to x 2^-e (ties to even)
+ * A block with an infinity or NaN is held as NaN throughout, so an overflow stays
+ * visible in what is computed from it.  A held value of a finite block is
+ * exactly representable in x's type.
+ * Errors: ZERO_E_INVAL (NULL, dtype, format), ZERO_E_RANGE (a stride too small,
+ * size overflow), ZERO_E_ALIGN, ZERO_E_DEVICE (launch failed).
+ */
+int zero_ckpt_write(const void *x, int dtype, uint64_t x_stride, const zero_ckpt_t *c,
+                    void *hip_stream);
+
+/*
+ * Reads a checkpoint back into out (fp16, bf16 or fp32), each value rounded to
+ * nearest even where the type does not hold it.  Errors as zero_ckpt_write.
+ */
+int zero_ckpt_read(const zero_ckpt_t *c, void *out, int dtype, uint64_t out_stride,
+                   void *hip_stream);
+
+/* Bytes of workspace for zero_ckpt_weight_grad at these sizes (0: none). */
+uint64_t zero_ckpt_weight_grad_workspace(uint64_t rows, uint64_t cols, uint64_t n);
+
+/*
+ * The weight gradient of a linear layer y = x W^T (W: n x cols) from the 8-bit
+ * checkpoint of its input: for every (j, c)
+ *   dw[j][c] = sum_{t < rows} dy[t][j] * held(x)[t][c]      (+ dw[j][c] before)
+ * with the held values rounded to dy's type (exact for a checkpoint written from
+ * that type), exact products, fp32 sums and one rounding to dw's type; with
+ * `accumulate` the old value is added in fp32 before it.  rows == 0 gives 0, or
+ * leaves dw with `accumulate`.  dw must not overlap the inputs.
+ * dy: fp16 or bf16, rows x n.  dw: dy's type or fp32.  workspace: device memory,
+ * 16-byte aligned, at least zero_ckpt_weight_grad_workspace bytes, written by the
+ * call; calls that may run at the same time need one each.  n and cols are at
+ * most 2^22.
+ * Errors: ZERO_E_INVAL (NULL, dtype, format, workspace missing), ZERO_E_RANGE (a
+ * stride or the workspace too small, n or cols too large, size overflow),
+ * ZERO_E_ALIGN, ZERO_E_DEVICE (launch failed).
+ */
+int zero_ckpt_weight_grad(const zero_ckpt_t *x, const void *dy, int dtype, uint64_t n,
+                          uint64_t dy_stride, void *dw, int dw_dtype, uint64_t dw_stride,
+                          int accumulate, void *workspace, uint64_t workspace_bytes,
+                          void *hip_stream);
+
+/* Norms. */
+#define ZERO_NORM_NONE 0  /* the identity */
+#define ZERO_NORM_RMS 1   /* x / sqrt(mean x^2 + eps) */
+#define ZERO_NORM_LAYER 2 /* (x - mean x) / sqrt(mean (x - mean x)^2 + eps) */
+#define ZERO_NORM_MAX_COLS 16384
+
+typedef struct zero_norm {
+  int kind;
+  double eps;         /* > 0 and finite, unless kind is ZERO_NORM_NONE */
+  const void *weight; /* cols elements of the call's type, or NULL (ones) */
+  const void *bias;   /* cols elements of the call's type, or NULL (zeros) */
+} zero_norm_t;
+
+/* Where a block's output joins the residual stream (zero_block_norm). */
+typedef struct zero_block_norm {
+  int dtype; /* ZERO_F16 or ZERO_BF16: every matrix and norm parameter */
+  uint64_t rows, cols;
+  const void *res; /* h */
+  uint64_t res_stride;
+  const void *block; /* b, or NULL: h' = h */
+  uint64_t block_stride;
+  const void *gate; /* g, or NULL (ones) */
+  uint64_t gate_stride; /* 0: one row of gates for every token */
+  double scale;
+  zero_norm_t post; /* the norm after the block */
+  zero_norm_t pre;  /* the norm before the next block */
+  void *out;        /* h', or NULL */
+  uint64_t out_stride;
+  void *z; /* rows x cols; NULL if and only if pre.kind is ZERO_NORM_NONE */
+  uint64_t z_stride;
+  float *stats; /* rows x 4 for the backward, 16-byte aligned, or NULL */
+  const zero_ckpt_t *ckpt_block; /* each: a checkpoint to write, or NULL */
+  const zero_ckpt_t *ckpt_out;
+  const zero_ckpt_t *ckpt_z;
+} zero_block_norm_t;
+
+/*
+ * The norms before and after a block, its gate and its residual scale, in one
+ * pass: for each of the rows, in fp32,
+ *   o = post(b);  h' = h + scale * (g . o);  z = pre(h')
+ * where a norm's value is normalised(x) . weight + bias.  z is computed from h'
+ * before its rounding to 16 bits; h' and z are rounded once each.  stats[row] =
+ * {mean, 1/deviation} of post's and then of pre's input (mean 0 for RMS; 0 and 1
+ * without the norm).  Checkpoints hold b, and h' and z after their rounding, as
+ * zero_ckpt_write stores them.
+ * out may be res and z may be block (same address and stride); other overlaps of
+ * an output are undefined.
+ * Errors: ZERO_E_INVAL (NULL, dtype, kind, eps, a gate, post norm or ckpt_block
+ * without a block, nothing to write), ZERO_E_RANGE (cols > ZERO_NORM_MAX_COLS, a
+ * stride too small, a checkpoint of other sizes, size overflow), ZERO_E_ALIGN,
+ * ZERO_E_DEVICE.
+ */
+int zero_block_norm(const zero_block_norm_t *a, void *hip_stream);
+
+/* The backward of zero_block_norm (zero_block_norm_grad). */
+typedef struct zero_block_norm_grad {
+  int dtype;
+  uint64_t rows, cols;
+  const void *dout; /* gradient of h' from its other uses, or NULL (zeros) */
+  uint64_t dout_stride;
+  const void *dz; /* gradient of z; NULL if and only if pre.kind is ZERO_NORM_NONE */
+  uint64_t dz_stride;
+  const zero_ckpt_t *ckpt_out;   /* of h'; needed if pre is a norm */
+  const zero_ckpt_t *ckpt_block; /* of b; needed if post is a norm or dgate is given */
+  const float *stats;            /* as zero_block_norm left them; needed with a norm */
+  const void *gate;
+  uint64_t gate_stride;
+  double scale;
+  zero_norm_t post, pre; /* weights and biases as in the forward */
+  void *dres;            /* gradient of h, or NULL */
+  uint64_t dres_stride;
+  void *dblock; /* gradient of b, or NULL */
+  uint64_t dblock_stride;
+  void *dgate; /* gradient of g, or NULL: a row of grad_dtype when gate_stride is 0, else rows x
+                  cols of dtype */
+  uint64_t dgate_stride;
+  void *dw_pre, *db_pre, *dw_post, *db_post; /* rows of grad_dtype, or NULL */
+  int grad_dtype;                            /* dtype or ZERO_F32 */
+  int accumulate; /* add to the parameters' gradients (and a gate row's) instead of setting them */
+  void *workspace;
+  uint64_t workspace_bytes;
+} zero_block_norm_grad_t;
+
+/* Bytes of workspace for the parameters' gradients at these sizes; none is needed
+ * when no gradient of a parameter is asked for. */
+uint64_t zero_block_norm_grad_workspace(uint64_t rows, uint64_t cols);
+
+/*
+ * With x1 = (held(h') - mean1) r1 and x2 = (held(b) - mean2) r2 from the
+ * checkpoints and stats, q = dz . w_pre, and [.] for layer norms only:
+ *   D = dout + r1 (q - x1 mean(q . x1) - [mean q]);   dres = D
+ *   p = scale D . g;  dgate = scale D . (x2 . w_post + b_post);  v = p . w_post
+ *   dblock = r2 (v - x2 mean(v . x2) - [mean v])
+ *   dw_pre = sum_t dz . x1, db_pre = sum_t dz, dw_post = sum_t p . x2, db_post = sum_t p
+ * in fp32, each output rounded once (a norm of kind NONE passes its gradient on).
+ * dres may be dout and dblock may be dz (same address and stride); other overlaps
+ * of an output are undefined.  Gradients of parameters are summed over the rows
+ * in a fixed order through the workspace (16-byte aligned device memory; calls
+ * that may run at the same time need one each); rows == 0 gives zeros, or leaves
+ * them with `accumulate`.
+ * Errors: as zero_block_norm, and ZERO_E_INVAL for a needed input that is NULL, a
+ * gradient of a weight or bias of a norm of kind NONE, or no output.
+ */
+int zero_block_norm_grad(const zero_block_norm_grad_t *a, void *hip_stream);
+
 /* Message of the calling thread's last error ("" if none).  Valid until the
  * thread's next call into the library. */
 const char *zero_last_error(void);

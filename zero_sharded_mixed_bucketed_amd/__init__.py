@@ -17,6 +17,16 @@ names follow the C ABI in ``include/zero.h``:
     gather_params(psi, nd, lo, length, shards, out)
     launch_occupancy(kernel)                    -> (workgroups per CU, dynamic LDS bytes)
 
+and, for the activations a rank keeps for its backward pass and the local
+gradient they give:
+
+    ckpt_empty(rows, cols, fmt)                 -> Ckpt (an 8-bit checkpoint's buffers)
+    ckpt_write(x, ckpt)                         fp16/bf16 -> 8 bits
+    ckpt_read(ckpt, out)                        8 bits -> fp16/bf16/fp32
+    ckpt_weight_grad(ckpt, dy, dw)              a linear layer's weight gradient
+    block_norm(res, block, out, z, stats)       the norms around a block, gate, residual scale
+    block_norm_grad(dout, dz, ckpt_out, ckpt_block, stats)   their backward
+
 Importing this package fails if libzero.so has not been built: there is no
 fallback path.
 """
@@ -41,11 +51,22 @@ STAGE_DP, STAGE_OS, STAGE_OS_G, STAGE_OS_G_P = 0, 1, 2, 3
 EXPORTS = ("zero_memory_model", "zero_memory_model_k", "zero_comm_volume",
            "zero_shard_geometry", "zero_bucket_intersect", "zero_row_stride",
            "zero_reduce_shard", "zero_adam_scalars", "zero_adam_step_shard",
-           "zero_gather_params", "zero_launch_occupancy", "zero_last_error")
+           "zero_gather_params", "zero_launch_occupancy", "zero_last_error",
+           "zero_ckpt_write", "zero_ckpt_read", "zero_ckpt_weight_grad",
+           "zero_ckpt_weight_grad_workspace", "zero_block_norm", "zero_block_norm_grad",
+           "zero_block_norm_grad_workspace")
 
 # Kernels of zero_launch_occupancy.
 KERNEL_REDUCE_W16, KERNEL_REDUCE_W8, KERNEL_REDUCE_W4, KERNEL_REDUCE_W2 = 0, 1, 2, 3
 KERNEL_ADAM_G32, KERNEL_ADAM_G16 = 4, 5
+
+# Formats of an 8-bit checkpoint, and the columns that share a scale byte.
+CKPT_INT8, CKPT_E4M3 = 0, 1
+CKPT_BLOCK = 32
+
+# Kinds of norm, and the widest row they take.
+NORM_NONE, NORM_RMS, NORM_LAYER = 0, 1, 2
+NORM_MAX_COLS = 16384
 
 
 class ZeroError(RuntimeError):
@@ -74,6 +95,47 @@ class Shard(ctypes.Structure):
                 ("grad", ctypes.c_void_p), ("grad_is_fp16", ctypes.c_int),
                 ("param16", ctypes.c_void_p), ("param16_origin", ctypes.c_uint64),
                 ("param16_len", ctypes.c_uint64)]
+
+
+class _CkptArg(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("rows", ctypes.c_uint64), ("cols", ctypes.c_uint64),
+                ("code_stride", ctypes.c_uint64), ("scale_stride", ctypes.c_uint64),
+                ("format", ctypes.c_int)]
+
+
+class _NormArg(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int), ("eps", ctypes.c_double), ("weight", ctypes.c_void_p),
+                ("bias", ctypes.c_void_p)]
+
+
+class _BlockNormArg(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("rows", ctypes.c_uint64), ("cols", ctypes.c_uint64),
+                ("res", ctypes.c_void_p), ("res_stride", ctypes.c_uint64),
+                ("block", ctypes.c_void_p), ("block_stride", ctypes.c_uint64),
+                ("gate", ctypes.c_void_p), ("gate_stride", ctypes.c_uint64),
+                ("scale", ctypes.c_double), ("post", _NormArg), ("pre", _NormArg),
+                ("out", ctypes.c_void_p), ("out_stride", ctypes.c_uint64),
+                ("z", ctypes.c_void_p), ("z_stride", ctypes.c_uint64),
+                ("stats", ctypes.c_void_p), ("ckpt_block", ctypes.POINTER(_CkptArg)),
+                ("ckpt_out", ctypes.POINTER(_CkptArg)), ("ckpt_z", ctypes.POINTER(_CkptArg))]
+
+
+class _BlockNormGradArg(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("rows", ctypes.c_uint64), ("cols", ctypes.c_uint64),
+                ("dout", ctypes.c_void_p), ("dout_stride", ctypes.c_uint64),
+                ("dz", ctypes.c_void_p), ("dz_stride", ctypes.c_uint64),
+                ("ckpt_out", ctypes.POINTER(_CkptArg)),
+                ("ckpt_block", ctypes.POINTER(_CkptArg)), ("stats", ctypes.c_void_p),
+                ("gate", ctypes.c_void_p), ("gate_stride", ctypes.c_uint64),
+                ("scale", ctypes.c_double), ("post", _NormArg), ("pre", _NormArg),
+                ("dres", ctypes.c_void_p), ("dres_stride", ctypes.c_uint64),
+                ("dblock", ctypes.c_void_p), ("dblock_stride", ctypes.c_uint64),
+                ("dgate", ctypes.c_void_p), ("dgate_stride", ctypes.c_uint64),
+                ("dw_pre", ctypes.c_void_p), ("db_pre", ctypes.c_void_p),
+                ("dw_post", ctypes.c_void_p), ("db_post", ctypes.c_void_p),
+                ("grad_dtype", ctypes.c_int), ("accumulate", ctypes.c_int),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_uint64)]
 
 
 def hip_runtimes() -> set:
@@ -123,6 +185,21 @@ def _load() -> ctypes.CDLL:
     lib.zero_gather_params.restype = ci
     lib.zero_launch_occupancy.argtypes = [ci, ctypes.POINTER(ci), ctypes.POINTER(u32)]
     lib.zero_launch_occupancy.restype = ci
+    K = ctypes.POINTER(_CkptArg)
+    lib.zero_ckpt_write.argtypes = [vp, ci, u64, K, vp]
+    lib.zero_ckpt_write.restype = ci
+    lib.zero_ckpt_read.argtypes = [K, vp, ci, u64, vp]
+    lib.zero_ckpt_read.restype = ci
+    lib.zero_ckpt_weight_grad_workspace.argtypes = [u64, u64, u64]
+    lib.zero_ckpt_weight_grad_workspace.restype = u64
+    lib.zero_ckpt_weight_grad.argtypes = [K, vp, ci, u64, u64, vp, ci, u64, ci, vp, u64, vp]
+    lib.zero_ckpt_weight_grad.restype = ci
+    lib.zero_block_norm.argtypes = [ctypes.POINTER(_BlockNormArg), vp]
+    lib.zero_block_norm.restype = ci
+    lib.zero_block_norm_grad_workspace.argtypes = [u64, u64]
+    lib.zero_block_norm_grad_workspace.restype = u64
+    lib.zero_block_norm_grad.argtypes = [ctypes.POINTER(_BlockNormGradArg), vp]
+    lib.zero_block_norm_grad.restype = ci
     lib.zero_last_error.argtypes = []
     lib.zero_last_error.restype = ctypes.c_char_p
     return lib
@@ -316,3 +393,307 @@ def gather_params(psi: int, nd: int, lo: int, length: int, shards, out, stream=N
         raise ValueError("out must be contiguous")
     _launch((shards, out), stream, lambda h: lib.zero_gather_params(
         psi, nd, lo, length, shards.data_ptr(), shards.stride(0), out.data_ptr(), h))
+
+
+# ---------------------------------------------------------------------------
+# Activations: 8-bit checkpoints, the weight gradient from them, block norms.
+
+def _dtype_code(t) -> int:
+    import torch
+    return {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}[t.dtype]
+
+
+def _matrix(t, name, dtypes, rows=None, cols=None):
+    """A device matrix with unit column stride and, if given, these sizes."""
+    _dev(t, name, dtypes)
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be a matrix with unit column stride")
+    if rows is not None and tuple(t.shape) != (rows, cols):
+        raise ValueError(f"{name} is {tuple(t.shape)}, expected {(rows, cols)}")
+
+
+def _stride(t) -> int:
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _row(t, name, dtype, cols):
+    _dev(t, name, (dtype,))
+    if t.dim() != 1 or t.shape[0] != cols or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous row of {cols}")
+
+
+class Ckpt:
+    """An 8-bit checkpoint's buffers: codes uint8 [rows, cols] and scales uint8
+    [rows, ceil(cols / 32)], each with unit column stride, in format CKPT_INT8
+    or CKPT_E4M3."""
+
+    def __init__(self, codes, scales, fmt: int):
+        import torch
+        if fmt not in (CKPT_INT8, CKPT_E4M3):
+            raise ValueError(f"unknown checkpoint format {fmt}")
+        for name, t in (("codes", codes), ("scales", scales)):
+            if not isinstance(t, torch.Tensor) or t.dtype != torch.uint8 or t.dim() != 2 \
+                    or (t.shape[1] > 1 and t.stride(1) != 1):
+                raise ValueError(f"{name} must be a uint8 matrix with unit column stride")
+        rows, cols = codes.shape
+        if tuple(scales.shape) != (rows, -(-cols // CKPT_BLOCK)):
+            raise ValueError(f"scales is {tuple(scales.shape)}, expected "
+                             f"{(rows, -(-cols // CKPT_BLOCK))}")
+        if codes.device != scales.device:
+            raise ValueError(f"codes and scales are on {codes.device} and {scales.device}")
+        self.codes, self.scales, self.fmt = codes, scales, fmt
+
+    @property
+    def rows(self) -> int:
+        return self.codes.shape[0]
+
+    @property
+    def cols(self) -> int:
+        return self.codes.shape[1]
+
+    def tensors(self):
+        return self.codes, self.scales
+
+    def resident_bytes(self) -> int:
+        return self.codes.numel() + self.scales.numel()
+
+    def row_range(self, lo: int, hi: int) -> "Ckpt":
+        """The checkpoint of rows [lo, hi), sharing memory: a rank of a group that
+        partitions a checkpoint by tokens writes its own range, and a checkpoint
+        gathered in rank order is read as one."""
+        return Ckpt(self.codes[lo:hi], self.scales[lo:hi], self.fmt)
+
+    def _arg(self):
+        for name, t in (("codes", self.codes), ("scales", self.scales)):
+            if not t.is_cuda:
+                raise ValueError(f"{name} must be a device tensor")
+        a = _CkptArg()
+        a.codes, a.scales = self.codes.data_ptr(), self.scales.data_ptr()
+        a.rows, a.cols = self.codes.shape
+        a.code_stride, a.scale_stride = _stride(self.codes), _stride(self.scales)
+        a.format = self.fmt
+        return a
+
+
+def ckpt_empty(rows: int, cols: int, fmt: int = CKPT_INT8, device=None) -> Ckpt:
+    """Uninitialised buffers of a checkpoint, code rows on 16 bytes."""
+    import torch
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else device
+    codes = torch.empty((rows, -(-cols // 16) * 16), dtype=torch.uint8, device=dev)[:, :cols]
+    scales = torch.empty((rows, -(-cols // CKPT_BLOCK)), dtype=torch.uint8, device=dev)
+    return Ckpt(codes, scales, fmt)
+
+
+def _workspace(nbytes, dev, stream):
+    """Workspace of one call, from the caching allocator of the call's stream."""
+    import torch
+    if nbytes == 0:
+        return None
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+
+
+def _given_workspace(workspace, need, dev, stream):
+    import torch
+    if workspace is None:
+        return _workspace(need, dev, stream)
+    _dev(workspace, "workspace", (torch.uint8,), need)
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace
+
+
+def ckpt_write(x, ckpt: Ckpt, stream=None) -> None:
+    """Stores x (float16/bfloat16 [rows, cols], any row stride) in 8 bits."""
+    import torch
+    _matrix(x, "x", (torch.float16, torch.bfloat16), ckpt.rows, ckpt.cols)
+    arg = ckpt._arg()
+    _launch((x, *ckpt.tensors()), stream, lambda h: lib.zero_ckpt_write(
+        x.data_ptr(), _dtype_code(x), _stride(x), ctypes.byref(arg), h))
+
+
+def ckpt_read(ckpt: Ckpt, out, stream=None) -> None:
+    """Reads the held values into out (float16/bfloat16/float32 [rows, cols])."""
+    import torch
+    _matrix(out, "out", (torch.float16, torch.bfloat16, torch.float32), ckpt.rows, ckpt.cols)
+    arg = ckpt._arg()
+    _launch((out, *ckpt.tensors()), stream, lambda h: lib.zero_ckpt_read(
+        ctypes.byref(arg), out.data_ptr(), _dtype_code(out), _stride(out), h))
+
+
+def ckpt_weight_grad_workspace(rows: int, cols: int, n: int) -> int:
+    """Bytes of workspace of ckpt_weight_grad at these sizes (0: none)."""
+    return lib.zero_ckpt_weight_grad_workspace(rows, cols, n)
+
+
+def ckpt_weight_grad(ckpt: Ckpt, dy, dw, accumulate: bool = False, workspace=None,
+                     stream=None) -> None:
+    """dw (+)= dy^T x of a linear layer y = x W^T, from its input's checkpoint.
+
+    dy: float16/bfloat16 [rows, n]; dw: dy's type or float32 [n, cols], e.g. the
+    tensor's place in the flat local gradient.  workspace: uint8 device tensor of
+    ckpt_weight_grad_workspace bytes, or None to take it from torch's allocator.
+    """
+    import torch
+    _matrix(dy, "dy", (torch.float16, torch.bfloat16))
+    if dy.shape[0] != ckpt.rows:
+        raise ValueError(f"dy has {dy.shape[0]} rows, the checkpoint {ckpt.rows}")
+    n = dy.shape[1]
+    _matrix(dw, "dw", (dy.dtype, torch.float32), n, ckpt.cols)
+    _one_device((dy, dw, *ckpt.tensors()), stream)
+    arg = ckpt._arg()
+    ws = _given_workspace(workspace, ckpt_weight_grad_workspace(ckpt.rows, ckpt.cols, n),
+                          dy.device, stream)
+    _launch((dy, dw, ws, *ckpt.tensors()), stream, lambda h: lib.zero_ckpt_weight_grad(
+        ctypes.byref(arg), dy.data_ptr(), _dtype_code(dy), n, _stride(dy), dw.data_ptr(),
+        _dtype_code(dw), _stride(dw), int(bool(accumulate)),
+        ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0, h))
+
+
+class Norm:
+    """A norm: kind NORM_RMS or NORM_LAYER (or NORM_NONE), eps, and a row of
+    weights and of biases (None: ones, zeros)."""
+
+    def __init__(self, kind: int = NORM_NONE, eps: float = 1e-5, weight=None, bias=None):
+        self.kind, self.eps, self.weight, self.bias = kind, eps, weight, bias
+
+    def tensors(self):
+        return tuple(t for t in (self.weight, self.bias) if t is not None)
+
+    def _arg(self, name, dtype, cols):
+        a = _NormArg()
+        a.kind, a.eps = self.kind, self.eps
+        for what in ("weight", "bias"):
+            t = getattr(self, what)
+            if t is not None:
+                _row(t, f"{name} {what}", dtype, cols)
+                setattr(a, what, t.data_ptr())
+        return a
+
+
+_NO_NORM = Norm()
+
+
+def _gate_stride(gate, dtype, rows, cols) -> int:
+    if gate.dim() == 1:
+        _row(gate, "gate", dtype, cols)
+        return 0
+    _matrix(gate, "gate", (dtype,), rows, cols)
+    if _stride(gate) == 0:
+        raise ValueError("gate: give one row for every token as a [cols] tensor")
+    return _stride(gate)
+
+
+def _stats(stats, rows):
+    import torch
+    _dev(stats, "stats", (torch.float32,))
+    if tuple(stats.shape) != (rows, 4) or not stats.is_contiguous():
+        raise ValueError(f"stats must be a contiguous [{rows}, 4] tensor")
+    return stats.data_ptr()
+
+
+def block_norm(res, block, out, z, stats, post: Optional[Norm] = None,
+               pre: Optional[Norm] = None, gate=None, scale: float = 1.0,
+               ckpt_block: Optional[Ckpt] = None, ckpt_out: Optional[Ckpt] = None,
+               ckpt_z: Optional[Ckpt] = None, stream=None) -> None:
+    """out = res + scale * gate . post(block);  z = pre(out), in one pass.
+
+    res, block, out, z: float16 or bfloat16 [rows, cols] of one type; block None:
+    out = res; out or stats None: not written; z None exactly when pre is None.
+    gate: None, [cols] (every token) or [rows, cols].  stats: float32 [rows, 4]
+    for the backward.  ckpt_*: checkpoints of block, out and z to write too.  out
+    may be res and z may be block.
+    """
+    import torch
+    _matrix(res, "res", (torch.float16, torch.bfloat16))
+    (rows, cols), dt = res.shape, res.dtype
+    post, pre = post or _NO_NORM, pre or _NO_NORM
+    a = _BlockNormArg()
+    a.dtype, a.rows, a.cols, a.scale = _dtype_code(res), rows, cols, scale
+    a.post, a.pre = post._arg("post", dt, cols), pre._arg("pre", dt, cols)
+    a.res, a.res_stride = res.data_ptr(), _stride(res)
+    for name, t in (("block", block), ("out", out), ("z", z)):
+        if t is not None:
+            _matrix(t, name, (dt,), rows, cols)
+            setattr(a, name, t.data_ptr())
+            setattr(a, name + "_stride", _stride(t))
+    if gate is not None:
+        a.gate, a.gate_stride = gate.data_ptr(), _gate_stride(gate, dt, rows, cols)
+    if stats is not None:
+        a.stats = _stats(stats, rows)
+    tensors = [res, block, out, z, stats, gate, *post.tensors(), *pre.tensors()]
+    for name, k in (("ckpt_block", ckpt_block), ("ckpt_out", ckpt_out), ("ckpt_z", ckpt_z)):
+        if k is not None:
+            setattr(a, name, ctypes.pointer(k._arg()))
+            tensors += k.tensors()
+    _launch(tensors, stream, lambda h: lib.zero_block_norm(ctypes.byref(a), h))
+
+
+def block_norm_grad_workspace(rows: int, cols: int) -> int:
+    """Bytes of workspace of block_norm_grad's parameter gradients."""
+    return lib.zero_block_norm_grad_workspace(rows, cols)
+
+
+def block_norm_grad(dout, dz, ckpt_out: Optional[Ckpt], ckpt_block: Optional[Ckpt], stats,
+                    post: Optional[Norm] = None, pre: Optional[Norm] = None, gate=None,
+                    scale: float = 1.0, dres=None, dblock=None, dgate=None, dw_pre=None,
+                    db_pre=None, dw_post=None, db_post=None, accumulate: bool = False,
+                    workspace=None, stream=None) -> None:
+    """The backward of block_norm from the checkpoints of its output and block.
+
+    dout: gradient of out from its other uses, or None; dz: gradient of z.  The
+    outputs given are written: dres and dblock [rows, cols]; dgate like the gate;
+    dw_* and db_* rows of the norms' weights and biases.  Those rows (and the row
+    of a [cols] gate) have one type, the call's or float32, and are added to with
+    `accumulate`.  dres may be dout and dblock may be dz.
+    """
+    import torch
+    first = next((t for t in (dz, dout, dres, dblock) if t is not None), None)
+    if first is None:
+        raise ValueError("dout, dz, dres and dblock are all None")
+    _matrix(first, "the gradient", (torch.float16, torch.bfloat16))
+    (rows, cols), dt = first.shape, first.dtype
+    post, pre = post or _NO_NORM, pre or _NO_NORM
+    a = _BlockNormGradArg()
+    a.dtype, a.rows, a.cols, a.scale = _dtype_code(first), rows, cols, scale
+    a.post, a.pre = post._arg("post", dt, cols), pre._arg("pre", dt, cols)
+    for name, t in (("dout", dout), ("dz", dz), ("dres", dres), ("dblock", dblock)):
+        if t is not None:
+            _matrix(t, name, (dt,), rows, cols)
+            setattr(a, name, t.data_ptr())
+            setattr(a, name + "_stride", _stride(t))
+    sums = {"dw_pre": dw_pre, "db_pre": db_pre, "dw_post": dw_post, "db_post": db_post}
+    if gate is not None:
+        a.gate, a.gate_stride = gate.data_ptr(), _gate_stride(gate, dt, rows, cols)
+        if gate.dim() == 1:
+            sums["dgate"] = dgate
+        elif dgate is not None:
+            _matrix(dgate, "dgate", (dt,), rows, cols)
+            a.dgate, a.dgate_stride = dgate.data_ptr(), _stride(dgate)
+    elif dgate is not None:
+        raise ValueError("dgate without a gate")
+    sums = {k: t for k, t in sums.items() if t is not None}
+    grad_dtype = next(iter(sums.values())).dtype if sums else dt
+    if grad_dtype not in (dt, torch.float32):
+        raise ValueError(f"parameter gradients have dtype {grad_dtype}, expected {dt} or float32")
+    for name, t in sums.items():
+        _row(t, name, grad_dtype, cols)
+        setattr(a, name, t.data_ptr())
+    a.grad_dtype = 2 if grad_dtype == torch.float32 else a.dtype
+    a.accumulate = int(bool(accumulate))
+    if stats is not None:
+        a.stats = _stats(stats, rows)
+    tensors = [dout, dz, stats, gate, dres, dblock, dgate, *sums.values(), *post.tensors(),
+               *pre.tensors()]
+    for name, k in (("ckpt_out", ckpt_out), ("ckpt_block", ckpt_block)):
+        if k is not None:
+            setattr(a, name, ctypes.pointer(k._arg()))
+            tensors += k.tensors()
+    _one_device([t for t in tensors if t is not None], stream)
+    need = block_norm_grad_workspace(rows, cols) if sums else 0
+    ws = _given_workspace(workspace, need, first.device, stream)
+    if ws is not None:
+        a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel()
+    _launch([*tensors, ws], stream, lambda h: lib.zero_block_norm_grad(ctypes.byref(a), h))

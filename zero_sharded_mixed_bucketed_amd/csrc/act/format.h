@@ -1,0 +1,269 @@
+// Device arithmetic shared by the activation-side kernels: 16-bit loads and
+// stores of 8-element chunks, the 8-bit checkpoint format, and sums over a
+// wavefront.
+//
+// The checkpoint format: rows of 8-bit codes in blocks of 32 columns, one scale
+// byte b per block that stands for 2^(b - 127); b = 0 stands for 0 and b = 255
+// for NaN.  A scale that is a power of two makes every held value exactly
+// representable in the 16-bit type it came from (7 significant bits of an int8
+// code, 4 of an e4m3 code, against 11 of fp16 and 8 of bf16), so whatever reads
+// a checkpoint back rounds nothing a second time.
+#ifndef ZERO_ACT_FORMAT_H_
+#define ZERO_ACT_FORMAT_H_
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#pragma clang fp contract(fast)
+
+namespace zero {
+namespace act {
+
+constexpr int kF16 = 0, kBf16 = 1, kF32 = 2;   // ZERO_F16, ZERO_BF16, ZERO_F32
+constexpr int kInt8 = 0, kE4m3 = 1;            // ZERO_CKPT_INT8, ZERO_CKPT_E4M3
+constexpr int kBlock = 32;                     // ZERO_CKPT_BLOCK
+constexpr int kChunk = 8;                      // columns a thread handles together
+constexpr int kQuad = kBlock / kChunk;         // neighbouring lanes that share a block
+
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+struct F16 { static constexpr int kType = kF16; };
+struct Bf16 { static constexpr int kType = kBf16; };
+
+// ------------------------------------------------------------ 16-bit values
+
+template <typename T>
+__device__ __forceinline__ float lo16(uint32_t w) {
+  if constexpr (T::kType == kF16)
+    return static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(w)));
+  else
+    return __builtin_bit_cast(float, w << 16);
+}
+
+template <typename T>
+__device__ __forceinline__ float hi16(uint32_t w) {
+  if constexpr (T::kType == kF16)
+    return static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(w >> 16)));
+  else
+    return __builtin_bit_cast(float, w & 0xFFFF0000u);
+}
+
+// One rounding to nearest even per value.
+template <typename T>
+__device__ __forceinline__ uint32_t pack16(float a, float b) {
+  if constexpr (T::kType == kF16) {
+    const uint32_t x = __builtin_bit_cast(uint16_t, static_cast<_Float16>(a));
+    const uint32_t y = __builtin_bit_cast(uint16_t, static_cast<_Float16>(b));
+    return x | (y << 16);
+  } else {
+    typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
+    typedef float f2 __attribute__((ext_vector_type(2)));
+    const f2 v = {a, b};
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf2));
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void unpack8(u32x4 w, float (&x)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = lo16<T>(w[i]);
+    x[2 * i + 1] = hi16<T>(w[i]);
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ u32x4 pack8(const float (&x)[8]) {
+  u32x4 w;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = pack16<T>(x[2 * i], x[2 * i + 1]);
+  return w;
+}
+
+// Eight 16-bit elements of a row from column c on; columns from `cols` on read
+// as 0 and are not touched.  `wide`: the row starts on 16 bytes.
+__device__ __forceinline__ u32x4 load8(const uint16_t* row, uint64_t c, uint64_t cols, bool wide) {
+  if (wide && c + kChunk <= cols) return *reinterpret_cast<const u32x4*>(row + c);
+  u32x4 w = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (c + i < cols) w[i >> 1] |= static_cast<uint32_t>(row[c + i]) << (16 * (i & 1));
+  return w;
+}
+
+__device__ __forceinline__ void store8(uint16_t* row, uint64_t c, uint64_t cols, bool wide,
+                                       u32x4 w) {
+  if (wide && c + kChunk <= cols) {
+    *reinterpret_cast<u32x4*>(row + c) = w;
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (c + i < cols) row[c + i] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
+}
+
+// Eight codes; `wide`: the row starts on 8 bytes.
+__device__ __forceinline__ u32x2 load_codes(const uint8_t* row, uint64_t c, uint64_t cols,
+                                            bool wide) {
+  if (wide && c + kChunk <= cols) return *reinterpret_cast<const u32x2*>(row + c);
+  u32x2 w = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (c + i < cols) w[i >> 2] |= static_cast<uint32_t>(row[c + i]) << (8 * (i & 3));
+  return w;
+}
+
+__device__ __forceinline__ void store_codes(uint8_t* row, uint64_t c, uint64_t cols, bool wide,
+                                            u32x2 w) {
+  if (wide && c + kChunk <= cols) {
+    *reinterpret_cast<u32x2*>(row + c) = w;
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (c + i < cols) row[c + i] = static_cast<uint8_t>(w[i >> 2] >> (8 * (i & 3)));
+}
+
+// ------------------------------------------------------------ the 8-bit format
+
+// 2^(b - 127) of a scale byte: its exponent field; 0 -> 0, 255 -> NaN.
+__device__ __forceinline__ float scale_of(uint32_t b) {
+  return __builtin_bit_cast(float, b == 255u ? 0x7FC00000u : b << 23);
+}
+
+template <int FMT>
+__device__ __forceinline__ void decode4(uint32_t w, float s, float* x) {
+  if constexpr (FMT == kInt8) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      x[i] = static_cast<float>(static_cast<int8_t>(w >> (8 * i))) * s;
+  } else {
+    typedef float f2 __attribute__((ext_vector_type(2)));
+    const f2 a = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(w), false);
+    const f2 b = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(w), true);
+    x[0] = a[0] * s;
+    x[1] = a[1] * s;
+    x[2] = b[0] * s;
+    x[3] = b[1] * s;
+  }
+}
+
+template <int FMT>
+__device__ __forceinline__ void decode8(u32x2 w, float s, float (&x)[8]) {
+  decode4<FMT>(w[0], s, x);
+  decode4<FMT>(w[1], s, x + 4);
+}
+
+// The value of lane i ^ 1, i ^ 2 within each quad of lanes.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return static_cast<uint32_t>(
+      __builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, 0xF, 0xF, true));
+}
+constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kHalfMirror = 0x141, kMirror = 0x140;
+
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  typedef uint16_t us2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(us2, a),
+                                                                __builtin_bit_cast(us2, b)));
+}
+
+// Encodes this lane's eight 16-bit elements of a block that four neighbouring
+// lanes share (all four call this together).  The block's largest magnitude is
+// found on the bit patterns, whose order as whole numbers is that of the
+// magnitudes, with infinities and NaN above every finite value.
+//   int8:  2^e = 2^(floor(log2 amax) - 6); codes rounded to nearest even and
+//          held to +-127 (amax 2^-e lies in [64, 128)).
+//   e4m3:  2^e is the least power of two with amax 2^-e <= 448; inputs are held
+//          to 1.875 times the type's top power of two, which is the largest
+//          value that 4 significant bits and the type both hold.
+// A block with an infinity or NaN becomes NaN as a whole, so an overflow stays
+// visible.  e is at least -126 (int8) or -117 (e4m3): every held value is a
+// normal fp32 number or 0.
+template <typename T, int FMT>
+__device__ __forceinline__ u32x2 encode8(u32x4 w, uint32_t* scale) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = max_u16x2(m, w[i] & 0x7FFF7FFFu);
+  m = max_u16x2(m, dpp<kXor1>(m));
+  m = max_u16x2(m, dpp<kXor2>(m));
+  const uint32_t hi = m >> 16, lo = m & 0xFFFFu;
+  const uint32_t top = hi > lo ? hi : lo;
+  constexpr uint32_t kInf = T::kType == kF16 ? 0x7C00u : 0x7F80u;
+  const uint32_t bits = __builtin_bit_cast(uint32_t, lo16<T>(top));
+  int e;
+  if constexpr (FMT == kInt8) {
+    e = static_cast<int>(bits >> 23) - 127 - 6;
+    e = e < -126 ? -126 : e;
+  } else {
+    constexpr float kTop = T::kType == kF16 ? 0x1.Ep15f : 0x1.Ep127f;
+    const uint32_t held = bits < __builtin_bit_cast(uint32_t, kTop)
+                              ? bits : __builtin_bit_cast(uint32_t, kTop);
+    // the mantissa of 448 is 1.75: anything above it carries into the exponent
+    e = static_cast<int>((held + 0x1FFFFFu) >> 23) - 127 - 8;
+    e = e < -117 ? -117 : e;
+  }
+  const bool finite = top < kInf;
+  *scale = finite ? static_cast<uint32_t>(e + 127) : 255u;
+  const float inv = __builtin_bit_cast(float, static_cast<uint32_t>(127 - e) << 23);
+  float x[8];
+  unpack8<T>(w, x);
+  u32x2 out;
+  if constexpr (FMT == kInt8) {
+    // adding 1.5 * 2^23 rounds to a whole number (nearest even) and leaves it in
+    // the low mantissa bits in two's complement
+    constexpr float kMagic = 0x1.8p23f;
+    uint32_t q[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float y = __builtin_fmaf(x[i], inv, kMagic);
+      q[i] = __builtin_bit_cast(uint32_t,
+                                __builtin_amdgcn_fmed3f(y, kMagic - 127.f, kMagic + 127.f));
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t a = __builtin_amdgcn_perm(q[4 * i + 1], q[4 * i], 0x0C0C0400u);
+      const uint32_t b = __builtin_amdgcn_perm(q[4 * i + 3], q[4 * i + 2], 0x04000C0Cu);
+      out[i] = a | b;
+    }
+  } else {
+    constexpr float kTop = T::kType == kF16 ? 0x1.Ep15f : 0x1.Ep127f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = __builtin_amdgcn_fmed3f(x[i], -kTop, kTop) * inv;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      int p = __builtin_amdgcn_cvt_pk_fp8_f32(x[4 * i], x[4 * i + 1], 0, false);
+      p = __builtin_amdgcn_cvt_pk_fp8_f32(x[4 * i + 2], x[4 * i + 3], p, true);
+      out[i] = static_cast<uint32_t>(p);
+    }
+  }
+  if (!finite) out = u32x2{0, 0};
+  return out;
+}
+
+// ------------------------------------------------------------ sums
+
+__device__ __forceinline__ float dpp_add(float v, uint32_t moved) {
+  return v + __builtin_bit_cast(float, moved);
+}
+
+// The sum over the 64 lanes, in every lane; the order is fixed.
+__device__ __forceinline__ float wave_sum(float v) {
+  v = dpp_add(v, dpp<kXor1>(__builtin_bit_cast(uint32_t, v)));
+  v = dpp_add(v, dpp<kXor2>(__builtin_bit_cast(uint32_t, v)));
+  v = dpp_add(v, dpp<kHalfMirror>(__builtin_bit_cast(uint32_t, v)));
+  v = dpp_add(v, dpp<kMirror>(__builtin_bit_cast(uint32_t, v)));
+  const int b = __builtin_bit_cast(int, v);
+  const float r0 = __builtin_bit_cast(float, __builtin_amdgcn_readlane(b, 0));
+  const float r1 = __builtin_bit_cast(float, __builtin_amdgcn_readlane(b, 16));
+  const float r2 = __builtin_bit_cast(float, __builtin_amdgcn_readlane(b, 32));
+  const float r3 = __builtin_bit_cast(float, __builtin_amdgcn_readlane(b, 48));
+  return (r0 + r1) + (r2 + r3);
+}
+
+}  // namespace act
+}  // namespace zero
+
+#endif  // ZERO_ACT_FORMAT_H_

@@ -9,14 +9,16 @@
 #include <map>
 #include <mutex>
 
+#include "act/launch.h"
 #include "kernels.h"
 #include "zero.h"
 
+namespace zero {
 namespace {
 
 thread_local char g_err[512];
 
-constexpr uint32_t kMaxReduceNd = 1u << 24;
+}  // namespace
 
 int fail(int code, const char* fmt, ...) {
   va_list ap;
@@ -30,6 +32,17 @@ int ok() {
   g_err[0] = '\0';
   return ZERO_OK;
 }
+
+const char* last_error() { return g_err; }
+
+}  // namespace zero
+
+namespace {
+
+using zero::fail;
+using zero::ok;
+
+constexpr uint32_t kMaxReduceNd = 1u << 24;
 
 // Resident workgroups per compute unit of `fn` with `lds` bytes of dynamic LDS,
 // from the runtime's occupancy calculator.
@@ -403,6 +416,6 @@ int zero_launch_occupancy(int kernel, int* wgs_per_cu, uint32_t* lds_bytes) {
   return ok();
 }
 
-const char* zero_last_error(void) { return g_err; }
+const char* zero_last_error(void) { return zero::last_error(); }
 
 }  // extern "C"

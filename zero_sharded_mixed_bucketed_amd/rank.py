@@ -19,6 +19,11 @@ and "Gradient lifecycle"):
   flat vector (16 Psi / Nd bytes in all).  Each layer's parameters are gathered
   from the rank shards just in time (gather_layer) and released after use.
 
+In backward a rank makes the local gradients that the reduce takes: linear_grad
+and norm_grad write the gradients of a layer's tensors to their flat places in
+the local gradient (stage 1) or in the bucket that is being filled (stages 2 and
+3), from activations kept in 8 bits (checkpoint; the guide's residual states).
+
 This module allocates with torch and calls the library; no arithmetic of the
 path happens here.
 """
@@ -28,7 +33,8 @@ from typing import Optional
 
 import torch
 
-from . import adam_step_shard, gather_params, memory_model, reduce_shard, shard_geometry
+from . import (CKPT_INT8, Ckpt, adam_step_shard, block_norm_grad, ckpt_empty, ckpt_weight_grad,
+               gather_params, memory_model, reduce_shard, shard_geometry)
 
 STAGE_OS = 1
 STAGE_OS_G = 2
@@ -126,3 +132,43 @@ class RankState:
         if self.stage != STAGE_OS_G_P:
             raise ValueError("only stage 3 gathers parameters")
         gather_params(self.geom.psi, self.geom.nd, lo, length, shards, out, stream=stream)
+
+    def checkpoint(self, tokens: int, width: int, fmt: int = CKPT_INT8) -> Ckpt:
+        """Buffers for `tokens` activations of `width` columns in 8 bits: 1 + 1/32
+        bytes an element (width a multiple of 32) where 16 bits take 2."""
+        return ckpt_empty(tokens, width, fmt, device=self.master.device)
+
+    def grad_slot(self, flat_lo: int, count: int, bucket=None, bucket_offset: int = 0):
+        """The fp16 elements of flat [flat_lo, flat_lo + count) of the local gradient:
+        in stage 1's retained one, or in `bucket`, a contiguous fp16 row that starts
+        at flat index bucket_offset."""
+        if bucket is None:
+            if self.stage != STAGE_OS:
+                raise ValueError("stages 2 and 3 keep no local gradient: give the bucket")
+            bucket, bucket_offset = self.local_grad, 0
+        elif bucket.dtype not in (torch.int16, torch.float16) or bucket.dim() != 1 \
+                or not bucket.is_contiguous():
+            raise ValueError("bucket must be a contiguous fp16 row")
+        lo = flat_lo - bucket_offset
+        if count < 0 or lo < 0 or lo + count > bucket.numel() \
+                or flat_lo + count > self.geom.psi:
+            raise ValueError(f"flat [{flat_lo}, +{count}) lies outside the local gradient")
+        return bucket[lo:lo + count].view(torch.float16)
+
+    def linear_grad(self, flat_lo: int, ckpt: Ckpt, dy, bucket=None, bucket_offset: int = 0,
+                    accumulate: bool = False, workspace=None, stream=None) -> None:
+        """The gradient of a linear layer's weight (dy.shape[1] x ckpt.cols, at flat
+        index flat_lo) from its input's checkpoint, into the local gradient."""
+        n, k = dy.shape[1], ckpt.cols
+        dw = self.grad_slot(flat_lo, n * k, bucket, bucket_offset).view(n, k)
+        ckpt_weight_grad(ckpt, dy, dw, accumulate=accumulate, workspace=workspace, stream=stream)
+
+    def norm_grad(self, places, dout, dz, ckpt_out, ckpt_block, stats, bucket=None,
+                  bucket_offset: int = 0, **call) -> None:
+        """block_norm_grad with the parameters' gradients in the local gradient:
+        places maps dw_pre, db_pre, dw_post, db_post and dgate (a gate of one row) to
+        their flat indices."""
+        first = next(t for t in (dz, dout) if t is not None)
+        slots = {name: self.grad_slot(lo, first.shape[1], bucket, bucket_offset)
+                 for name, lo in places.items()}
+        block_norm_grad(dout, dz, ckpt_out, ckpt_block, stats, **slots, **call)
