@@ -3,8 +3,7 @@
 // wavefront.
 //
 // The checkpoint format: rows of 8-bit codes in blocks of 32 columns, one scale
-// byte b per block that stands for 2^(b - 127); b = 0 stands for 0 and b = 255
-// for NaN.  A scale that is a power of two makes every held value exactly
+// byte b per block that stands for 2^(b - 127), or for NaN if b = 255.  A scale that is a power of two makes every held value exactly
 // representable in the 16-bit type it came from (7 significant bits of an int8
 // code, 4 of an e4m3 code, against 11 of fp16 and 8 of bf16), so whatever reads
 // a checkpoint back rounds nothing a second time.
@@ -53,14 +52,13 @@ __device__ __forceinline__ float hi16(uint32_t w) {
 // One rounding to nearest even per value.
 template <typename T>
 __device__ __forceinline__ uint32_t pack16(float a, float b) {
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  const f2 v = {a, b};
   if constexpr (T::kType == kF16) {
-    const uint32_t x = __builtin_bit_cast(uint16_t, static_cast<_Float16>(a));
-    const uint32_t y = __builtin_bit_cast(uint16_t, static_cast<_Float16>(b));
-    return x | (y << 16);
+    typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, h2));
   } else {
     typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
-    typedef float f2 __attribute__((ext_vector_type(2)));
-    const f2 v = {a, b};
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf2));
   }
 }
@@ -128,9 +126,9 @@ __device__ __forceinline__ void store_codes(uint8_t* row, uint64_t c, uint64_t c
 
 // ------------------------------------------------------------ the 8-bit format
 
-// 2^(b - 127) of a scale byte: its exponent field; 0 -> 0, 255 -> NaN.
+// 2^(b - 127) of a scale byte: its exponent field (2^-127 is subnormal); 255: NaN.
 __device__ __forceinline__ float scale_of(uint32_t b) {
-  return __builtin_bit_cast(float, b == 255u ? 0x7FC00000u : b << 23);
+  return __builtin_bit_cast(float, b == 255u ? 0x7FC00000u : b == 0 ? 0x00400000u : b << 23);
 }
 
 template <int FMT>
@@ -155,6 +153,52 @@ __device__ __forceinline__ void decode8(u32x2 w, float s, float (&x)[8]) {
   decode4<FMT>(w[0], s, x);
   decode4<FMT>(w[1], s, x + 4);
 }
+
+// Codes straight to 16-bit values, each rounded to nearest even, two at a time, for
+// kernels that feed the matrix instructions: Scale16 is made once a block, then
+// pair<I> gives codes 2 I and 2 I + 1 of a chunk.
+template <typename T, int FMT>
+struct Scale16 {
+  float s, off;
+
+  __device__ __forceinline__ void set(uint32_t b) {
+    if constexpr (FMT == kE4m3) {
+      s = __builtin_bit_cast(float, b << 23);   // only its exponent field is read
+    } else if constexpr (T::kType == kF16) {
+      // 2^73 and more overflow alike, and 1152 * 2^73 is finite
+      s = scale_of(b == 255u || b < 200u ? b : 200u);
+      off = -1152.0f * s;
+    } else {
+      s = scale_of(b);
+    }
+  }
+
+  template <int I>
+  __device__ __forceinline__ uint32_t pair(u32x2 w) const {
+    if constexpr (FMT == kE4m3) {
+      if constexpr (T::kType == kF16)
+        return __builtin_bit_cast(
+            uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w[I / 2], s, I % 2 != 0));
+      else
+        return __builtin_bit_cast(
+            uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[I / 2], s, I % 2 != 0));
+    } else if constexpr (T::kType == kF16) {
+      // 0x6400 | u is the half 1024 + u, u = code + 128: one fused multiply-add in
+      // fp32 gives code * 2^e, rounded once to 16 bits
+      typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+      const h2 c = __builtin_bit_cast(
+          h2, __builtin_amdgcn_perm(0x64646464u, w[I / 2] ^ 0x80808080u,
+                                    I % 2 ? 0x04030402u : 0x04010400u));
+      const h2 v = {static_cast<_Float16>(__builtin_fmaf(static_cast<float>(c[0]), s, off)),
+                    static_cast<_Float16>(__builtin_fmaf(static_cast<float>(c[1]), s, off))};
+      return __builtin_bit_cast(uint32_t, v);
+    } else {
+      constexpr int kAt = I % 2 * 16;
+      return pack16<T>(static_cast<float>(static_cast<int8_t>(w[I / 2] >> kAt)) * s,
+                       static_cast<float>(static_cast<int8_t>(w[I / 2] >> (kAt + 8))) * s);
+    }
+  }
+};
 
 // The value of lane i ^ 1, i ^ 2 within each quad of lanes.
 template <int CTRL>

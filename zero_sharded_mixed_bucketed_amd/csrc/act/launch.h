@@ -96,6 +96,7 @@ struct WeightGradLaunch {
   void* dw;
   uint64_t dw_stride;
   int dw_dtype, accumulate;
+  int dw_wide;                  // rows of dw start on 16 bytes
   float* partial;               // weight_grad_workspace bytes
 };
 

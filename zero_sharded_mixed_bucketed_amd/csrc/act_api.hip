@@ -228,6 +228,7 @@ int zero_ckpt_weight_grad(const zero_ckpt_t* x, const void* dy, int dtype, uint6
   L.dw_stride = dw_stride;
   L.dw_dtype = dw_dtype;
   L.accumulate = accumulate;
+  L.dw_wide = aligned(dw, 16) && (dw_stride % (dw_dtype == ZERO_F32 ? 4 : 8) == 0 || n <= 1);
   L.partial = static_cast<float*>(workspace);
   return device(zero::act::launch_weight_grad(L, static_cast<hipStream_t>(hip_stream)),
                 "weight gradient");

@@ -3,7 +3,11 @@
 // the checkpoint holds.
 //
 // Every held value is exact in 16 bits, so the products run on the 16-bit matrix
-// instructions with the dequantised values themselves, and sums are fp32.  The
+// instructions with the dequantised values themselves, and sums are fp32.  Bound by
+// the matrix unit and, on random data, by the power it may draw: 8192 tokens,
+// 4096 -> 16384 takes 0.88-1.0 ms in bf16 and 0.90-1.12 ms in fp16 (e4m3 - int8
+// codes), 0.98-1.25 PFLOP/s, where a library's plain 16-bit product of the same
+// values, dequantised beforehand, takes 0.90-1.0 ms.  The
 // long axis t is the slow one of both operands; the matrix instructions want it
 // in each lane's registers, so tiles lie in shared memory as they come (t by
 // columns, 16 bits) and are read with the transposing shared-memory loads.
@@ -23,9 +27,8 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kThreads = 256;   // four waves, two by two
-constexpr int kTileN = 128, kTileK = 128, kTileT = 32;
 constexpr int kFrag = 32;       // rows and columns of a matrix instruction
-constexpr int kFn = kTileN / 2 / kFrag, kFk = kTileK / 2 / kFrag;
+constexpr int kDepth = 16;      // tokens of a matrix instruction
 
 // Offset of (t, col) in a shared tile of COLS 16-bit columns: rows of 64-byte
 // granules whose order is permuted by t, so that the four rows a transposing
@@ -41,17 +44,15 @@ __device__ __forceinline__ s16x4 read_tr(const uint16_t* p) {
       (lds_s16x4*)(__attribute__((address_space(3))) uint16_t*)p);
 }
 
-// A 32 x 16 operand: lane l gets column col + l % 32 of rows t .. t + 7 or
-// t + 8 .. t + 15 (upper lanes).
+// Half of a 32 x 16 operand: lane l gets column col + l % 32 of four tokens, from
+// t + 8 (l / 32) + 4 half on.
 template <int COLS>
-__device__ __forceinline__ u32x4 fragment(const uint16_t* tile, uint32_t t, uint32_t col) {
+__device__ __forceinline__ u32x2 half_fragment(const uint16_t* tile, uint32_t t, uint32_t col,
+                                               int half) {
   const uint32_t lane = threadIdx.x % 64;
-  const uint32_t r = t + (lane / 32) * 8 + (lane % 16) / 4;
+  const uint32_t r = t + (lane / 32) * 8 + (lane % 16) / 4 + half * 4;
   const uint32_t c = col + (lane / 16 % 2) * 16 + lane % 4 * 4;
-  const s16x4 a = read_tr(tile + place<COLS>(r, c));
-  const s16x4 b = read_tr(tile + place<COLS>(r + 4, c));
-  const u32x2 x = __builtin_bit_cast(u32x2, a), y = __builtin_bit_cast(u32x2, b);
-  return u32x4{x[0], x[1], y[0], y[1]};
+  return __builtin_bit_cast(u32x2, read_tr(tile + place<COLS>(r, c)));
 }
 
 template <typename T>
@@ -64,134 +65,438 @@ __device__ __forceinline__ f32x16 mfma(u32x4 a, u32x4 b, f32x16 c) {
                                                    __builtin_bit_cast(bhalf8, b), c, 0, 0, 0);
 }
 
-__device__ __forceinline__ void put(void* dw, uint64_t at, int dtype, int accumulate, float s) {
-  if (dtype == kF32) {
-    float* o = static_cast<float*>(dw) + at;
-    *o = accumulate ? *o + s : s;
+// Orders one wave's shared-memory accesses before and after this point.
+__device__ __forceinline__ void wave_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// Where sums go: dW, or a split's fp32 partial sums.
+struct Dest {
+  void* p;
+  uint64_t stride;
+  int dtype, accumulate, wide;
+};
+
+__device__ __forceinline__ Dest destination(const WeightGradLaunch& a, uint32_t split,
+                                            uint64_t per_split) {
+  if (per_split < a.rows)
+    return {a.partial + split * a.n * a.k, a.k, kF32, 0, a.k % 4 == 0};
+  return {a.dw, a.dw_stride, a.dw_dtype, a.accumulate, a.dw_wide};
+}
+
+__device__ __forceinline__ void put(const Dest& d, uint64_t at, float s) {
+  if (d.dtype == kF32) {
+    float* o = static_cast<float*>(d.p) + at;
+    *o = d.accumulate ? *o + s : s;
   } else {
-    uint16_t* o = static_cast<uint16_t*>(dw) + at;
-    if (dtype == kF16)
-      *o = static_cast<uint16_t>(pack16<F16>(accumulate ? lo16<F16>(*o) + s : s, 0.f));
+    uint16_t* o = static_cast<uint16_t*>(d.p) + at;
+    if (d.dtype == kF16)
+      *o = static_cast<uint16_t>(pack16<F16>(d.accumulate ? lo16<F16>(*o) + s : s, 0.f));
     else
-      *o = static_cast<uint16_t>(pack16<Bf16>(accumulate ? lo16<Bf16>(*o) + s : s, 0.f));
+      *o = static_cast<uint16_t>(pack16<Bf16>(d.accumulate ? lo16<Bf16>(*o) + s : s, 0.f));
   }
 }
 
-template <typename T, int FMT>
+template <typename T>
+__device__ __forceinline__ void put8_16(uint16_t* o, int accumulate, float (&x)[8]) {
+  u32x4* w = reinterpret_cast<u32x4*>(o);
+  if (accumulate) {
+    float old[8];
+    unpack8<T>(*w, old);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] += old[i];
+  }
+  *w = pack8<T>(x);
+}
+
+// Eight neighbouring sums of row n from column k on.
+__device__ __forceinline__ void put8(const Dest& d, uint64_t n, uint64_t k, uint64_t cols, f32x4 u,
+                                     f32x4 v) {
+  const uint64_t at = n * d.stride + k;
+  float x[8] = {u[0], u[1], u[2], u[3], v[0], v[1], v[2], v[3]};
+  if (d.wide && k + kChunk <= cols) {
+    if (d.dtype == kF32) {
+      f32x4* o = reinterpret_cast<f32x4*>(static_cast<float*>(d.p) + at);
+      if (d.accumulate) {
+        u += o[0];
+        v += o[1];
+      }
+      o[0] = u;
+      o[1] = v;
+    } else if (d.dtype == kF16) {
+      put8_16<F16>(static_cast<uint16_t*>(d.p) + at, d.accumulate, x);
+    } else {
+      put8_16<Bf16>(static_cast<uint16_t*>(d.p) + at, d.accumulate, x);
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (k + i < cols) put(d, at + i, x[i]);
+}
+
+// The split and tile of a workgroup.  Workgroups go to the eight dies in turn, each
+// with an L2 of its own: die x takes the x-th eighth of the pieces, and pieces run
+// down groups of eight tile rows, so that the 32 that a die has in hand together
+// read 8 + 4 column strips of the operands.
+struct Piece {
+  uint32_t split, n, k;
+};
+
+constexpr uint32_t kDies = 8, kGroupRows = 8;
+
+__device__ __forceinline__ Piece piece_of(uint32_t wg, uint32_t wgs, uint32_t tk,
+                                          uint32_t tiles) {
+  const uint32_t die = wg % kDies, each = wgs / kDies, more = wgs % kDies;
+  const uint32_t id = die * each + (die < more ? die : more) + wg / kDies;
+  const uint32_t split = id / tiles, tile = id % tiles;
+  const uint32_t tn = tiles / tk, group = tile / (kGroupRows * tk);
+  const uint32_t rest = tile % (kGroupRows * tk), row0 = group * kGroupRows;
+  const uint32_t rows = tn - row0 < kGroupRows ? tn - row0 : kGroupRows;
+  return {split, row0 + rest % rows, rest / rows};
+}
+
+// A workgroup's TILE x TILE piece of dW over one split of the tokens, DEPTH tokens
+// at a time through two buffers of shared memory.  While the matrix unit works on
+// one tile, the next one goes from registers to the other buffer, dequantised, and
+// the one after it is loaded into those registers; the operands of a matrix step
+// are read during the step before it.
+//
+// WIDE: rows of dY start on 16 bytes and rows of codes on 8.  Whole tiles are then
+// loaded without a branch: columns past the matrix read padding between rows, or
+// other columns, and reach only sums that are not stored.  The tile that holds
+// the split's last tokens is loaded with every check.
+template <typename T, int FMT, int TILE, int DEPTH, bool WIDE>
 __global__ __launch_bounds__(kThreads) void weight_grad_kernel(WeightGradLaunch a, int dy_wide,
-                                                               uint64_t per_split) {
-  __shared__ uint16_t ly[2][kTileT * kTileN];
-  __shared__ uint16_t lx[2][kTileT * kTileK];
-  const uint64_t n0 = static_cast<uint64_t>(blockIdx.y) * kTileN;
-  const uint64_t k0 = static_cast<uint64_t>(blockIdx.x) * kTileK;
-  const uint64_t t_lo = blockIdx.z * per_split;
+                                                               uint64_t per_split, uint32_t tk,
+                                                               uint32_t tiles) {
+  constexpr int kF = TILE / 2 / kFrag;                    // fragments of a wave, each way
+  constexpr uint32_t kRowLanes = TILE / kChunk;           // lanes of a tile row
+  constexpr uint32_t kStep = kThreads / kRowLanes;        // rows a pass of the workgroup
+  constexpr int kPass = DEPTH / kStep;                    // passes a tile
+  constexpr int kSub = DEPTH / kDepth;                    // matrix steps a tile
+  // two tiles of each operand; at the end, 32 rows of each wave's sums
+  constexpr uint32_t kCols = TILE / 2, kPitch = kCols + 8;
+  constexpr uint32_t kTiles = 2 * DEPTH * TILE, kOut = 4 * kFrag * kPitch;
+  __shared__ float lds[kTiles > kOut ? kTiles : kOut];
+  uint16_t (*ly)[DEPTH * TILE] = reinterpret_cast<uint16_t (*)[DEPTH * TILE]>(lds);
+  uint16_t (*lx)[DEPTH * TILE] = ly + 2;
+  const Piece piece_at = piece_of(blockIdx.x, gridDim.x, tk, tiles);
+  const uint32_t split = piece_at.split;
+  const uint64_t n0 = static_cast<uint64_t>(piece_at.n) * TILE;
+  const uint64_t k0 = static_cast<uint64_t>(piece_at.k) * TILE;
+  const uint64_t t_lo = split * per_split;
   const uint64_t t_hi = t_lo + per_split < a.rows ? t_lo + per_split : a.rows;
   const uint32_t tid = threadIdx.x, wave = tid / 64;
-  const uint32_t wn = wave / 2 * (kTileN / 2), wk = wave % 2 * (kTileK / 2);
+  const uint32_t wn = wave / 2 * (TILE / 2), wk = wave % 2 * (TILE / 2);
 
-  u32x4 ry[2];
-  u32x2 rx[2];
-  uint32_t rs[2];
-  constexpr uint32_t kRowLanes = kTileN / kChunk;   // lanes of a tile row
-  constexpr uint32_t kStep = kThreads / kRowLanes;  // rows a pass
+  u32x4 ry[kPass];
+  u32x2 rx[kPass];
+  uint32_t rs[kPass];
   const uint32_t st = tid / kRowLanes, sc = tid % kRowLanes * kChunk;
-  auto load = [&](uint64_t t0) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
+  const bool in_n = n0 + sc < a.n, in_k = k0 + sc < a.k;
+  // with every check: t < t_hi, columns inside, any alignment
+  auto load_any = [&](uint64_t t0) {
+#pragma unroll 1
+    for (int i = 0; i < kPass; ++i) {
       const uint64_t t = t0 + i * kStep + st;
-      ry[i] = u32x4{0, 0, 0, 0};
-      rx[i] = u32x2{0, 0};
-      rs[i] = 0;
-      if (t >= t_hi) continue;
-      if (n0 + sc < a.n) ry[i] = load8(a.dy + t * a.dy_stride, n0 + sc, a.n, dy_wide);
-      if (k0 + sc < a.k) {
-        rx[i] = load_codes(a.x.codes + t * a.x.code_stride, k0 + sc, a.k, a.x.wide);
-        rs[i] = a.x.scales[t * a.x.scale_stride + (k0 + sc) / kBlock];
+      u32x4 y = {0, 0, 0, 0};
+      u32x2 x = {0, 0};
+      uint32_t b = 0;
+      if (t < t_hi) {
+        if (in_n) y = load8(a.dy + t * a.dy_stride, n0 + sc, a.n, dy_wide);
+        if (in_k) {
+          x = load_codes(a.x.codes + t * a.x.code_stride, k0 + sc, a.k, a.x.wide);
+          b = a.x.scales[t * a.x.scale_stride + (k0 + sc) / kBlock];
+        }
       }
+#pragma unroll
+      for (int q = 0; q < kPass; ++q)                     // registers take fixed indexes
+        if (q == i) {
+          ry[q] = y;
+          rx[q] = x;
+          rs[q] = b;
+        }
     }
   };
-  f32x16 acc[kFn][kFk];
+  // the lane's columns, or column 0 where the tile passes the matrix's edge
+  const uint16_t* py = a.dy + (in_n ? n0 + sc : 0);
+  const uint8_t* px = a.x.codes + (in_k ? k0 + sc : 0);
+  const uint8_t* ps = a.x.scales + (in_k ? (k0 + sc) / kBlock : 0);
+  auto load_one = [&](uint64_t t0, int i) {               // tokens below `whole`
+    const uint64_t t = t0 + i * kStep + st;
+    ry[i] = *reinterpret_cast<const u32x4*>(py + t * a.dy_stride);
+    rx[i] = *reinterpret_cast<const u32x2*>(px + t * a.x.code_stride);
+    rs[i] = ps[t * a.x.scale_stride];
+  };
+  // A pass from registers to shared memory in kParts parts, the loads that refill
+  // its registers last.
+  constexpr int kParts = 6;
+  Scale16<T, FMT> scale;
+  u32x4 held;
+  auto stage = [&](int buf, int i, int part) {
+    const uint32_t t = i * kStep + st;
+    switch (part) {
+      case 0:
+        // keeps the compiler from taking the codes apart where they are loaded,
+        // which would wait for the load there
+        asm("" : "+v"(rx[i][0]), "+v"(rx[i][1]), "+v"(rs[i]));
+        scale.set(rs[i]);
+        break;
+      case 1: held[0] = scale.template pair<0>(rx[i]); break;
+      case 2: held[1] = scale.template pair<1>(rx[i]); break;
+      case 3: held[2] = scale.template pair<2>(rx[i]); break;
+      case 4: held[3] = scale.template pair<3>(rx[i]); break;
+      default:
+        *reinterpret_cast<u32x4*>(&ly[buf][place<TILE>(t, sc)]) = ry[i];
+        *reinterpret_cast<u32x4*>(&lx[buf][place<TILE>(t, sc)]) = held;
+    }
+  };
+  // Tokens that wide loads may take: chunks that pass the last column must not
+  // reach past the matrix's last row.
+  uint64_t whole = t_hi;
+  if (t_hi == a.rows && (a.n % kChunk || a.k % kChunk) && t_hi > t_lo) whole = t_hi - 1;
+  auto load = [&](uint64_t t0) {
+    if (WIDE && t0 + DEPTH <= whole) {
 #pragma unroll
-  for (int i = 0; i < kFn; ++i)
+      for (int i = 0; i < kPass; ++i) load_one(t0, i);
+    } else {
+      load_any(t0);
+    }
+  };
+
+  f32x16 acc[kF][kF];
 #pragma unroll
-    for (int j = 0; j < kFk; ++j)
+  for (int i = 0; i < kF; ++i)
+#pragma unroll
+    for (int j = 0; j < kF; ++j)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
 
-  load(t_lo);
-  int buf = 0;
-  for (uint64_t t0 = t_lo; t0 < t_hi; t0 += kTileT, buf ^= 1) {
+  // Operands of a step: 4 kF transposing loads, in the order of their use.
+  u32x4 fy[2][kF], fx[2][kF];
+  auto read = [&](int buf, int s, int to, int q) {
+    const int f = q / 2, half = q % 2;
+    // fragments in order: y0, x0 .. x(kF-1), y1 .. y(kF-1)
+    const bool of_x = f >= 1 && f <= kF;
+    const int i = of_x ? f - 1 : f == 0 ? 0 : f - kF;
+    const uint16_t* tile_at = of_x ? lx[buf] : ly[buf];
+    const u32x2 v = half_fragment<TILE>(tile_at, s * kDepth, (of_x ? wk : wn) + i * kFrag, half);
+    u32x4& reg = of_x ? fx[to][i] : fy[to][i];
+    reg[2 * half] = v[0];
+    reg[2 * half + 1] = v[1];
+  };
+  auto read_all = [&](int buf, int s, int to) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t t = i * kStep + st;
-      *reinterpret_cast<u32x4*>(&ly[buf][place<kTileN>(t, sc)]) = ry[i];
-      float x[8];
-      decode8<FMT>(rx[i], scale_of(rs[i]), x);
-      *reinterpret_cast<u32x4*>(&lx[buf][place<kTileK>(t, sc)]) = pack8<T>(x);
-    }
-    // the other buffer was last read before the barrier of the turn before
-    __syncthreads();
-    if (t0 + kTileT < t_hi) load(t0 + kTileT);
-#pragma unroll
-    for (int s = 0; s < kTileT; s += 16) {
-      u32x4 fy[kFn], fx[kFk];
-#pragma unroll
-      for (int i = 0; i < kFn; ++i) fy[i] = fragment<kTileN>(ly[buf], s, wn + i * kFrag);
-#pragma unroll
-      for (int j = 0; j < kFk; ++j) fx[j] = fragment<kTileK>(lx[buf], s, wk + j * kFrag);
-#pragma unroll
-      for (int i = 0; i < kFn; ++i)
-#pragma unroll
-        for (int j = 0; j < kFk; ++j) acc[i][j] = mfma<T>(fy[i], fx[j], acc[i][j]);
-    }
-  }
+    for (int q = 0; q < 4 * kF; ++q) read(buf, s, to, q);
+  };
 
-  const uint32_t lane = tid % 64;
-  float* part = gridDim.z > 1 ? a.partial + blockIdx.z * a.n * a.k : nullptr;
+  load(t_lo);
 #pragma unroll
-  for (int i = 0; i < kFn; ++i)
+  for (int i = 0; i < kPass; ++i)
 #pragma unroll
-    for (int j = 0; j < kFk; ++j)
+    for (int q = 0; q < kParts; ++q) stage(0, i, q);
+  load(t_lo + DEPTH);
+  __syncthreads();
+  read_all(0, 0, 0);
+  uint32_t buf = 0;
+  uint64_t t0 = t_lo;
+  static_assert(kSub % 2 == 0, "the operands' registers take turns");
+  // A turn: all of tile t0's steps; tile t0 + DEPTH from registers to the other
+  // buffer (last read before the barrier of the turn before) over all steps but the
+  // last; then the barrier, behind which the next tile's first operands are read
+  // while the last step runs.  Between two matrix instructions goes about as much
+  // other work as one of them takes, and the compiler keeps it there: left to
+  // itself it gathers the arithmetic in long runs, beside which the matrix unit
+  // stands idle.
+  constexpr int kMul = kF * kF;                            // matrix instructions a step
+  constexpr int kSlots = (kSub - 1) * kMul;
+  constexpr int kPerSlot = (kPass * kParts + kSlots - 1) / kSlots;
+  auto turn = [&](auto refill) {
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const uint64_t n = n0 + wn + i * kFrag + r / 4 * 8 + lane / 32 * 4 + r % 4;
-        const uint64_t k = k0 + wk + j * kFrag + lane % 32;
-        if (n >= a.n || k >= a.k) continue;
-        if (part) part[n * a.k + k] = acc[i][j][r];
-        else put(a.dw, n * a.dw_stride + k, a.dw_dtype, a.accumulate, acc[i][j][r]);
+    for (int s = 0; s < kSub; ++s) {
+      const bool last = s + 1 == kSub;
+      if (last) __syncthreads();
+#pragma unroll
+      for (int m = 0; m < kMul; ++m) {
+        const int i = m / kF, j = m % kF;
+        acc[i][j] = mfma<T>(fy[s & 1][i], fx[s & 1][j], acc[i][j]);
+#pragma unroll
+        for (int q = m * 4 / kF; q < (m + 1) * 4 / kF; ++q)
+          read(last ? buf ^ 1 : buf, last ? 0 : s + 1, (s + 1) & 1, q);
+        if (!last) {
+#pragma unroll
+          for (int q = 0; q < kPerSlot; ++q) {
+            const int w = (s * kMul + m) * kPerSlot + q;
+            if (w >= kPass * kParts) continue;
+            stage(buf ^ 1, w / kParts, w % kParts);
+            if (w % kParts == kParts - 1) refill(w / kParts);
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
       }
+    }
+    buf ^= 1;
+  };
+  if constexpr (WIDE) {
+    for (; t0 + 3 * DEPTH <= whole; t0 += DEPTH)
+      turn([&](int i) { load_one(t0 + 2 * DEPTH, i); });
+  }
+#pragma unroll 1
+  for (; t0 < t_hi; t0 += DEPTH) {
+    turn([](int) {});
+    load_any(t0 + 2 * DEPTH);   // zeros past the end
+  }
+  __syncthreads();
+
+  // Through shared memory, so that a lane stores eight neighbouring columns: each
+  // wave turns 32 rows at a time in a piece of its own, whose rows lie kPitch
+  // words apart (4 kPitch = 32 mod 64: the two halves of a wave, four rows apart,
+  // meet different banks).
+  const uint32_t lane = tid % 64;
+  static_assert((4 * kPitch) % 64 == 32, "");
+  float* piece = lds + wave * kFrag * kPitch;
+  const Dest out = destination(a, split, per_split);
+  // a whole tile that is only stored, in 16-byte pieces
+  const bool inside = out.wide && !out.accumulate && n0 + TILE <= a.n && k0 + TILE <= a.k;
+#pragma unroll
+  for (int i = 0; i < kF; ++i) {
+#pragma unroll
+    for (int j = 0; j < kF; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        piece[(r / 4 * 8 + lane / 32 * 4 + r % 4) * kPitch + j * kFrag + lane % 32] =
+            acc[i][j][r];
+    wave_order();
+    constexpr uint32_t kLanes = kCols / kChunk;           // lanes of a row
+    constexpr int kRows = kFrag * kLanes / 64;            // passes over the 32 rows
+    const uint32_t q = lane / kLanes, c = lane % kLanes * kChunk;
+    const uint64_t n = n0 + wn + i * kFrag + q, k = k0 + wk + c;
+    const float* p = piece + q * kPitch + c;
+    f32x4 u[kRows], v[kRows];
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      u[r] = *reinterpret_cast<const f32x4*>(p + r * (64 / kLanes) * kPitch);
+      v[r] = *reinterpret_cast<const f32x4*>(p + r * (64 / kLanes) * kPitch + 4);
+    }
+    if (inside && out.dtype == T::kType) {
+      uint16_t* o = static_cast<uint16_t*>(out.p) + n * out.stride + k;
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
+        const float x[8] = {u[r][0], u[r][1], u[r][2], u[r][3], v[r][0], v[r][1], v[r][2], v[r][3]};
+        *reinterpret_cast<u32x4*>(o + r * (64 / kLanes) * out.stride) = pack8<T>(x);
+      }
+    } else if (inside) {
+      float* o = static_cast<float*>(out.p) + n * out.stride + k;
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
+        *reinterpret_cast<f32x4*>(o + r * (64 / kLanes) * out.stride) = u[r];
+        *reinterpret_cast<f32x4*>(o + r * (64 / kLanes) * out.stride + 4) = v[r];
+      }
+    } else {
+#pragma unroll 1
+      for (int r = 0; r < kRows; ++r) {
+        const float* pr = p + r * (64 / kLanes) * kPitch;
+        const uint64_t row = n + r * (64 / kLanes);
+        if (row < a.n && k < a.k)
+          put8(out, row, k, a.k, *reinterpret_cast<const f32x4*>(pr),
+               *reinterpret_cast<const f32x4*>(pr + 4));
+      }
+    }
+    wave_order();
+  }
 }
 
-// Adds the splits' partial sums in their order.
+// Adds the splits' partial sums in their order, eight neighbouring columns a thread.
 __global__ __launch_bounds__(kThreads) void weight_grad_join_kernel(WeightGradLaunch a,
                                                                     uint32_t splits) {
-  const uint64_t count = a.n * a.k;
-  for (uint64_t i = static_cast<uint64_t>(blockIdx.x) * kThreads + threadIdx.x; i < count;
-       i += static_cast<uint64_t>(gridDim.x) * kThreads) {
-    float s = 0.f;
-    for (uint32_t p = 0; p < splits; ++p) s += a.partial[p * count + i];
-    put(a.dw, i / a.k * a.dw_stride + i % a.k, a.dw_dtype, a.accumulate, s);
+  const uint64_t per_row = (a.k + kChunk - 1) / kChunk, count = a.n * a.k;
+  const uint64_t id = static_cast<uint64_t>(blockIdx.x) * kThreads + threadIdx.x;
+  const uint64_t n = id / per_row, k = id % per_row * kChunk;
+  if (n >= a.n) return;
+  const bool wide = a.k % 4 == 0 && k + kChunk <= a.k;
+  f32x4 u = {0.f, 0.f, 0.f, 0.f}, v = u;
+  const float* p = a.partial + n * a.k + k;
+#pragma unroll 8
+  for (uint32_t s = 0; s < splits; ++s, p += count) {
+    if (wide) {
+      u += *reinterpret_cast<const f32x4*>(p);
+      v += *reinterpret_cast<const f32x4*>(p + 4);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (k + i < a.k) u[i] += p[i];
+        if (k + 4 + i < a.k) v[i] += p[4 + i];
+      }
+    }
   }
+  put8({a.dw, a.dw_stride, a.dw_dtype, a.accumulate, a.dw_wide}, n, k, a.k, u, v);
 }
 
 struct Plan {
+  int tile;
   uint64_t tn, tk, splits, per_split;
 };
 
+// Estimated microseconds of a choice, from measurements on MI355X: a workgroup of
+// 256 x 256 has a compute unit to itself and takes 14 us and 0.028 a token; one of
+// 128 x 128 takes 7 us and 0.015 a token alone on its unit, 0.021 beside a second
+// one; a join costs a launch, and its partial sums' way out and back.
+double estimate(int tile, uint64_t wgs, uint64_t splits, uint64_t per_split, uint64_t outs) {
+  constexpr uint64_t kUnits = 256;
+  const uint64_t at_once = tile == 256 ? kUnits : 2 * kUnits;
+  const double rounds = static_cast<double>((wgs + at_once - 1) / at_once);
+  const double token = tile == 256 ? 0.028 : wgs > kUnits ? 0.021 : 0.015;
+  const double run = rounds * ((tile == 256 ? 14.0 : 7.0) + token * static_cast<double>(per_split));
+  return splits == 1 ? run
+                     : run + 3.0 + static_cast<double>(splits) * static_cast<double>(outs) * 8 / 6e6;
+}
+
+// The tile and the number of splits with the least estimate.  Small tiles fill the
+// chip with less output, splits with more tokens: at 16001 x 1032 -> 776 the best
+// choice takes 53 us where one split of 256 x 256 tiles takes 480.
 Plan plan(uint64_t rows, uint64_t k, uint64_t n) {
-  Plan p;
-  p.tn = (n + kTileN - 1) / kTileN;
-  p.tk = (k + kTileK - 1) / kTileK;
-  const uint64_t tiles = p.tn * p.tk;
-  uint64_t s = tiles < 512 ? 512 / tiles : 1;
-  const uint64_t most = rows / 256;  // a split sums 256 tokens at least
-  if (s > most) s = most;
-  if (s < 1) s = 1;
-  p.per_split = ((rows + s - 1) / s + kTileT - 1) / kTileT * kTileT;
-  if (p.per_split == 0) p.per_split = kTileT;
-  p.splits = (rows + p.per_split - 1) / p.per_split;
-  if (p.splits == 0) p.splits = 1;
-  return p;
+  Plan best;
+  double least = 0;
+  bool first = true;
+  for (int tile = 128; tile <= 256; tile *= 2) {
+    Plan p;
+    p.tile = tile;
+    p.tn = (n + tile - 1) / tile;
+    p.tk = (k + tile - 1) / tile;
+    const uint64_t most = rows / 256 < 64 ? (rows < 512 ? 1 : rows / 256) : 64;
+    for (uint64_t s = 1; s <= most; ++s) {
+      p.per_split = rows ? ((rows + s - 1) / s + 63) / 64 * 64 : 64;
+      p.splits = rows ? (rows + p.per_split - 1) / p.per_split : 1;
+      const double us = estimate(tile, p.tn * p.tk * p.splits, p.splits, p.per_split, n * k);
+      if (first || us < least) {
+        least = us;
+        best = p;
+        first = false;
+      }
+    }
+  }
+  return best;
+}
+
+template <typename T, int FMT, int TILE, int DEPTH>
+void run_tile(const WeightGradLaunch& a, const Plan& p, uint32_t wgs, int dy_wide,
+              hipStream_t stream) {
+  const uint32_t tk = static_cast<uint32_t>(p.tk), tiles = static_cast<uint32_t>(p.tn * p.tk);
+  if (dy_wide && a.x.wide)
+    weight_grad_kernel<T, FMT, TILE, DEPTH, true>
+        <<<wgs, kThreads, 0, stream>>>(a, dy_wide, p.per_split, tk, tiles);
+  else
+    weight_grad_kernel<T, FMT, TILE, DEPTH, false>
+        <<<wgs, kThreads, 0, stream>>>(a, dy_wide, p.per_split, tk, tiles);
+}
+
+template <typename T, int FMT>
+void run(const WeightGradLaunch& a, const Plan& p, uint32_t wgs, int dy_wide,
+         hipStream_t stream) {
+  if (p.tile == 256) run_tile<T, FMT, 256, 64>(a, p, wgs, dy_wide, stream);
+  else run_tile<T, FMT, 128, 32>(a, p, wgs, dy_wide, stream);
 }
 
 }  // namespace
@@ -203,25 +508,21 @@ uint64_t weight_grad_workspace(uint64_t rows, uint64_t k, uint64_t n) {
 
 hipError_t launch_weight_grad(const WeightGradLaunch& a, hipStream_t stream) {
   const Plan p = plan(a.rows, a.k, a.n);
-  if (p.tk > 0x7FFFFFFFull || p.tn > 65535) return hipErrorInvalidConfiguration;
-  const int dy_wide = reinterpret_cast<uintptr_t>(a.dy) % 16 == 0 && a.dy_stride % 8 == 0;
-  const dim3 grid(static_cast<uint32_t>(p.tk), static_cast<uint32_t>(p.tn),
-                  static_cast<uint32_t>(p.splits));
+  const uint64_t wgs = p.tn * p.tk * p.splits;   // at most 2^30 tiles of 128 x 128
+  if (wgs > 0x7FFFFFFFull) return hipErrorInvalidConfiguration;
+  const int dy_wide = reinterpret_cast<uintptr_t>(a.dy) % 16 == 0 &&
+                      (a.dy_stride % 8 == 0 || a.rows <= 1);
   if (a.dtype == kF16) {
-    if (a.x.format == kInt8)
-      weight_grad_kernel<F16, kInt8><<<grid, kThreads, 0, stream>>>(a, dy_wide, p.per_split);
-    else
-      weight_grad_kernel<F16, kE4m3><<<grid, kThreads, 0, stream>>>(a, dy_wide, p.per_split);
+    if (a.x.format == kInt8) run<F16, kInt8>(a, p, wgs, dy_wide, stream);
+    else run<F16, kE4m3>(a, p, wgs, dy_wide, stream);
   } else {
-    if (a.x.format == kInt8)
-      weight_grad_kernel<Bf16, kInt8><<<grid, kThreads, 0, stream>>>(a, dy_wide, p.per_split);
-    else
-      weight_grad_kernel<Bf16, kE4m3><<<grid, kThreads, 0, stream>>>(a, dy_wide, p.per_split);
+    if (a.x.format == kInt8) run<Bf16, kInt8>(a, p, wgs, dy_wide, stream);
+    else run<Bf16, kE4m3>(a, p, wgs, dy_wide, stream);
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
-  const uint64_t wgs = (a.n * a.k + kThreads - 1) / kThreads;
-  weight_grad_join_kernel<<<static_cast<uint32_t>(wgs < 4096 ? wgs : 4096), kThreads, 0, stream>>>(
+  const uint64_t joins = (a.n * ((a.k + kChunk - 1) / kChunk) + kThreads - 1) / kThreads;
+  weight_grad_join_kernel<<<static_cast<uint32_t>(joins), kThreads, 0, stream>>>(
       a, static_cast<uint32_t>(p.splits));
   return hipGetLastError();
 }
