@@ -326,7 +326,7 @@ int zero_launch_occupancy(int kernel, int *wgs_per_cu, uint32_t *lds_bytes);
  * An 8-bit checkpoint of a rows x cols matrix in device memory: the code of
  * (r, c) is codes[r * code_stride + c], and its value is
  *   value(code) * 2^(b - 127),  b = scales[r * scale_stride + c / 32];
- * b = 0 stands for 0 and b = 255 for NaN.  int8 codes are two's complement
+ * b = 255 stands for NaN.  int8 codes are two's complement
  * (-127..127), e4m3 codes are 8-bit floats with 4 exponent and 3 mantissa bits,
  * bias 7, no infinities.  Padding columns between rows are never touched.
  */

@@ -2,7 +2,7 @@
 around a block, in 64 bits.
 
 The checkpoint format, per row and block of 32 columns (a scale byte b stands
-for 2^(b - 127), 0 for 0 and 255 for NaN):
+for 2^(b - 127), 255 for NaN):
 
 * int8: the scale is 2^(floor(log2 amax) - 6), codes are whole numbers nearest
   to x / scale (ties to even) and within +-127;
@@ -90,7 +90,7 @@ def held(codes: np.ndarray, scales: np.ndarray, fmt: str) -> np.ndarray:
     t, h = codes.shape
     v = codes.view(np.int8).astype(np.float64) if fmt == "int8" else _E4M3_ALL[codes]
     b = scales.astype(np.int64)
-    s = np.where(b == 255, np.nan, np.where(b == 0, 0.0, np.ldexp(1.0, b - 127)))
+    s = np.where(b == 255, np.nan, np.ldexp(1.0, b - 127))
     return v * np.repeat(s, BLOCK, axis=1)[:, :h]
 
 

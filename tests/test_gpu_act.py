@@ -188,6 +188,21 @@ def test_weight_grad(t, k, n, pad, wpad, fmt, dtype, out, accumulate):
     assert torch.equal(buf, before)
 
 
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_weight_grad_reads_every_code_and_scale(fmt, dtype):
+    """One token with a unit gradient: dw is the held row, rounded to dy's type."""
+    codes = torch.arange(256, dtype=torch.uint8, device="cuda").view(1, 256)
+    one = torch.ones((1, 1), dtype=TORCH[dtype], device="cuda")
+    dw = torch.empty((1, 256), dtype=torch.float32, device="cuda")
+    for b in range(256):
+        scales = torch.full((1, 8), b, dtype=torch.uint8, device="cuda")
+        Z.ckpt_weight_grad(Z.Ckpt(codes, scales, FMT[fmt]), one, dw)
+        held = oact.held(codes.cpu().numpy(), scales.cpu().numpy(), fmt)
+        want = torch.from_numpy(held).float().to(TORCH[dtype]).double().numpy()
+        assert np.array_equal(f64(dw), want, equal_nan=True), b
+
+
 def test_weight_grad_without_tokens():
     x = Z.ckpt_empty(0, 70, Z.CKPT_INT8)
     dy = torch.empty((0, 33), dtype=torch.float16, device="cuda")

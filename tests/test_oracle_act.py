@@ -91,7 +91,8 @@ def test_store_special_blocks():
         assert h[2, 0] == (127 * 512.0 if fmt == "int8" else 61440.0)
         assert (h[3] == 0).all()
     assert np.isnan(act.held(np.ones((1, 3), np.uint8), np.array([[255]], np.uint8), "int8")).all()
-    assert (act.held(np.ones((1, 3), np.uint8), np.array([[0]], np.uint8), "int8") == 0).all()
+    assert (act.held(np.ones((1, 3), np.uint8), np.zeros((1, 1), np.uint8), "int8")
+            == 2.0 ** -127).all()
 
 
 def test_weight_grad_is_the_sum_over_tokens():

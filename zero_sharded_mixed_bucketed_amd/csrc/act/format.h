@@ -28,6 +28,13 @@ typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
+// The same where memory is aligned to its elements only: rows may start anywhere
+// (an odd row length does that to every other row), and the chip loads and stores
+// 16 bytes from any address.
+typedef u32x4 u32x4_at2 __attribute__((aligned(2)));
+typedef u32x2 u32x2_at1 __attribute__((aligned(1)));
+typedef f32x4 f32x4_at4 __attribute__((aligned(4)));
+
 struct F16 { static constexpr int kType = kF16; };
 struct Bf16 { static constexpr int kType = kBf16; };
 
@@ -80,21 +87,22 @@ __device__ __forceinline__ u32x4 pack8(const float (&x)[8]) {
   return w;
 }
 
-// Eight 16-bit elements of a row from column c on; columns from `cols` on read
-// as 0 and are not touched.  `wide`: the row starts on 16 bytes.
-__device__ __forceinline__ u32x4 load8(const uint16_t* row, uint64_t c, uint64_t cols, bool wide) {
-  if (wide && c + kChunk <= cols) return *reinterpret_cast<const u32x4*>(row + c);
+// Eight 16-bit elements of a row from column c < cols on; those from `cols` on are
+// 0, and their memory is not touched.
+__device__ __forceinline__ u32x4 load8(const uint16_t* row, uint64_t c, uint64_t cols) {
+  if (c + kChunk <= cols) return *reinterpret_cast<const u32x4_at2*>(row + c);
+  uint32_t e[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) e[i] = row[c + i < cols ? c + i : cols - 1];
   u32x4 w = {0, 0, 0, 0};
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (c + i < cols) w[i >> 1] |= static_cast<uint32_t>(row[c + i]) << (16 * (i & 1));
+  for (int i = 0; i < 8; ++i) w[i >> 1] |= (c + i < cols ? e[i] : 0u) << (16 * (i & 1));
   return w;
 }
 
-__device__ __forceinline__ void store8(uint16_t* row, uint64_t c, uint64_t cols, bool wide,
-                                       u32x4 w) {
-  if (wide && c + kChunk <= cols) {
-    *reinterpret_cast<u32x4*>(row + c) = w;
+__device__ __forceinline__ void store8(uint16_t* row, uint64_t c, uint64_t cols, u32x4 w) {
+  if (c + kChunk <= cols) {
+    *reinterpret_cast<u32x4_at2*>(row + c) = w;
     return;
   }
 #pragma unroll
@@ -102,21 +110,21 @@ __device__ __forceinline__ void store8(uint16_t* row, uint64_t c, uint64_t cols,
     if (c + i < cols) row[c + i] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
 }
 
-// Eight codes; `wide`: the row starts on 8 bytes.
-__device__ __forceinline__ u32x2 load_codes(const uint8_t* row, uint64_t c, uint64_t cols,
-                                            bool wide) {
-  if (wide && c + kChunk <= cols) return *reinterpret_cast<const u32x2*>(row + c);
+// Eight codes, likewise.
+__device__ __forceinline__ u32x2 load_codes(const uint8_t* row, uint64_t c, uint64_t cols) {
+  if (c + kChunk <= cols) return *reinterpret_cast<const u32x2_at1*>(row + c);
+  uint32_t e[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) e[i] = row[c + i < cols ? c + i : cols - 1];
   u32x2 w = {0, 0};
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (c + i < cols) w[i >> 2] |= static_cast<uint32_t>(row[c + i]) << (8 * (i & 3));
+  for (int i = 0; i < 8; ++i) w[i >> 2] |= (c + i < cols ? e[i] : 0u) << (8 * (i & 3));
   return w;
 }
 
-__device__ __forceinline__ void store_codes(uint8_t* row, uint64_t c, uint64_t cols, bool wide,
-                                            u32x2 w) {
-  if (wide && c + kChunk <= cols) {
-    *reinterpret_cast<u32x2*>(row + c) = w;
+__device__ __forceinline__ void store_codes(uint8_t* row, uint64_t c, uint64_t cols, u32x2 w) {
+  if (c + kChunk <= cols) {
+    *reinterpret_cast<u32x2_at1*>(row + c) = w;
     return;
   }
 #pragma unroll

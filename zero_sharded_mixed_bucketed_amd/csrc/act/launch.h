@@ -20,7 +20,6 @@ struct Ckpt {
   uint8_t* scales;
   uint64_t code_stride, scale_stride;
   int format;
-  int wide;  // code rows start on 8 bytes
 };
 
 struct StoreLaunch {  // write: x -> c; read: c -> x
@@ -28,7 +27,6 @@ struct StoreLaunch {  // write: x -> c; read: c -> x
   void* x;
   uint64_t x_stride;
   int dtype;
-  int wide;  // rows of x start on 16 bytes
   uint64_t rows, cols;
 };
 
@@ -39,7 +37,6 @@ hipError_t launch_ckpt_read(const StoreLaunch& a, hipStream_t stream);
 struct Rows {
   uint16_t* p;
   uint64_t stride;  // 0: the same row for every token
-  int wide;         // rows start on 16 bytes
 };
 
 struct NormArgs {
@@ -96,7 +93,6 @@ struct WeightGradLaunch {
   void* dw;
   uint64_t dw_stride;
   int dw_dtype, accumulate;
-  int dw_wide;                  // rows of dw start on 16 bytes
   float* partial;               // weight_grad_workspace bytes
 };
 

@@ -46,15 +46,13 @@ Ckpt ckpt_of(const zero_ckpt_t* c) {
   k.code_stride = c ? c->code_stride : 0;
   k.scale_stride = c ? c->scale_stride : 0;
   k.format = c ? c->format : ZERO_CKPT_INT8;
-  k.wide = c && aligned(c->codes, 8) && (c->code_stride % 8 == 0 || c->rows <= 1);
   return k;
 }
 
-Rows rows_of(const void* p, uint64_t stride, uint64_t rows) {
+Rows rows_of(const void* p, uint64_t stride) {
   Rows r;
   r.p = static_cast<uint16_t*>(const_cast<void*>(p));
   r.stride = stride;
-  r.wide = p && aligned(p, 16) && (stride % 8 == 0 || rows <= 1);
   return r;
 }
 
@@ -81,7 +79,6 @@ zero::act::StoreLaunch store_of(const void* x, int dtype, uint64_t stride, const
   L.x = const_cast<void*>(x);
   L.x_stride = stride;
   L.dtype = dtype;
-  L.wide = aligned(x, 16) && (stride % (dtype == ZERO_F32 ? 4 : 8) == 0 || c->rows <= 1);
   L.rows = c->rows;
   L.cols = c->cols;
   return L;
@@ -152,8 +149,8 @@ zero::act::NormArgs norm_of(const zero_norm_t& n) {
   zero::act::NormArgs a;
   a.kind = n.kind;
   a.eps = static_cast<float>(n.eps);
-  a.w = rows_of(n.weight, 0, 1);
-  a.b = rows_of(n.bias, 0, 1);
+  a.w = rows_of(n.weight, 0);
+  a.b = rows_of(n.bias, 0);
   return a;
 }
 
@@ -228,7 +225,6 @@ int zero_ckpt_weight_grad(const zero_ckpt_t* x, const void* dy, int dtype, uint6
   L.dw_stride = dw_stride;
   L.dw_dtype = dw_dtype;
   L.accumulate = accumulate;
-  L.dw_wide = aligned(dw, 16) && (dw_stride % (dw_dtype == ZERO_F32 ? 4 : 8) == 0 || n <= 1);
   L.partial = static_cast<float*>(workspace);
   return device(zero::act::launch_weight_grad(L, static_cast<hipStream_t>(hip_stream)),
                 "weight gradient");
@@ -267,11 +263,11 @@ int zero_block_norm(const zero_block_norm_t* a, void* hip_stream) {
   L.dtype = a->dtype;
   L.rows = a->rows;
   L.cols = static_cast<uint32_t>(a->cols);
-  L.res = rows_of(a->res, a->res_stride, a->rows);
-  L.block = rows_of(a->block, a->block_stride, a->rows);
-  L.gate = rows_of(a->gate, a->gate_stride, a->rows);
-  L.out = rows_of(a->out, a->out_stride, a->rows);
-  L.z = rows_of(a->z, a->z_stride, a->rows);
+  L.res = rows_of(a->res, a->res_stride);
+  L.block = rows_of(a->block, a->block_stride);
+  L.gate = rows_of(a->gate, a->gate_stride);
+  L.out = rows_of(a->out, a->out_stride);
+  L.z = rows_of(a->z, a->z_stride);
   L.post = norm_of(a->post);
   L.pre = norm_of(a->pre);
   L.scale = static_cast<float>(a->scale);
@@ -355,12 +351,12 @@ int zero_block_norm_grad(const zero_block_norm_grad_t* a, void* hip_stream) {
   L.dtype = a->dtype;
   L.rows = a->rows;
   L.cols = static_cast<uint32_t>(a->cols);
-  L.dout = rows_of(a->dout, a->dout_stride, a->rows);
-  L.dz = rows_of(a->dz, a->dz_stride, a->rows);
-  L.gate = rows_of(a->gate, a->gate_stride, a->rows);
-  L.dres = rows_of(a->dres, a->dres_stride, a->rows);
-  L.dblock = rows_of(a->dblock, a->dblock_stride, a->rows);
-  L.dgate = rows_of(gate_row ? nullptr : a->dgate, a->dgate_stride, a->rows);
+  L.dout = rows_of(a->dout, a->dout_stride);
+  L.dz = rows_of(a->dz, a->dz_stride);
+  L.gate = rows_of(a->gate, a->gate_stride);
+  L.dres = rows_of(a->dres, a->dres_stride);
+  L.dblock = rows_of(a->dblock, a->dblock_stride);
+  L.dgate = rows_of(gate_row ? nullptr : a->dgate, a->dgate_stride);
   L.c_out = ckpt_of(pre ? a->ckpt_out : nullptr);
   L.c_block = ckpt_of(need_block ? a->ckpt_block : nullptr);
   L.block = block;

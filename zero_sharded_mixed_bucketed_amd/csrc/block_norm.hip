@@ -59,8 +59,8 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float* red, int& turn) {
 template <typename T>
 __device__ __forceinline__ void row_of(const Rows& r, uint64_t c, uint32_t cols, float absent,
                                        float (&x)[8]) {
-  if (r.p) {
-    unpack8<T>(load8(r.p, c, cols, r.wide), x);
+  if (r.p && c < cols) {
+    unpack8<T>(load8(r.p, c, cols), x);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = absent;
@@ -75,7 +75,7 @@ __device__ __forceinline__ void emit(const Ckpt& c, uint64_t row, uint32_t chunk
                                         : encode8<T, kE4m3>(w, &scale);
   const uint32_t col = chunk * kChunk;
   if (!live || col >= cols) return;
-  store_codes(c.codes + row * c.code_stride, col, cols, c.wide, codes);
+  store_codes(c.codes + row * c.code_stride, col, cols, codes);
   if (chunk % kQuad == 0) c.scales[row * c.scale_stride + chunk / kQuad] = static_cast<uint8_t>(scale);
 }
 
@@ -130,10 +130,10 @@ __global__ __launch_bounds__(Shape<W>::kThreads) void block_norm_kernel(BlockNor
     for (int j = 0; j < kHeld; ++j) {
       const uint32_t chunk = j * S::kLanes + lane;
       u32x4 wx = {0, 0, 0, 0}, wb = {0, 0, 0, 0};
-      if (live) {
-        wx = load8(a.res.p + row * a.res.stride, chunk * kChunk, a.cols, a.res.wide);
+      if (live && chunk * kChunk < a.cols) {
+        wx = load8(a.res.p + row * a.res.stride, chunk * kChunk, a.cols);
         if (a.block.p)
-          wb = load8(a.block.p + row * a.block.stride, chunk * kChunk, a.cols, a.block.wide);
+          wb = load8(a.block.p + row * a.block.stride, chunk * kChunk, a.cols);
       }
       unpack8<T>(wx, x[j]);
       unpack8<T>(wb, b[j]);
@@ -163,7 +163,7 @@ __global__ __launch_bounds__(Shape<W>::kThreads) void block_norm_kernel(BlockNor
       const uint32_t chunk = j * S::kLanes + lane;
       const u32x4 w = pack8<T>(x[j]);
       if (a.out.p && live)
-        store8(a.out.p + row * a.out.stride, chunk * kChunk, a.cols, a.out.wide, w);
+        store8(a.out.p + row * a.out.stride, chunk * kChunk, a.cols, w);
       if (a.c_out.codes) emit<T>(a.c_out, row, chunk, a.cols, live, w);
     }
     if (a.pre.kind != ZERO_NORM_NONE) {
@@ -179,7 +179,7 @@ __global__ __launch_bounds__(Shape<W>::kThreads) void block_norm_kernel(BlockNor
         for (int i = 0; i < 8; ++i)
           z[i] = chunk * kChunk + i < a.cols ? (x[j][i] - st[2]) * st[3] * w[i] + c[i] : 0.f;
         const u32x4 wz = pack8<T>(z);
-        if (live) store8(a.z.p + row * a.z.stride, chunk * kChunk, a.cols, a.z.wide, wz);
+        if (live) store8(a.z.p + row * a.z.stride, chunk * kChunk, a.cols, wz);
         if (a.c_z.codes) emit<T>(a.c_z, row, chunk, a.cols, live, wz);
       }
     }
@@ -240,9 +240,8 @@ __global__ __launch_bounds__(Shape<W>::kThreads) void block_norm_grad_kernel(
 #pragma unroll
     for (int j = 0; j < kHeld; ++j) {
       u32x4 w = {0, 0, 0, 0};
-      if (live && a.dout.p)
-        w = load8(a.dout.p + row * a.dout.stride, (j * S::kLanes + lane) * kChunk, a.cols,
-                  a.dout.wide);
+      if (live && a.dout.p && (j * S::kLanes + lane) * kChunk < a.cols)
+        w = load8(a.dout.p + row * a.dout.stride, (j * S::kLanes + lane) * kChunk, a.cols);
       unpack8<T>(w, d[j]);
     }
     if (pre) {
@@ -255,8 +254,8 @@ __global__ __launch_bounds__(Shape<W>::kThreads) void block_norm_grad_kernel(
         u32x2 c = {0, 0};
         uint32_t sb = 0;
         if (live && col < a.cols) {
-          w = load8(a.dz.p + row * a.dz.stride, col, a.cols, a.dz.wide);
-          c = load_codes(a.c_out.codes + row * a.c_out.code_stride, col, a.cols, a.c_out.wide);
+          w = load8(a.dz.p + row * a.dz.stride, col, a.cols);
+          c = load_codes(a.c_out.codes + row * a.c_out.code_stride, col, a.cols);
           sb = a.c_out.scales[row * a.c_out.scale_stride + chunk / kQuad];
         }
         unpack8<T>(w, q[j]);
@@ -285,8 +284,7 @@ __global__ __launch_bounds__(Shape<W>::kThreads) void block_norm_grad_kernel(
     if (a.dres.p && live) {
 #pragma unroll
       for (int j = 0; j < kHeld; ++j)
-        store8(a.dres.p + row * a.dres.stride, (j * S::kLanes + lane) * kChunk, a.cols,
-               a.dres.wide, pack8<T>(d[j]));
+        store8(a.dres.p + row * a.dres.stride, (j * S::kLanes + lane) * kChunk, a.cols, pack8<T>(d[j]));
     }
     if (block) {
       float v[kHeld][8], xn[kHeld][8];
@@ -297,8 +295,7 @@ __global__ __launch_bounds__(Shape<W>::kThreads) void block_norm_grad_kernel(
         u32x2 c = {0, 0};
         uint32_t sb = 0;
         if (live && col < a.cols && a.c_block.codes) {
-          c = load_codes(a.c_block.codes + row * a.c_block.code_stride, col, a.cols,
-                         a.c_block.wide);
+          c = load_codes(a.c_block.codes + row * a.c_block.code_stride, col, a.cols);
           sb = a.c_block.scales[row * a.c_block.scale_stride + chunk / kQuad];
         }
         if (a.c_block.format == kInt8) decode8<kInt8>(c, scale_of(sb), xn[j]);
@@ -325,7 +322,7 @@ __global__ __launch_bounds__(Shape<W>::kThreads) void block_norm_grad_kernel(
           t[1] += v[j][i];
         }
         if (a.dgate.p && live)
-          store8(a.dgate.p + row * a.dgate.stride, col, a.cols, a.dgate.wide, pack8<T>(dg));
+          store8(a.dgate.p + row * a.dgate.stride, col, a.cols, pack8<T>(dg));
       }
       if (a.dblock.p) {
         if (a.post.kind != ZERO_NORM_NONE) {
@@ -339,8 +336,7 @@ __global__ __launch_bounds__(Shape<W>::kThreads) void block_norm_grad_kernel(
         if (live) {
 #pragma unroll
           for (int j = 0; j < kHeld; ++j)
-            store8(a.dblock.p + row * a.dblock.stride, (j * S::kLanes + lane) * kChunk, a.cols,
-                   a.dblock.wide, pack8<T>(v[j]));
+            store8(a.dblock.p + row * a.dblock.stride, (j * S::kLanes + lane) * kChunk, a.cols, pack8<T>(v[j]));
         }
       }
     }

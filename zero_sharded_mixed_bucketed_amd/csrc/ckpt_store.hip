@@ -46,9 +46,8 @@ __global__ __launch_bounds__(kThreads) void ckpt_write_kernel(StoreLaunch a, uin
   for (int j = 0; j < kPerThread; ++j) {
     at[j] = where(row0, first, j * kThreads + threadIdx.x, per_row);
     w[j] = u32x4{0, 0, 0, 0};
-    if (at[j].row < a.rows)
-      w[j] = load8(x + at[j].row * a.x_stride, static_cast<uint64_t>(at[j].chunk) * kChunk,
-                   a.cols, a.wide);
+    const uint64_t col = static_cast<uint64_t>(at[j].chunk) * kChunk;
+    if (at[j].row < a.rows && col < a.cols) w[j] = load8(x + at[j].row * a.x_stride, col, a.cols);
   }
 #pragma unroll
   for (int j = 0; j < kPerThread; ++j) {
@@ -56,7 +55,7 @@ __global__ __launch_bounds__(kThreads) void ckpt_write_kernel(StoreLaunch a, uin
     const u32x2 codes = encode8<T, FMT>(w[j], &scale);
     if (at[j].row >= a.rows) continue;
     store_codes(a.c.codes + at[j].row * a.c.code_stride,
-                static_cast<uint64_t>(at[j].chunk) * kChunk, a.cols, a.c.wide, codes);
+                static_cast<uint64_t>(at[j].chunk) * kChunk, a.cols, codes);
     if ((at[j].chunk & (kQuad - 1)) == 0)
       a.c.scales[at[j].row * a.c.scale_stride + at[j].chunk / kQuad] =
           static_cast<uint8_t>(scale);
@@ -78,7 +77,7 @@ __global__ __launch_bounds__(kThreads) void ckpt_read_kernel(StoreLaunch a, uint
     s[j] = 0;
     const uint64_t col = static_cast<uint64_t>(at[j].chunk) * kChunk;
     if (at[j].row < a.rows && col < a.cols) {
-      w[j] = load_codes(a.c.codes + at[j].row * a.c.code_stride, col, a.cols, a.c.wide);
+      w[j] = load_codes(a.c.codes + at[j].row * a.c.code_stride, col, a.cols);
       s[j] = a.c.scales[at[j].row * a.c.scale_stride + at[j].chunk / kQuad];
     }
   }
@@ -90,9 +89,9 @@ __global__ __launch_bounds__(kThreads) void ckpt_read_kernel(StoreLaunch a, uint
     decode8<FMT>(w[j], scale_of(s[j]), x);
     if constexpr (DTYPE == kF32) {
       float* row = static_cast<float*>(a.x) + at[j].row * a.x_stride;
-      if (a.wide && col + kChunk <= a.cols) {
-        *reinterpret_cast<f32x4*>(row + col) = f32x4{x[0], x[1], x[2], x[3]};
-        *reinterpret_cast<f32x4*>(row + col + 4) = f32x4{x[4], x[5], x[6], x[7]};
+      if (col + kChunk <= a.cols) {
+        *reinterpret_cast<f32x4_at4*>(row + col) = f32x4{x[0], x[1], x[2], x[3]};
+        *reinterpret_cast<f32x4_at4*>(row + col + 4) = f32x4{x[4], x[5], x[6], x[7]};
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -100,8 +99,7 @@ __global__ __launch_bounds__(kThreads) void ckpt_read_kernel(StoreLaunch a, uint
       }
     } else {
       using T = typename std::conditional<DTYPE == kF16, F16, Bf16>::type;
-      store8(static_cast<uint16_t*>(a.x) + at[j].row * a.x_stride, col, a.cols, a.wide,
-             pack8<T>(x));
+      store8(static_cast<uint16_t*>(a.x) + at[j].row * a.x_stride, col, a.cols, pack8<T>(x));
     }
   }
 }

@@ -75,14 +75,14 @@ __device__ __forceinline__ void wave_order() {
 struct Dest {
   void* p;
   uint64_t stride;
-  int dtype, accumulate, wide;
+  int dtype, accumulate;
 };
 
 __device__ __forceinline__ Dest destination(const WeightGradLaunch& a, uint32_t split,
                                             uint64_t per_split) {
   if (per_split < a.rows)
-    return {a.partial + split * a.n * a.k, a.k, kF32, 0, a.k % 4 == 0};
-  return {a.dw, a.dw_stride, a.dw_dtype, a.accumulate, a.dw_wide};
+    return {a.partial + split * a.n * a.k, a.k, kF32, 0};
+  return {a.dw, a.dw_stride, a.dw_dtype, a.accumulate};
 }
 
 __device__ __forceinline__ void put(const Dest& d, uint64_t at, float s) {
@@ -100,7 +100,7 @@ __device__ __forceinline__ void put(const Dest& d, uint64_t at, float s) {
 
 template <typename T>
 __device__ __forceinline__ void put8_16(uint16_t* o, int accumulate, float (&x)[8]) {
-  u32x4* w = reinterpret_cast<u32x4*>(o);
+  u32x4_at2* w = reinterpret_cast<u32x4_at2*>(o);
   if (accumulate) {
     float old[8];
     unpack8<T>(*w, old);
@@ -115,9 +115,9 @@ __device__ __forceinline__ void put8(const Dest& d, uint64_t n, uint64_t k, uint
                                      f32x4 v) {
   const uint64_t at = n * d.stride + k;
   float x[8] = {u[0], u[1], u[2], u[3], v[0], v[1], v[2], v[3]};
-  if (d.wide && k + kChunk <= cols) {
+  if (k + kChunk <= cols) {
     if (d.dtype == kF32) {
-      f32x4* o = reinterpret_cast<f32x4*>(static_cast<float*>(d.p) + at);
+      f32x4_at4* o = reinterpret_cast<f32x4_at4*>(static_cast<float*>(d.p) + at);
       if (d.accumulate) {
         u += o[0];
         v += o[1];
@@ -163,14 +163,13 @@ __device__ __forceinline__ Piece piece_of(uint32_t wg, uint32_t wgs, uint32_t tk
 // the one after it is loaded into those registers; the operands of a matrix step
 // are read during the step before it.
 //
-// WIDE: rows of dY start on 16 bytes and rows of codes on 8.  Whole tiles are then
-// loaded without a branch: columns past the matrix read padding between rows, or
-// other columns, and reach only sums that are not stored.  The tile that holds
-// the split's last tokens is loaded with every check.
-template <typename T, int FMT, int TILE, int DEPTH, bool WIDE>
-__global__ __launch_bounds__(kThreads) void weight_grad_kernel(WeightGradLaunch a, int dy_wide,
-                                                               uint64_t per_split, uint32_t tk,
-                                                               uint32_t tiles) {
+// Whole tiles below token `safe` are loaded without a branch: chunks that pass a
+// row's end read what follows it, which reaches only sums that are not stored.
+// Other tiles are loaded with every check.
+template <typename T, int FMT, int TILE, int DEPTH>
+__global__ __launch_bounds__(kThreads) void weight_grad_kernel(WeightGradLaunch a,
+                                                               uint64_t safe, uint64_t per_split,
+                                                               uint32_t tk, uint32_t tiles) {
   constexpr int kF = TILE / 2 / kFrag;                    // fragments of a wave, each way
   constexpr uint32_t kRowLanes = TILE / kChunk;           // lanes of a tile row
   constexpr uint32_t kStep = kThreads / kRowLanes;        // rows a pass of the workgroup
@@ -205,9 +204,9 @@ __global__ __launch_bounds__(kThreads) void weight_grad_kernel(WeightGradLaunch 
       u32x2 x = {0, 0};
       uint32_t b = 0;
       if (t < t_hi) {
-        if (in_n) y = load8(a.dy + t * a.dy_stride, n0 + sc, a.n, dy_wide);
+        if (in_n) y = load8(a.dy + t * a.dy_stride, n0 + sc, a.n);
         if (in_k) {
-          x = load_codes(a.x.codes + t * a.x.code_stride, k0 + sc, a.k, a.x.wide);
+          x = load_codes(a.x.codes + t * a.x.code_stride, k0 + sc, a.k);
           b = a.x.scales[t * a.x.scale_stride + (k0 + sc) / kBlock];
         }
       }
@@ -220,15 +219,20 @@ __global__ __launch_bounds__(kThreads) void weight_grad_kernel(WeightGradLaunch 
         }
     }
   };
-  // the lane's columns, or column 0 where the tile passes the matrix's edge
-  const uint16_t* py = a.dy + (in_n ? n0 + sc : 0);
-  const uint8_t* px = a.x.codes + (in_k ? k0 + sc : 0);
-  const uint8_t* ps = a.x.scales + (in_k ? (k0 + sc) / kBlock : 0);
+  // Bytes from a pass's first row to the lane's columns (column 0 where the tile
+  // passes the matrix's edge); the row itself is the same for all lanes.
+  const uint32_t oy = st * static_cast<uint32_t>(a.dy_stride) * 2 +
+                      static_cast<uint32_t>(in_n ? n0 + sc : 0) * 2;
+  const uint32_t ox = st * static_cast<uint32_t>(a.x.code_stride) +
+                      static_cast<uint32_t>(in_k ? k0 + sc : 0);
+  const uint32_t os = st * static_cast<uint32_t>(a.x.scale_stride) +
+                      static_cast<uint32_t>(in_k ? (k0 + sc) / kBlock : 0);
   auto load_one = [&](uint64_t t0, int i) {               // tokens below `whole`
-    const uint64_t t = t0 + i * kStep + st;
-    ry[i] = *reinterpret_cast<const u32x4*>(py + t * a.dy_stride);
-    rx[i] = *reinterpret_cast<const u32x2*>(px + t * a.x.code_stride);
-    rs[i] = ps[t * a.x.scale_stride];
+    const uint64_t t = t0 + i * kStep;
+    ry[i] = *reinterpret_cast<const u32x4_at2*>(
+        reinterpret_cast<const uint8_t*>(a.dy + t * a.dy_stride) + oy);
+    rx[i] = *reinterpret_cast<const u32x2_at1*>(a.x.codes + t * a.x.code_stride + ox);
+    rs[i] = *(a.x.scales + t * a.x.scale_stride + os);
   };
   // A pass from registers to shared memory in kParts parts, the loads that refill
   // its registers last.
@@ -253,12 +257,9 @@ __global__ __launch_bounds__(kThreads) void weight_grad_kernel(WeightGradLaunch 
         *reinterpret_cast<u32x4*>(&lx[buf][place<TILE>(t, sc)]) = held;
     }
   };
-  // Tokens that wide loads may take: chunks that pass the last column must not
-  // reach past the matrix's last row.
-  uint64_t whole = t_hi;
-  if (t_hi == a.rows && (a.n % kChunk || a.k % kChunk) && t_hi > t_lo) whole = t_hi - 1;
+  const uint64_t whole = t_hi < safe ? t_hi : safe;
   auto load = [&](uint64_t t0) {
-    if (WIDE && t0 + DEPTH <= whole) {
+    if (t0 + DEPTH <= whole) {
 #pragma unroll
       for (int i = 0; i < kPass; ++i) load_one(t0, i);
     } else {
@@ -339,10 +340,9 @@ __global__ __launch_bounds__(kThreads) void weight_grad_kernel(WeightGradLaunch 
     }
     buf ^= 1;
   };
-  if constexpr (WIDE) {
-    for (; t0 + 3 * DEPTH <= whole; t0 += DEPTH)
-      turn([&](int i) { load_one(t0 + 2 * DEPTH, i); });
-  }
+#pragma unroll 1
+  for (; t0 + 3 * DEPTH <= whole; t0 += DEPTH)
+    turn([&](int i) { load_one(t0 + 2 * DEPTH, i); });
 #pragma unroll 1
   for (; t0 < t_hi; t0 += DEPTH) {
     turn([](int) {});
@@ -359,7 +359,7 @@ __global__ __launch_bounds__(kThreads) void weight_grad_kernel(WeightGradLaunch 
   float* piece = lds + wave * kFrag * kPitch;
   const Dest out = destination(a, split, per_split);
   // a whole tile that is only stored, in 16-byte pieces
-  const bool inside = out.wide && !out.accumulate && n0 + TILE <= a.n && k0 + TILE <= a.k;
+  const bool inside = !out.accumulate && n0 + TILE <= a.n && k0 + TILE <= a.k;
 #pragma unroll
   for (int i = 0; i < kF; ++i) {
 #pragma unroll
@@ -385,14 +385,14 @@ __global__ __launch_bounds__(kThreads) void weight_grad_kernel(WeightGradLaunch 
 #pragma unroll
       for (int r = 0; r < kRows; ++r) {
         const float x[8] = {u[r][0], u[r][1], u[r][2], u[r][3], v[r][0], v[r][1], v[r][2], v[r][3]};
-        *reinterpret_cast<u32x4*>(o + r * (64 / kLanes) * out.stride) = pack8<T>(x);
+        *reinterpret_cast<u32x4_at2*>(o + r * (64 / kLanes) * out.stride) = pack8<T>(x);
       }
     } else if (inside) {
       float* o = static_cast<float*>(out.p) + n * out.stride + k;
 #pragma unroll
       for (int r = 0; r < kRows; ++r) {
-        *reinterpret_cast<f32x4*>(o + r * (64 / kLanes) * out.stride) = u[r];
-        *reinterpret_cast<f32x4*>(o + r * (64 / kLanes) * out.stride + 4) = v[r];
+        *reinterpret_cast<f32x4_at4*>(o + r * (64 / kLanes) * out.stride) = u[r];
+        *reinterpret_cast<f32x4_at4*>(o + r * (64 / kLanes) * out.stride + 4) = v[r];
       }
     } else {
 #pragma unroll 1
@@ -415,14 +415,14 @@ __global__ __launch_bounds__(kThreads) void weight_grad_join_kernel(WeightGradLa
   const uint64_t id = static_cast<uint64_t>(blockIdx.x) * kThreads + threadIdx.x;
   const uint64_t n = id / per_row, k = id % per_row * kChunk;
   if (n >= a.n) return;
-  const bool wide = a.k % 4 == 0 && k + kChunk <= a.k;
+  const bool whole = k + kChunk <= a.k;
   f32x4 u = {0.f, 0.f, 0.f, 0.f}, v = u;
   const float* p = a.partial + n * a.k + k;
 #pragma unroll 8
   for (uint32_t s = 0; s < splits; ++s, p += count) {
-    if (wide) {
-      u += *reinterpret_cast<const f32x4*>(p);
-      v += *reinterpret_cast<const f32x4*>(p + 4);
+    if (whole) {
+      u += *reinterpret_cast<const f32x4_at4*>(p);
+      v += *reinterpret_cast<const f32x4_at4*>(p + 4);
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -431,7 +431,7 @@ __global__ __launch_bounds__(kThreads) void weight_grad_join_kernel(WeightGradLa
       }
     }
   }
-  put8({a.dw, a.dw_stride, a.dw_dtype, a.accumulate, a.dw_wide}, n, k, a.k, u, v);
+  put8({a.dw, a.dw_stride, a.dw_dtype, a.accumulate}, n, k, a.k, u, v);
 }
 
 struct Plan {
@@ -480,23 +480,25 @@ Plan plan(uint64_t rows, uint64_t k, uint64_t n) {
   return best;
 }
 
-template <typename T, int FMT, int TILE, int DEPTH>
-void run_tile(const WeightGradLaunch& a, const Plan& p, uint32_t wgs, int dy_wide,
-              hipStream_t stream) {
+template <typename T, int FMT>
+void run(const WeightGradLaunch& a, const Plan& p, uint32_t wgs, uint64_t safe,
+         hipStream_t stream) {
   const uint32_t tk = static_cast<uint32_t>(p.tk), tiles = static_cast<uint32_t>(p.tn * p.tk);
-  if (dy_wide && a.x.wide)
-    weight_grad_kernel<T, FMT, TILE, DEPTH, true>
-        <<<wgs, kThreads, 0, stream>>>(a, dy_wide, p.per_split, tk, tiles);
+  if (p.tile == 256)
+    weight_grad_kernel<T, FMT, 256, 64>
+        <<<wgs, kThreads, 0, stream>>>(a, safe, p.per_split, tk, tiles);
   else
-    weight_grad_kernel<T, FMT, TILE, DEPTH, false>
-        <<<wgs, kThreads, 0, stream>>>(a, dy_wide, p.per_split, tk, tiles);
+    weight_grad_kernel<T, FMT, 128, 32>
+        <<<wgs, kThreads, 0, stream>>>(a, safe, p.per_split, tk, tiles);
 }
 
-template <typename T, int FMT>
-void run(const WeightGradLaunch& a, const Plan& p, uint32_t wgs, int dy_wide,
-         hipStream_t stream) {
-  if (p.tile == 256) run_tile<T, FMT, 256, 64>(a, p, wgs, dy_wide, stream);
-  else run_tile<T, FMT, 128, 32>(a, p, wgs, dy_wide, stream);
+// Rows of a rows x cols matrix whose chunks all end inside it, though the last one
+// may pass its own row's end.
+uint64_t safe_rows(uint64_t rows, uint64_t cols, uint64_t stride) {
+  const uint64_t over = (kChunk - cols % kChunk) % kChunk;
+  if (over == 0) return rows;
+  const uint64_t back = rows > 1 ? (over + stride - 1) / stride : rows;
+  return back < rows ? rows - back : 0;
 }
 
 }  // namespace
@@ -510,14 +512,18 @@ hipError_t launch_weight_grad(const WeightGradLaunch& a, hipStream_t stream) {
   const Plan p = plan(a.rows, a.k, a.n);
   const uint64_t wgs = p.tn * p.tk * p.splits;   // at most 2^30 tiles of 128 x 128
   if (wgs > 0x7FFFFFFFull) return hipErrorInvalidConfiguration;
-  const int dy_wide = reinterpret_cast<uintptr_t>(a.dy) % 16 == 0 &&
-                      (a.dy_stride % 8 == 0 || a.rows <= 1);
+  const uint64_t of_y = safe_rows(a.rows, a.n, a.dy_stride);
+  const uint64_t of_x = safe_rows(a.rows, a.k, a.x.code_stride);
+  uint64_t safe = of_y < of_x ? of_y : of_x;
+  // offsets inside a pass of 16 rows are 32 bits wide
+  constexpr uint64_t kFar = 1ull << 26;
+  if (a.dy_stride >= kFar || a.x.code_stride >= kFar || a.x.scale_stride >= kFar) safe = 0;
   if (a.dtype == kF16) {
-    if (a.x.format == kInt8) run<F16, kInt8>(a, p, wgs, dy_wide, stream);
-    else run<F16, kE4m3>(a, p, wgs, dy_wide, stream);
+    if (a.x.format == kInt8) run<F16, kInt8>(a, p, wgs, safe, stream);
+    else run<F16, kE4m3>(a, p, wgs, safe, stream);
   } else {
-    if (a.x.format == kInt8) run<Bf16, kInt8>(a, p, wgs, dy_wide, stream);
-    else run<Bf16, kE4m3>(a, p, wgs, dy_wide, stream);
+    if (a.x.format == kInt8) run<Bf16, kInt8>(a, p, wgs, safe, stream);
+    else run<Bf16, kE4m3>(a, p, wgs, safe, stream);
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
