@@ -452,7 +452,8 @@ typedef struct zero_block_norm_grad {
   const void *dz; /* gradient of z; NULL if and only if pre.kind is ZERO_NORM_NONE */
   uint64_t dz_stride;
   const zero_ckpt_t *ckpt_out;   /* of h'; needed if pre is a norm */
-  const zero_ckpt_t *ckpt_block; /* of b; needed if post is a norm or dgate is given */
+  const zero_ckpt_t *ckpt_block; /* of b; needed if post is a norm or dgate is given; of
+                                    ckpt_out's format if both are needed */
   const float *stats;            /* as zero_block_norm left them; needed with a norm */
   const void *gate;
   uint64_t gate_stride;

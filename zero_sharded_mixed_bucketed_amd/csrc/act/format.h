@@ -70,6 +70,14 @@ __device__ __forceinline__ uint32_t pack16(float a, float b) {
   }
 }
 
+// Keeps the compiler from carrying what it made from a packed value past this
+// point (unpacking again is cheaper than holding twice the registers), and from
+// unpacking one before it, where that would wait for a load.
+template <typename V>
+__device__ __forceinline__ void forget(V& w) {
+  asm volatile("" : "+v"(w));
+}
+
 template <typename T>
 __device__ __forceinline__ void unpack8(u32x4 w, float (&x)[8]) {
 #pragma unroll
@@ -130,6 +138,75 @@ __device__ __forceinline__ void store_codes(uint8_t* row, uint64_t c, uint64_t c
 #pragma unroll
   for (int i = 0; i < 8; ++i)
     if (c + i < cols) row[c + i] = static_cast<uint8_t>(w[i >> 2] >> (8 * (i & 3)));
+}
+
+// The same for kernels that issue the loads of many chunks before they use them:
+// every lane loads its chunk without a branch, or, past the last whole chunk, the
+// row's last eight elements; mend8 then shifts those into place, or puts 0 where
+// the row has ended.  Rows of fewer than eight elements are loaded by mend8.
+// FULL: every chunk is whole.
+template <bool FULL>
+__device__ __forceinline__ uint32_t early(uint32_t c, uint32_t cols) {
+  if constexpr (FULL) return c;
+  return c + kChunk <= cols ? c : cols - kChunk;
+}
+
+template <bool FULL>
+__device__ __forceinline__ u32x4 load8_early(const uint16_t* row, uint32_t c, uint32_t cols) {
+  if (!FULL && cols < kChunk) return u32x4{0, 0, 0, 0};
+  return *reinterpret_cast<const u32x4_at2*>(row + early<FULL>(c, cols));
+}
+
+template <bool FULL>
+__device__ __forceinline__ u32x2 load_codes_early(const uint8_t* row, uint32_t c, uint32_t cols) {
+  if (!FULL && cols < kChunk) return u32x2{0, 0};
+  return *reinterpret_cast<const u32x2_at1*>(row + early<FULL>(c, cols));
+}
+
+template <bool FULL>
+__device__ __forceinline__ void mend8(u32x4& w, const uint16_t* row, uint32_t c, uint32_t cols) {
+  if (FULL || c + kChunk <= cols) return;
+  if (c >= cols) {
+    w = u32x4{0, 0, 0, 0};
+  } else if (cols < kChunk) {
+    w = load8(row, c, cols);
+  } else {
+    const uint32_t by = c + kChunk - cols;   // elements to drop, 1 .. 7
+    if (by & 4) w = u32x4{w[2], w[3], 0, 0};
+    if (by & 2) w = u32x4{w[1], w[2], w[3], 0};
+    if (by & 1)
+      w = u32x4{__builtin_amdgcn_alignbit(w[1], w[0], 16), __builtin_amdgcn_alignbit(w[2], w[1], 16),
+                __builtin_amdgcn_alignbit(w[3], w[2], 16), w[3] >> 16};
+  }
+}
+
+// Both at once, for rows that lie in the caches.
+template <bool FULL>
+__device__ __forceinline__ u32x4 load8_row(const uint16_t* row, uint32_t c, uint32_t cols) {
+  u32x4 w = load8_early<FULL>(row, c, cols);
+  mend8<FULL>(w, row, c, cols);
+  return w;
+}
+
+template <bool FULL>
+__device__ __forceinline__ void store8_row(uint16_t* row, uint32_t c, uint32_t cols, u32x4 w) {
+  if constexpr (FULL) *reinterpret_cast<u32x4_at2*>(row + c) = w;
+  else if (c < cols) store8(row, c, cols, w);
+}
+
+template <bool FULL>
+__device__ __forceinline__ void mend_codes(u32x2& w, const uint8_t* row, uint32_t c,
+                                           uint32_t cols) {
+  if (FULL || c + kChunk <= cols) return;
+  if (c >= cols) {
+    w = u32x2{0, 0};
+  } else if (cols < kChunk) {
+    w = load_codes(row, c, cols);
+  } else {
+    const uint32_t by = c + kChunk - cols;
+    const uint64_t v = (static_cast<uint64_t>(w[1]) << 32 | w[0]) >> (8 * by);
+    w = u32x2{static_cast<uint32_t>(v), static_cast<uint32_t>(v >> 32)};
+  }
 }
 
 // ------------------------------------------------------------ the 8-bit format

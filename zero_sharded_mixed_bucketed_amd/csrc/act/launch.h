@@ -67,7 +67,8 @@ struct BlockNormGradLaunch {
   uint64_t rows;
   uint32_t cols;
   Rows dout, dz, gate, dres, dblock, dgate;  // dgate: per token
-  Ckpt c_out, c_block;          // absent where not needed
+  Ckpt c_out, c_block;          // absent where not needed; both of `format`
+  int format;
   int block;                    // an output on the block's side is wanted
   const float* stats;
   NormArgs post, pre;

@@ -335,6 +335,8 @@ int zero_block_norm_grad(const zero_block_norm_grad_t* a, void* hip_stream) {
       return fail(ZERO_E_INVAL, "a pre norm needs dz and ckpt_out");
     if (need_block && !a->ckpt_block)
       return fail(ZERO_E_INVAL, "a post norm or dgate needs ckpt_block");
+    if (pre && need_block && a->ckpt_out->format != a->ckpt_block->format)
+      return fail(ZERO_E_INVAL, "ckpt_out and ckpt_block have different formats");
     if ((pre || (block && post)) && !a->stats) return fail(ZERO_E_INVAL, "a norm needs stats");
   }
   const uint64_t need = any ? zero::act::norm_grad_workspace(a->rows, a->cols) : 0;
@@ -359,6 +361,7 @@ int zero_block_norm_grad(const zero_block_norm_grad_t* a, void* hip_stream) {
   L.dgate = rows_of(gate_row ? nullptr : a->dgate, a->dgate_stride);
   L.c_out = ckpt_of(pre ? a->ckpt_out : nullptr);
   L.c_block = ckpt_of(need_block ? a->ckpt_block : nullptr);
+  L.format = pre ? a->ckpt_out->format : need_block ? a->ckpt_block->format : ZERO_CKPT_INT8;
   L.block = block;
   L.stats = a->stats;
   L.post = norm_of(a->post);

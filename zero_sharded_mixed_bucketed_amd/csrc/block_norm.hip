@@ -4,10 +4,10 @@
 // with post and pre an RMS or layer norm (or none), and their backward from the
 // 8-bit checkpoints of b and h'.
 //
-// A row is held by W waves, two chunks of eight columns a thread, from the first
-// load to the last store: each input is read once and each output written once,
-// and the row sums go through lane exchanges and, between waves, shared memory.
-// Bound by memory: 8 bytes an element forward, about 10 backward.
+// One workgroup holds a row from the first load to the last store: each input is
+// read once and each output written once.  A thread holds chunks of eight columns;
+// row sums go through lane exchanges and, where a row has several waves, shared
+// memory.  Bound by memory: 8 bytes an element forward, about 10 backward.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -19,342 +19,506 @@ namespace zero {
 namespace act {
 namespace {
 
-constexpr int kHeld = 2;  // chunks a thread holds
-
-template <int W>
-struct Shape {
-  static constexpr int kLanes = 64 * W;                            // of a row
-  static constexpr int kThreads = kLanes < 256 ? 256 : kLanes;     // of a workgroup
-  static constexpr int kGroups = kThreads / kLanes;                // rows at a time
-};
-
-// Sums of N values over the row's lanes, in every lane, in a fixed order.  The
-// two halves of `red` take turns, so one barrier a call is enough: whoever
-// writes a half again has passed the barrier that followed its last reads.
-template <int W, int N>
-__device__ __forceinline__ void row_sums(float (&v)[N], float* red, int& turn) {
+// Sums of N values over the workgroup's `waves` waves, in every lane, in a fixed
+// order.  The two halves of `red` take turns, so one barrier a call is enough:
+// whoever writes a half again has passed the barrier that followed its last reads.
+template <int MAX_WAVES, int N>
+__device__ __forceinline__ void row_sums(float (&v)[N], float* red, int& turn, int waves) {
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
-  if constexpr (W > 1) {
-    constexpr int kWaves = Shape<W>::kThreads / 64;
-    const int wave = threadIdx.x / 64;
-    float* half = red + turn * (kWaves * N);
+  if constexpr (MAX_WAVES > 1) {
+    if (waves == 1) return;
+    float* half = red + turn * (MAX_WAVES * N);
     turn ^= 1;
     if (threadIdx.x % 64 == 0) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) half[wave * N + i] = v[i];
+      for (int i = 0; i < N; ++i) half[threadIdx.x / 64 * N + i] = v[i];
     }
     __syncthreads();
-    const int first = wave / W * W;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      float s = 0.f;
+    for (int i = 0; i < N; ++i) v[i] = half[i];
+    for (int k = 1; k < waves; ++k)
 #pragma unroll
-      for (int k = 0; k < W; ++k) s += half[(first + k) * N + i];
-      v[i] = s;
-    }
-  }
-}
-
-template <typename T>
-__device__ __forceinline__ void row_of(const Rows& r, uint64_t c, uint32_t cols, float absent,
-                                       float (&x)[8]) {
-  if (r.p && c < cols) {
-    unpack8<T>(load8(r.p, c, cols), x);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = absent;
+      for (int i = 0; i < N; ++i) v[i] += half[k * N + i];
   }
 }
 
 template <typename T>
 __device__ __forceinline__ void emit(const Ckpt& c, uint64_t row, uint32_t chunk, uint32_t cols,
-                                     bool live, u32x4 w) {
+                                     u32x4 w) {
   uint32_t scale;
   const u32x2 codes = c.format == kInt8 ? encode8<T, kInt8>(w, &scale)
                                         : encode8<T, kE4m3>(w, &scale);
   const uint32_t col = chunk * kChunk;
-  if (!live || col >= cols) return;
+  if (col >= cols) return;
   store_codes(c.codes + row * c.code_stride, col, cols, codes);
-  if (chunk % kQuad == 0) c.scales[row * c.scale_stride + chunk / kQuad] = static_cast<uint8_t>(scale);
+  if (chunk % kQuad == 0)
+    c.scales[row * c.scale_stride + chunk / kQuad] = static_cast<uint8_t>(scale);
 }
 
-// (mean, 1 / deviation) of the row; columns beyond the row hold 0.
-template <int W>
-__device__ __forceinline__ void row_stats(const float (&x)[kHeld][8], int kind, float eps,
-                                          uint32_t cols, float inv_n, uint32_t lane, float* red,
-                                          int& turn, float* mean, float* rstd) {
-  float m = 0.f;
-  if (kind == ZERO_NORM_LAYER) {
-    float s[1] = {0.f};
+// ------------------------------------------------------------ forward
+
+// Up to eight chunks a thread: rows of up to 4096 columns take one wave, and its
+// sums no barrier.  Nothing is kept from row to row; many rows at once on a compute
+// unit hide the loads, and the norms' weights come from the caches.  At 16384 x
+// 4096 bf16 with a gate a channel this moves FORWARD_RATE.
+template <typename T, int WAVES, int HELD, bool FULL>
+__global__ __launch_bounds__(64 * WAVES, HELD > 5 ? 3 : 4) void block_norm_kernel(BlockNormLaunch a,
+                                                                   uint64_t row0) {
+  constexpr uint32_t kLanes = 64 * WAVES;
+  __shared__ float red[2 * WAVES];
+  int turn = 0;
+  const uint64_t row = row0 + blockIdx.x;
+  const uint32_t lane = threadIdx.x, cols = a.cols;
+  const float inv_n = 1.0f / static_cast<float>(cols);
+  const uint16_t* res = a.res.p + row * a.res.stride;
+  const uint16_t* block = a.block.p + row * a.block.stride;
+  const uint16_t* gate = a.gate.p + row * a.gate.stride;
+  const bool has_block = a.block.p != nullptr;
+
+  u32x4 wx[HELD], wb[HELD];
 #pragma unroll
-    for (int j = 0; j < kHeld; ++j)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) s[0] += x[j][i];
-    row_sums<W>(s, red, turn);
-    m = s[0] * inv_n;
+  for (int j = 0; j < HELD; ++j) {
+    const uint32_t c = (j * kLanes + lane) * kChunk;
+    wx[j] = load8_early<FULL>(res, c, cols);
+    wb[j] = u32x4{0, 0, 0, 0};
+    if (has_block) wb[j] = load8_early<FULL>(block, c, cols);
   }
-  float q[1] = {0.f};
 #pragma unroll
-  for (int j = 0; j < kHeld; ++j) {
-    const uint32_t col = (j * Shape<W>::kLanes + lane) * kChunk;
+  for (int j = 0; j < HELD; ++j) {
+    const uint32_t c = (j * kLanes + lane) * kChunk;
+    mend8<FULL>(wx[j], res, c, cols);
+    if (has_block) mend8<FULL>(wb[j], block, c, cols);
+  }
+
+  // (mean, 1 / deviation) from values of the row; columns beyond it hold 0
+  auto stats = [&](auto value, int kind, float eps, float* mean, float* rstd) {
+    float m = 0.f;
+    if (kind == ZERO_NORM_LAYER) {
+      float s[1] = {0.f};
+#pragma unroll
+      for (int j = 0; j < HELD; ++j) {
+        float x[8];
+        value(j, x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[0] += x[i];
+      }
+      row_sums<WAVES>(s, red, turn, WAVES);
+      m = s[0] * inv_n;
+    }
+    float q[1] = {0.f};
+#pragma unroll
+    for (int j = 0; j < HELD; ++j) {
+      const uint32_t c = (j * kLanes + lane) * kChunk;
+      float x[8];
+      value(j, x);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float d = FULL || c + i < cols ? x[i] - m : 0.f;
+        q[0] += d * d;
+      }
+    }
+    row_sums<WAVES>(q, red, turn, WAVES);
+    *mean = m;
+    *rstd = 1.0f / sqrtf(q[0] * inv_n + eps);
+  };
+  auto row_of = [&](const uint16_t* p, uint32_t c, float absent, float (&x)[8]) {
+    if (p) {
+      unpack8<T>(load8_row<FULL>(p, c, cols), x);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = absent;
+    }
+  };
+
+  float m2 = 0.f, r2 = 1.f, m1 = 0.f, r1 = 1.f;
+  if (a.post.kind != ZERO_NORM_NONE)
+    stats([&](int j, float (&x)[8]) { forget(wb[j]); unpack8<T>(wb[j], x); }, a.post.kind, a.post.eps, &m2, &r2);
+  if (a.c_block.codes) {
+#pragma unroll
+    for (int j = 0; j < HELD; ++j) emit<T>(a.c_block, row, j * kLanes + lane, cols, wb[j]);
+  }
+  float x[HELD][8];   // h'
+#pragma unroll
+  for (int j = 0; j < HELD; ++j) {
+    forget(wb[j]);
+    unpack8<T>(wx[j], x[j]);
+    if (!has_block) continue;
+    const uint32_t c = (j * kLanes + lane) * kChunk;
+    float b[8], w[8], bias[8], g[8];
+    unpack8<T>(wb[j], b);
+    row_of(a.post.w.p, c, 1.f, w);
+    row_of(a.post.b.p, c, 0.f, bias);
+    row_of(a.gate.p ? gate : nullptr, c, 1.f, g);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float d = col + i < cols ? x[j][i] - m : 0.f;
-      q[0] += d * d;
+      const float o = (b[i] - m2) * r2 * w[i] + bias[i];
+      x[j][i] = FULL || c + i < cols ? x[j][i] + a.scale * (g[i] * o) : 0.f;
     }
   }
-  row_sums<W>(q, red, turn);
-  *mean = m;
-  *rstd = 1.0f / sqrtf(q[0] * inv_n + eps);
-}
-
-template <typename T, int W>
-__global__ __launch_bounds__(Shape<W>::kThreads) void block_norm_kernel(BlockNormLaunch a) {
-  using S = Shape<W>;
-  __shared__ float red[2 * S::kThreads / 64];
-  int turn = 0;
-  const uint32_t lane = threadIdx.x % S::kLanes;
-  const uint32_t group = threadIdx.x / S::kLanes;
-  const float inv_n = 1.0f / static_cast<float>(a.cols);
-  // every group of a workgroup makes the same number of turns, so the barriers
-  // of row_sums meet; a group without a row computes on zeros and stores nothing
-  for (uint64_t base = static_cast<uint64_t>(blockIdx.x) * S::kGroups; base < a.rows;
-       base += static_cast<uint64_t>(gridDim.x) * S::kGroups) {
-    const uint64_t row = base + group;
-    const bool live = row < a.rows;
-    float x[kHeld][8];   // h, then h'
-    float b[kHeld][8];
-    float st[4] = {0.f, 1.f, 0.f, 1.f};
+  if (a.out.p) {
 #pragma unroll
-    for (int j = 0; j < kHeld; ++j) {
-      const uint32_t chunk = j * S::kLanes + lane;
-      u32x4 wx = {0, 0, 0, 0}, wb = {0, 0, 0, 0};
-      if (live && chunk * kChunk < a.cols) {
-        wx = load8(a.res.p + row * a.res.stride, chunk * kChunk, a.cols);
-        if (a.block.p)
-          wb = load8(a.block.p + row * a.block.stride, chunk * kChunk, a.cols);
-      }
-      unpack8<T>(wx, x[j]);
-      unpack8<T>(wb, b[j]);
-      if (a.c_block.codes) emit<T>(a.c_block, row, chunk, a.cols, live, wb);
+    for (int j = 0; j < HELD; ++j)
+      store8_row<FULL>(a.out.p + row * a.out.stride, (j * kLanes + lane) * kChunk, cols,
+                       pack8<T>(x[j]));
+  }
+  if (a.c_out.codes) {
+#pragma unroll
+    for (int j = 0; j < HELD; ++j)
+      emit<T>(a.c_out, row, j * kLanes + lane, cols, pack8<T>(x[j]));
+  }
+  if (a.pre.kind != ZERO_NORM_NONE) {
+    // from h' before its rounding to 16 bits: z is then rounded once
+    stats([&](int j, float (&v)[8]) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = x[j][i];
+    }, a.pre.kind, a.pre.eps, &m1, &r1);
+#pragma unroll
+    for (int j = 0; j < HELD; ++j) {
+      const uint32_t c = (j * kLanes + lane) * kChunk;
+      float w[8], bias[8];
+      row_of(a.pre.w.p, c, 1.f, w);
+      row_of(a.pre.b.p, c, 0.f, bias);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        x[j][i] = FULL || c + i < cols ? (x[j][i] - m1) * r1 * w[i] + bias[i] : 0.f;
+      store8_row<FULL>(a.z.p + row * a.z.stride, c, cols, pack8<T>(x[j]));
     }
-    if (a.block.p) {
-      if (a.post.kind != ZERO_NORM_NONE)
-        row_stats<W>(b, a.post.kind, a.post.eps, a.cols, inv_n, lane, red, turn, &st[0], &st[1]);
+    if (a.c_z.codes) {
 #pragma unroll
-      for (int j = 0; j < kHeld; ++j) {
-        const uint32_t col = (j * S::kLanes + lane) * kChunk;
-        float w[8], c[8], g[8];
-        row_of<T>(a.post.w, col, a.cols, 1.f, w);
-        row_of<T>(a.post.b, col, a.cols, 0.f, c);
-        Rows gate = a.gate;
-        if (gate.p && live) gate.p += row * gate.stride;
-        row_of<T>(gate, col, a.cols, 1.f, g);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float o = (b[j][i] - st[0]) * st[1] * w[i] + c[i];
-          x[j][i] = col + i < a.cols ? x[j][i] + a.scale * (g[i] * o) : 0.f;
-        }
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < kHeld; ++j) {
-      const uint32_t chunk = j * S::kLanes + lane;
-      const u32x4 w = pack8<T>(x[j]);
-      if (a.out.p && live)
-        store8(a.out.p + row * a.out.stride, chunk * kChunk, a.cols, w);
-      if (a.c_out.codes) emit<T>(a.c_out, row, chunk, a.cols, live, w);
-    }
-    if (a.pre.kind != ZERO_NORM_NONE) {
-      // from h' before its rounding to 16 bits: z is then rounded once
-      row_stats<W>(x, a.pre.kind, a.pre.eps, a.cols, inv_n, lane, red, turn, &st[2], &st[3]);
-#pragma unroll
-      for (int j = 0; j < kHeld; ++j) {
-        const uint32_t chunk = j * S::kLanes + lane;
-        float w[8], c[8], z[8];
-        row_of<T>(a.pre.w, chunk * kChunk, a.cols, 1.f, w);
-        row_of<T>(a.pre.b, chunk * kChunk, a.cols, 0.f, c);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          z[i] = chunk * kChunk + i < a.cols ? (x[j][i] - st[2]) * st[3] * w[i] + c[i] : 0.f;
-        const u32x4 wz = pack8<T>(z);
-        if (live) store8(a.z.p + row * a.z.stride, chunk * kChunk, a.cols, wz);
-        if (a.c_z.codes) emit<T>(a.c_z, row, chunk, a.cols, live, wz);
-      }
-    }
-    if (live && lane == 0 && a.stats) {
-      float* p = a.stats + row * 4;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) p[i] = st[i];
+      for (int j = 0; j < HELD; ++j)
+        emit<T>(a.c_z, row, j * kLanes + lane, cols, pack8<T>(x[j]));
     }
   }
+  if (lane == 0 && a.stats)
+    *reinterpret_cast<f32x4*>(a.stats + row * 4) = f32x4{m2, r2, m1, r1};
 }
 
 // ------------------------------------------------------------ backward
 
-// Row streams that keep partial sums of the parameter gradients, at most.
-constexpr uint64_t kStreams = 512;
-
 uint64_t padded(uint64_t cols) { return (cols + kChunk - 1) / kChunk * kChunk; }
 
-// The gradient through one norm: q the gradient of the normalised value, xn that
-// value, sums {sum q xn, sum q} over the row.
-__device__ __forceinline__ float back(float q, float xn, float rstd, float mean_qx, float mean_q) {
-  return rstd * (q - xn * mean_qx - mean_q);
+// Chunks a thread holds, and waves of a row (at most 8).
+int grad_held(uint64_t cols) { return cols <= 8 * 64 * 2 * kChunk ? 2 : 4; }
+
+int grad_waves(uint64_t cols) {
+  const uint64_t per = 64 * grad_held(cols) * kChunk;
+  return static_cast<int>((cols + per - 1) / per);
 }
 
-// SETS: 2 -- the norms' weights; 3 -- and a gate per channel; 5 -- and biases.
-template <typename T, int W, int SETS>
-__global__ __launch_bounds__(Shape<W>::kThreads) void block_norm_grad_kernel(
-    BlockNormGradLaunch a, uint64_t streams, uint64_t pad) {
-  using S = Shape<W>;
-  __shared__ float red[2 * 2 * S::kThreads / 64];
-  int turn = 0;
-  const uint32_t lane = threadIdx.x % S::kLanes;
-  const uint32_t group = threadIdx.x / S::kLanes;
-  const float inv_n = 1.0f / static_cast<float>(a.cols);
-  const bool pre = a.pre.kind != ZERO_NORM_NONE;
-  const bool block = a.block != 0;
-  const float layer1 = a.pre.kind == ZERO_NORM_LAYER ? inv_n : 0.f;
-  const float layer2 = a.post.kind == ZERO_NORM_LAYER ? inv_n : 0.f;
-  float sum[SETS][kHeld][8];
-#pragma unroll
-  for (int s = 0; s < SETS; ++s)
-#pragma unroll
-    for (int j = 0; j < kHeld; ++j)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sum[s][j][i] = 0.f;
+// Rows that are worked on at once, at most (eight waves on each of 256 compute
+// units); each keeps partial sums of the parameters' gradients.
+uint64_t grad_streams(uint64_t rows, uint64_t cols) {
+  const uint64_t most = 2048 / grad_waves(cols);
+  return rows < most ? rows : most;
+}
 
-  for (uint64_t base = static_cast<uint64_t>(blockIdx.x) * S::kGroups; base < a.rows;
-       base += static_cast<uint64_t>(gridDim.x) * S::kGroups) {
-    const uint64_t row = base + group;
-    const bool live = row < a.rows;
-    float st[4] = {0.f, 1.f, 0.f, 1.f};
-    if (live && a.stats) {
-      const f32x4 v = *reinterpret_cast<const f32x4*>(a.stats + row * 4);
+// Everything of a row that a thread loads.
+template <int HELD, bool FULL>
+struct GradRow {
+  u32x4 d[HELD], z[HELD], g[HELD];
+  u32x2 out[HELD], block[HELD];
+  uint32_t s_out[HELD], s_block[HELD];
+  f32x4 st;
+
+  __device__ __forceinline__ void clear() {   // what is absent stays 0
 #pragma unroll
-      for (int i = 0; i < 4; ++i) st[i] = v[i];
+    for (int j = 0; j < HELD; ++j) {
+      d[j] = z[j] = g[j] = u32x4{0, 0, 0, 0};
+      out[j] = block[j] = u32x2{0, 0};
+      s_out[j] = s_block[j] = 0;
     }
-    float d[kHeld][8];   // dh', then the whole gradient of h'
+  }
+
+  __device__ __forceinline__ void load(const BlockNormGradLaunch& a, uint64_t row, uint32_t lanes,
+                                       bool token_gate) {
+    const uint16_t* pd = a.dout.p + row * a.dout.stride;
+    const uint16_t* pz = a.dz.p + row * a.dz.stride;
+    const uint16_t* pg = a.gate.p + row * a.gate.stride;
+    const uint8_t* po = a.c_out.codes + row * a.c_out.code_stride;
+    const uint8_t* pb = a.c_block.codes + row * a.c_block.code_stride;
+    const uint8_t* so = a.c_out.scales + row * a.c_out.scale_stride;
+    const uint8_t* sb = a.c_block.scales + row * a.c_block.scale_stride;
+    st = f32x4{0.f, 1.f, 0.f, 1.f};
+    if (a.stats) st = *reinterpret_cast<const f32x4*>(a.stats + row * 4);
 #pragma unroll
-    for (int j = 0; j < kHeld; ++j) {
-      u32x4 w = {0, 0, 0, 0};
-      if (live && a.dout.p && (j * S::kLanes + lane) * kChunk < a.cols)
-        w = load8(a.dout.p + row * a.dout.stride, (j * S::kLanes + lane) * kChunk, a.cols);
-      unpack8<T>(w, d[j]);
-    }
-    if (pre) {
-      float q[kHeld][8], xn[kHeld][8];
-      float t[2] = {0.f, 0.f};
-#pragma unroll
-      for (int j = 0; j < kHeld; ++j) {
-        const uint32_t chunk = j * S::kLanes + lane, col = chunk * kChunk;
-        u32x4 w = {0, 0, 0, 0};
-        u32x2 c = {0, 0};
-        uint32_t sb = 0;
-        if (live && col < a.cols) {
-          w = load8(a.dz.p + row * a.dz.stride, col, a.cols);
-          c = load_codes(a.c_out.codes + row * a.c_out.code_stride, col, a.cols);
-          sb = a.c_out.scales[row * a.c_out.scale_stride + chunk / kQuad];
-        }
-        unpack8<T>(w, q[j]);
-        if (a.c_out.format == kInt8) decode8<kInt8>(c, scale_of(sb), xn[j]);
-        else decode8<kE4m3>(c, scale_of(sb), xn[j]);
-        float wt[8];
-        row_of<T>(a.pre.w, col, a.cols, 1.f, wt);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const bool in = live && col + i < a.cols;
-          xn[j][i] = in ? (xn[j][i] - st[2]) * st[3] : 0.f;
-          sum[kDwPre][j][i] += q[j][i] * xn[j][i];
-          if constexpr (SETS == 5) sum[kDbPre][j][i] += q[j][i];
-          q[j][i] *= wt[i];
-          t[0] += q[j][i] * xn[j][i];
-          t[1] += q[j][i];
-        }
+    for (int j = 0; j < HELD; ++j) {
+      const uint32_t chunk = j * lanes + threadIdx.x, c = chunk * kChunk;
+      const uint32_t b = FULL || c < a.cols ? chunk / kQuad : 0;
+      if (a.dout.p) d[j] = load8_early<FULL>(pd, c, a.cols);
+      if (a.c_out.codes) {
+        z[j] = load8_early<FULL>(pz, c, a.cols);
+        out[j] = load_codes_early<FULL>(po, c, a.cols);
+        s_out[j] = so[b];
       }
-      row_sums<W>(t, red, turn);
-#pragma unroll
-      for (int j = 0; j < kHeld; ++j)
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          d[j][i] += back(q[j][i], xn[j][i], st[3], t[0] * inv_n, t[1] * layer1);
-    }
-    if (a.dres.p && live) {
-#pragma unroll
-      for (int j = 0; j < kHeld; ++j)
-        store8(a.dres.p + row * a.dres.stride, (j * S::kLanes + lane) * kChunk, a.cols, pack8<T>(d[j]));
-    }
-    if (block) {
-      float v[kHeld][8], xn[kHeld][8];
-      float t[2] = {0.f, 0.f};
-#pragma unroll
-      for (int j = 0; j < kHeld; ++j) {
-        const uint32_t chunk = j * S::kLanes + lane, col = chunk * kChunk;
-        u32x2 c = {0, 0};
-        uint32_t sb = 0;
-        if (live && col < a.cols && a.c_block.codes) {
-          c = load_codes(a.c_block.codes + row * a.c_block.code_stride, col, a.cols);
-          sb = a.c_block.scales[row * a.c_block.scale_stride + chunk / kQuad];
-        }
-        if (a.c_block.format == kInt8) decode8<kInt8>(c, scale_of(sb), xn[j]);
-        else decode8<kE4m3>(c, scale_of(sb), xn[j]);
-        float wt[8], bt[8], g[8], dg[8];
-        row_of<T>(a.post.w, col, a.cols, 1.f, wt);
-        row_of<T>(a.post.b, col, a.cols, 0.f, bt);
-        Rows gate = a.gate;
-        if (gate.p && live) gate.p += row * gate.stride;
-        row_of<T>(gate, col, a.cols, 1.f, g);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const bool in = live && col + i < a.cols;
-          xn[j][i] = in ? (xn[j][i] - st[0]) * st[1] : 0.f;
-          const float u = in ? a.scale * d[j][i] : 0.f;
-          dg[i] = u * (xn[j][i] * wt[i] + bt[i]);
-          const float p = u * g[i];
-          if constexpr (SETS == 3) sum[2][j][i] += dg[i];
-          if constexpr (SETS == 5) sum[kDgate][j][i] += dg[i];
-          if constexpr (SETS == 5) sum[kDbPost][j][i] += p;
-          sum[kDwPost][j][i] += p * xn[j][i];
-          v[j][i] = p * wt[i];
-          t[0] += v[j][i] * xn[j][i];
-          t[1] += v[j][i];
-        }
-        if (a.dgate.p && live)
-          store8(a.dgate.p + row * a.dgate.stride, col, a.cols, pack8<T>(dg));
+      if (a.c_block.codes) {
+        block[j] = load_codes_early<FULL>(pb, c, a.cols);
+        s_block[j] = sb[b];
       }
-      if (a.dblock.p) {
-        if (a.post.kind != ZERO_NORM_NONE) {
-          row_sums<W>(t, red, turn);
+      if (token_gate) g[j] = load8_early<FULL>(pg, c, a.cols);
+    }
+  }
+
+  // Where the loads are waited for.
+  __device__ __forceinline__ void settle(const BlockNormGradLaunch& a, uint64_t row,
+                                         uint32_t lanes, bool token_gate) {
+    forget(st);
 #pragma unroll
-          for (int j = 0; j < kHeld; ++j)
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              v[j][i] = back(v[j][i], xn[j][i], st[1], t[0] * inv_n, t[1] * layer2);
+    for (int j = 0; j < HELD; ++j) {
+      forget(d[j]);
+      forget(z[j]);
+      forget(out[j]);
+      forget(block[j]);
+      forget(s_out[j]);
+      forget(s_block[j]);
+      if (token_gate) forget(g[j]);
+      if constexpr (!FULL) {
+        const uint32_t c = (j * lanes + threadIdx.x) * kChunk, cols = a.cols;
+        if (c + kChunk <= cols) continue;
+        if (a.dout.p) mend8<FULL>(d[j], a.dout.p + row * a.dout.stride, c, cols);
+        if (a.c_out.codes) {
+          mend8<FULL>(z[j], a.dz.p + row * a.dz.stride, c, cols);
+          mend_codes<FULL>(out[j], a.c_out.codes + row * a.c_out.code_stride, c, cols);
         }
-        if (live) {
-#pragma unroll
-          for (int j = 0; j < kHeld; ++j)
-            store8(a.dblock.p + row * a.dblock.stride, (j * S::kLanes + lane) * kChunk, a.cols, pack8<T>(v[j]));
-        }
+        if (a.c_block.codes)
+          mend_codes<FULL>(block[j], a.c_block.codes + row * a.c_block.code_stride, c, cols);
+        if (token_gate) mend8<FULL>(g[j], a.gate.p + row * a.gate.stride, c, cols);
       }
     }
   }
-  if (!a.partial) return;
-  const uint64_t stream = static_cast<uint64_t>(blockIdx.x) * S::kGroups + group;
+};
+
+constexpr int kGradThreads = 512;  // of a workgroup, at most
+
+// One workgroup takes rows blockIdx.x, blockIdx.x + gridDim.x, ..., loading one
+// while it works on the one before, and keeps the parameters' gradients of its rows
+// in registers; SETS: 3 -- those of the weights and of a gate a channel; 5 -- and of
+// biases.  Two chunks a thread leave room for that.
+//
+// Both norms' row sums are taken together, behind one barrier.  The gradient of
+// post's input needs sums of v = y D and v x2 (y = s g w_post), where
+//   D = e - r1 a x1 - r1 m,  e = dout + r1 q,  a = mean(q x1),  m = [mean q]
+// is known only after pre's; but it is linear in a and m, so sums of y e, y x1, y
+// and their products with x2 give it afterwards.
+//
+// Up to 8192 columns a thread holds two chunks, and the values of the first half
+// stay in registers for the second; wider rows take four, load nothing ahead, read
+// the norms' weights from the caches and make those values again.  The biases' sums
+// lie in shared memory, each thread's in places of its own: with them in registers
+// the kernel ran out and took 2.5 times as long.
+template <typename T, int FMT, int HELD, int SETS, bool FULL>
+__global__ __launch_bounds__(kGradThreads, 2) void block_norm_grad_kernel(BlockNormGradLaunch a,
+                                                                          uint64_t pad) {
+  constexpr bool kAhead = HELD == 2, kKeep = kAhead;
+  constexpr int kMaxWaves = kGradThreads / 64;
+  constexpr int kRowSums = 8;
+  __shared__ float red[2 * kMaxWaves * kRowSums];
+  int turn = 0;
+  const uint32_t lanes = blockDim.x, waves = lanes / 64, cols = a.cols;
+  const float inv_n = 1.0f / static_cast<float>(cols);
+  const bool pre = a.c_out.codes != nullptr;
+  const bool post = a.post.kind != ZERO_NORM_NONE;
+  const bool layer1 = a.pre.kind == ZERO_NORM_LAYER, layer2 = a.post.kind == ZERO_NORM_LAYER;
+  const bool token_gate = a.gate.p && a.gate.stride != 0;
+  // The norms' rows, the same for every token; 1 where absent.  Columns past the
+  // row's end need no further care: dout, dz and w_post are 0 there, which keeps them
+  // out of the row sums, and nothing is stored there.
+  constexpr uint32_t kOne = T::kType == kF16 ? 0x3C00u : 0x3F80u;
+  u32x4 w1[HELD], w2[HELD], b2[HELD], gc[HELD];
+  auto load_rows = [&](int j) {
+    uint32_t c = (j * lanes + threadIdx.x) * kChunk;
+    if constexpr (!kAhead) forget(c);   // a load each time, not registers in between
+    u32x4 ones;
 #pragma unroll
-  for (int s = 0; s < SETS; ++s)
+    for (int i = 0; i < 4; ++i)
+      ones[i] = (FULL || c + 2 * i < cols ? kOne : 0u) |
+                (FULL || c + 2 * i + 1 < cols ? kOne : 0u) << 16;
+    w1[j] = w2[j] = gc[j] = ones;
+    b2[j] = u32x4{0, 0, 0, 0};
+    if (a.pre.w.p) w1[j] = load8_row<FULL>(a.pre.w.p, c, cols);
+    if (a.post.w.p) w2[j] = load8_row<FULL>(a.post.w.p, c, cols);
+    if (a.post.b.p) b2[j] = load8_row<FULL>(a.post.b.p, c, cols);
+    if (a.gate.p && !token_gate) gc[j] = load8_row<FULL>(a.gate.p, c, cols);
+  };
+  if constexpr (kAhead) {
 #pragma unroll
-    for (int j = 0; j < kHeld; ++j) {
-      const uint64_t col = static_cast<uint64_t>(j * S::kLanes + lane) * kChunk;
-      if (col >= pad) continue;
-      float* p = a.partial + (static_cast<uint64_t>(s) * streams + stream) * pad + col;
-      *reinterpret_cast<f32x4*>(p) =
-          f32x4{sum[s][j][0], sum[s][j][1], sum[s][j][2], sum[s][j][3]};
-      *reinterpret_cast<f32x4*>(p + 4) =
-          f32x4{sum[s][j][4], sum[s][j][5], sum[s][j][6], sum[s][j][7]};
+    for (int j = 0; j < HELD; ++j) load_rows(j);
+  }
+  float sum[3][HELD][8];   // of the weights and the gate
+  constexpr int kGate = 2;
+#pragma unroll
+  for (int s = 0; s < 3; ++s)
+#pragma unroll
+    for (int j = 0; j < HELD; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[s][j][i] = 0.f;
+  extern __shared__ f32x4 bias_sums[];   // SETS == 5: 4 HELD of each thread
+  auto bias_at = [&](int set, int j, int half) -> f32x4& {
+    return bias_sums[((set * HELD + j) * 2 + half) * lanes + threadIdx.x];
+  };
+  if constexpr (SETS == 5) {
+#pragma unroll
+    for (int q = 0; q < 4 * HELD; ++q)
+      bias_at(q / (2 * HELD), q / 2 % HELD, q % 2) = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+  auto add_bias = [&](int set, int j, const float (&v)[8]) {
+    if constexpr (SETS == 5) {
+      bias_at(set, j, 0) += f32x4{v[0], v[1], v[2], v[3]};
+      bias_at(set, j, 1) += f32x4{v[4], v[5], v[6], v[7]};
     }
+  };
+
+  GradRow<HELD, FULL> next;
+  next.clear();
+  uint64_t row = blockIdx.x;
+  if (kAhead && row < a.rows) next.load(a, row, lanes, token_gate);
+  for (; row < a.rows; row += gridDim.x) {
+    GradRow<HELD, FULL> r;
+    if constexpr (kAhead) {
+      r = next;
+#pragma unroll
+      for (int j = 0; j < HELD; ++j) {
+        forget(w1[j]);
+        forget(w2[j]);
+        forget(b2[j]);
+        forget(gc[j]);
+      }
+    } else {
+      r.clear();
+      r.load(a, row, lanes, token_gate);
+    }
+    r.settle(a, row, lanes, token_gate);
+    if (kAhead && row + gridDim.x < a.rows) next.load(a, row + gridDim.x, lanes, token_gate);
+    const float m2 = r.st[0], r2 = r.st[1], m1 = r.st[2], r1 = r.st[3];
+
+    float x1[HELD][8], x2[HELD][8], e[HELD][8];
+    // x1, x2, e and the gradient z of the normalised pre value's input
+    auto front = [&](int j, float (&z)[8], float (&q)[8]) {
+      float k[8], w[8], d[8];
+      unpack8<T>(r.z[j], z);
+      unpack8<T>(w1[j], w);
+      unpack8<T>(r.d[j], d);
+      decode8<FMT>(r.out[j], scale_of(r.s_out[j]), k);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        x1[j][i] = (k[i] - m1) * r1;
+        q[i] = z[i] * w[i];
+        e[j][i] = d[i] + r1 * q[i];
+      }
+      decode8<FMT>(r.block[j], scale_of(r.s_block[j]), k);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x2[j][i] = (k[i] - m2) * r2;
+    };
+    auto gates = [&](int j, float (&g)[8]) { unpack8<T>(token_gate ? r.g[j] : gc[j], g); };
+
+    // sums: q x1, q; y e x2, y x1 x2, y x2; y e, y x1, y
+    float t[kRowSums];
+#pragma unroll
+    for (int i = 0; i < kRowSums; ++i) t[i] = 0.f;
+#pragma unroll
+    for (int j = 0; j < HELD; ++j) {
+      float z[8], q[8], g[8], w[8];
+      if constexpr (!kAhead) load_rows(j);
+      front(j, z, q);
+      gates(j, g);
+      unpack8<T>(w2[j], w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        sum[kDwPre][j][i] += z[i] * x1[j][i];
+        t[0] += q[i] * x1[j][i];
+        const float y = a.scale * g[i] * w[i], yx = y * x2[j][i];
+        t[2] += yx * e[j][i];
+        t[3] += yx * x1[j][i];
+        if constexpr (SETS == 5) {
+          t[1] += q[i];
+          t[4] += yx;
+          t[5] += y * e[j][i];
+          t[6] += y * x1[j][i];
+          t[7] += y;
+        }
+      }
+      add_bias(0, j, z);
+      // one chunk at a time: side by side they need more registers than there are
+      if constexpr (HELD > 2) __builtin_amdgcn_sched_barrier(0);
+    }
+    float mean_qx, mean_q = 0.f, mean_vx, mean_v = 0.f;
+    if constexpr (SETS == 5) {
+      row_sums<kMaxWaves>(t, red, turn, waves);
+      mean_qx = t[0] * inv_n;
+      mean_q = layer1 ? t[1] * inv_n : 0.f;
+      mean_vx = (t[2] - r1 * (mean_qx * t[3] + mean_q * t[4])) * inv_n;
+      mean_v = (t[5] - r1 * (mean_qx * t[6] + mean_q * t[7])) * inv_n;
+    } else {
+      float u[3] = {t[0], t[2], t[3]};
+      row_sums<kMaxWaves>(u, red, turn, waves);
+      mean_qx = u[0] * inv_n;
+      mean_vx = (u[1] - r1 * mean_qx * u[2]) * inv_n;
+    }
+    if (!pre) mean_qx = mean_q = 0.f;
+    if (!post) mean_vx = 0.f;
+    if (!layer2) mean_v = 0.f;
+
+#pragma unroll
+    for (int j = 0; j < HELD; ++j) {
+      const uint32_t c = (j * lanes + threadIdx.x) * kChunk;
+      forget(w2[j]);
+      forget(gc[j]);
+      forget(r.g[j]);
+      if constexpr (!kKeep) {
+        forget(r.z[j]);
+        forget(r.d[j]);
+        forget(r.out[j]);
+        forget(r.block[j]);
+        forget(w1[j]);
+        if constexpr (!kAhead) load_rows(j);
+        float z[8], q[8];
+        front(j, z, q);
+      }
+      float d[8], dg[8], db[8], p[8], g[8], w[8], bias[8];
+      gates(j, g);
+      unpack8<T>(w2[j], w);
+      unpack8<T>(b2[j], bias);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        d[i] = e[j][i] - r1 * (x1[j][i] * mean_qx + mean_q);
+        const float u = a.scale * d[i];
+        p[i] = u * g[i];
+        dg[i] = u * (x2[j][i] * w[i] + bias[i]);
+        sum[kGate][j][i] += dg[i];
+        sum[kDwPost][j][i] += p[i] * x2[j][i];
+        db[i] = r2 * (p[i] * w[i] - x2[j][i] * mean_vx - mean_v);
+      }
+      add_bias(1, j, p);
+      if (a.dres.p) store8_row<FULL>(a.dres.p + row * a.dres.stride, c, cols, pack8<T>(d));
+      if (a.dblock.p) store8_row<FULL>(a.dblock.p + row * a.dblock.stride, c, cols, pack8<T>(db));
+      if (a.dgate.p) store8_row<FULL>(a.dgate.p + row * a.dgate.stride, c, cols, pack8<T>(dg));
+      if constexpr (HELD > 2) __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+  if (!a.partial) return;
+  constexpr int kSetOf[kSums] = {kDwPre, kDwPost, kDgate, kDbPre, kDbPost};
+#pragma unroll
+  for (int s = 0; s < SETS; ++s) {
+    if (!a.sums[kSetOf[s]]) continue;
+#pragma unroll
+    for (int j = 0; j < HELD; ++j) {
+      const uint64_t col = static_cast<uint64_t>(j * lanes + threadIdx.x) * kChunk;
+      if (col >= pad) continue;
+      f32x4 u, v;
+      if (s < 3) {
+        const float (&x)[8] = sum[s < 3 ? s : 0][j];
+        u = f32x4{x[0], x[1], x[2], x[3]};
+        v = f32x4{x[4], x[5], x[6], x[7]};
+      } else {
+        u = bias_at(s - 3, j, 0);
+        v = bias_at(s - 3, j, 1);
+      }
+      float* p = a.partial +
+                 (static_cast<uint64_t>(kSetOf[s]) * gridDim.x + blockIdx.x) * pad + col;
+      *reinterpret_cast<f32x4*>(p) = u;
+      *reinterpret_cast<f32x4*>(p + 4) = v;
+    }
+  }
 }
 
 // Joins the streams' partial sums in a fixed order: 64 columns a workgroup, 16
@@ -363,7 +527,6 @@ struct JoinArgs {
   const float* partial;
   uint64_t streams, pad;
   uint32_t cols;
-  int n;
   int set[kSums];
   void* out[kSums];
   int dtype, accumulate;
@@ -377,8 +540,10 @@ __global__ __launch_bounds__(64 * kJoinWaves) void join_sums_kernel(JoinArgs a) 
   const uint32_t col = blockIdx.x * 64 + lane;
   const float* p = a.partial + static_cast<uint64_t>(a.set[blockIdx.y]) * a.streams * a.pad + col;
   float s = 0.f;
-  if (col < a.cols)
+  if (col < a.cols) {
+#pragma unroll 8
     for (uint64_t k = wave; k < a.streams; k += kJoinWaves) s += p[k * a.pad];
+  }
   part[wave][lane] = s;
   __syncthreads();
   if (wave != 0 || col >= a.cols) return;
@@ -400,64 +565,74 @@ __global__ __launch_bounds__(64 * kJoinWaves) void join_sums_kernel(JoinArgs a) 
   }
 }
 
-// Waves of a row: the least power of two whose threads hold it.
-int waves_of(uint64_t cols) {
-  int w = 1;
-  while (static_cast<uint64_t>(w) * 64 * kHeld * kChunk < cols) w *= 2;
-  return w;
+// ------------------------------------------------------------ launches
+
+template <typename T, int WAVES, int HELD>
+void forward_rows(const BlockNormLaunch& a, hipStream_t stream) {
+  constexpr uint64_t kMost = 1ull << 30;   // rows of a launch
+  const bool full = a.cols == 64u * WAVES * HELD * kChunk;
+  for (uint64_t row0 = 0; row0 < a.rows; row0 += kMost) {
+    const uint64_t left = a.rows - row0;
+    const uint32_t wgs = static_cast<uint32_t>(left < kMost ? left : kMost);
+    if (full) block_norm_kernel<T, WAVES, HELD, true><<<wgs, 64 * WAVES, 0, stream>>>(a, row0);
+    else block_norm_kernel<T, WAVES, HELD, false><<<wgs, 64 * WAVES, 0, stream>>>(a, row0);
+  }
 }
-
-uint64_t groups_of(int waves) { return waves < 4 ? 4 / waves : 1; }
-
-constexpr uint64_t kForwardWgs = 2048;  // eight workgroups for each of 256 compute units
 
 template <typename T>
 void forward(const BlockNormLaunch& a, hipStream_t stream) {
-  const int w = waves_of(a.cols);
-  const uint64_t need = (a.rows + groups_of(w) - 1) / groups_of(w);
-  const uint32_t wgs = static_cast<uint32_t>(need < kForwardWgs ? need : kForwardWgs);
-  switch (w) {
-    case 1: block_norm_kernel<T, 1><<<wgs, Shape<1>::kThreads, 0, stream>>>(a); break;
-    case 2: block_norm_kernel<T, 2><<<wgs, Shape<2>::kThreads, 0, stream>>>(a); break;
-    case 4: block_norm_kernel<T, 4><<<wgs, Shape<4>::kThreads, 0, stream>>>(a); break;
-    case 8: block_norm_kernel<T, 8><<<wgs, Shape<8>::kThreads, 0, stream>>>(a); break;
-    default: block_norm_kernel<T, 16><<<wgs, Shape<16>::kThreads, 0, stream>>>(a); break;
+  // the least waves whose threads hold the row in up to eight chunks, and the least
+  // chunks: 5120 columns in 2 x 5 take 160 us where 2 x 8 takes 335
+  const uint32_t per = 64 * kChunk;
+  const uint32_t waves = a.cols <= 8 * per ? 1 : a.cols <= 16 * per ? 2 : 4;
+  const uint32_t held = (a.cols + waves * per - 1) / (waves * per);
+  if (waves == 1) {
+    if (held <= 1) forward_rows<T, 1, 1>(a, stream);
+    else if (held <= 2) forward_rows<T, 1, 2>(a, stream);
+    else if (held <= 4) forward_rows<T, 1, 4>(a, stream);
+    else if (held <= 6) forward_rows<T, 1, 6>(a, stream);
+    else forward_rows<T, 1, 8>(a, stream);
+  } else if (waves == 2) {
+    if (held <= 5) forward_rows<T, 2, 5>(a, stream);
+    else if (held <= 6) forward_rows<T, 2, 6>(a, stream);
+    else forward_rows<T, 2, 8>(a, stream);
+  } else {
+    if (held <= 5) forward_rows<T, 4, 5>(a, stream);
+    else if (held <= 6) forward_rows<T, 4, 6>(a, stream);
+    else forward_rows<T, 4, 8>(a, stream);
   }
 }
 
-template <typename T, int SETS>
-void backward(const BlockNormGradLaunch& a, uint32_t wgs, uint64_t streams, hipStream_t stream) {
+template <typename T, int FMT>
+void backward(const BlockNormGradLaunch& a, int sets, uint32_t wgs, hipStream_t stream) {
   const uint64_t pad = padded(a.cols);
-  switch (waves_of(a.cols)) {
-    case 1:
-      block_norm_grad_kernel<T, 1, SETS><<<wgs, Shape<1>::kThreads, 0, stream>>>(a, streams, pad);
-      break;
-    case 2:
-      block_norm_grad_kernel<T, 2, SETS><<<wgs, Shape<2>::kThreads, 0, stream>>>(a, streams, pad);
-      break;
-    case 4:
-      block_norm_grad_kernel<T, 4, SETS><<<wgs, Shape<4>::kThreads, 0, stream>>>(a, streams, pad);
-      break;
-    case 8:
-      block_norm_grad_kernel<T, 8, SETS><<<wgs, Shape<8>::kThreads, 0, stream>>>(a, streams, pad);
-      break;
-    default:
-      block_norm_grad_kernel<T, 16, SETS><<<wgs, Shape<16>::kThreads, 0, stream>>>(a, streams,
-                                                                                     pad);
-      break;
+  const int held = grad_held(a.cols);
+  const uint32_t threads = 64 * grad_waves(a.cols);
+  const bool full = a.cols == static_cast<uint32_t>(held) * threads * kChunk;
+  const uint32_t shared = 4 * held * threads * sizeof(f32x4);   // at most 128 KiB
+  if (held == 2) {
+    if (full && sets == 3)
+      block_norm_grad_kernel<T, FMT, 2, 3, true><<<wgs, threads, 0, stream>>>(a, pad);
+    else if (full)
+      block_norm_grad_kernel<T, FMT, 2, 5, true><<<wgs, threads, shared, stream>>>(a, pad);
+    else if (sets == 3)
+      block_norm_grad_kernel<T, FMT, 2, 3, false><<<wgs, threads, 0, stream>>>(a, pad);
+    else
+      block_norm_grad_kernel<T, FMT, 2, 5, false><<<wgs, threads, shared, stream>>>(a, pad);
+  } else {
+    if (full && sets == 3)
+      block_norm_grad_kernel<T, FMT, 4, 3, true><<<wgs, threads, 0, stream>>>(a, pad);
+    else if (sets == 3)
+      block_norm_grad_kernel<T, FMT, 4, 3, false><<<wgs, threads, 0, stream>>>(a, pad);
+    else
+      block_norm_grad_kernel<T, FMT, 4, 5, false><<<wgs, threads, shared, stream>>>(a, pad);
   }
-}
-
-uint64_t grad_wgs(uint64_t rows, uint64_t cols) {
-  const uint64_t g = groups_of(waves_of(cols)), need = (rows + g - 1) / g;
-  const uint64_t most = kStreams / g;
-  return need < most ? need : most;
 }
 
 }  // namespace
 
 uint64_t norm_grad_workspace(uint64_t rows, uint64_t cols) {
-  return grad_wgs(rows, cols) * groups_of(waves_of(cols)) * padded(cols) * kSums * sizeof(float);
+  return grad_streams(rows, cols) * padded(cols) * kSums * sizeof(float);
 }
 
 hipError_t launch_block_norm(const BlockNormLaunch& a, hipStream_t stream) {
@@ -471,18 +646,18 @@ hipError_t launch_block_norm_grad(const BlockNormGradLaunch& in, hipStream_t str
   bool any = false;
   for (void* p : a.sums) any = any || p != nullptr;
   if (!any) a.partial = nullptr;
-  const uint32_t wgs = static_cast<uint32_t>(grad_wgs(a.rows, a.cols));
-  const uint64_t streams = wgs * groups_of(waves_of(a.cols));
-  const int sets = a.sums[kDbPre] || a.sums[kDbPost] ? 5 : a.sums[kDgate] ? 3 : 2;
+  const uint32_t wgs = static_cast<uint32_t>(grad_streams(a.rows, a.cols));
+  // layer norms need the row sums of the biases' path too
+  const bool five = a.sums[kDbPre] || a.sums[kDbPost] || a.pre.kind == ZERO_NORM_LAYER ||
+                    a.post.kind == ZERO_NORM_LAYER;
+  const int sets = five ? 5 : 3;
   if (wgs) {
     if (a.dtype == kF16) {
-      if (sets == 2) backward<F16, 2>(a, wgs, streams, stream);
-      else if (sets == 3) backward<F16, 3>(a, wgs, streams, stream);
-      else backward<F16, 5>(a, wgs, streams, stream);
+      if (a.format == kInt8) backward<F16, kInt8>(a, sets, wgs, stream);
+      else backward<F16, kE4m3>(a, sets, wgs, stream);
     } else {
-      if (sets == 2) backward<Bf16, 2>(a, wgs, streams, stream);
-      else if (sets == 3) backward<Bf16, 3>(a, wgs, streams, stream);
-      else backward<Bf16, 5>(a, wgs, streams, stream);
+      if (a.format == kInt8) backward<Bf16, kInt8>(a, sets, wgs, stream);
+      else backward<Bf16, kE4m3>(a, sets, wgs, stream);
     }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -490,18 +665,18 @@ hipError_t launch_block_norm_grad(const BlockNormGradLaunch& in, hipStream_t str
   if (!any) return hipSuccess;
   JoinArgs j;
   j.partial = a.partial;
-  j.streams = streams;
+  j.streams = wgs;
   j.pad = padded(a.cols);
   j.cols = a.cols;
   j.dtype = a.grad_dtype;
   j.accumulate = a.accumulate;
-  j.n = 0;
+  int n = 0;
   for (int s = 0; s < kSums; ++s) {
     if (!a.sums[s]) continue;
-    j.set[j.n] = s == kDgate && sets == 3 ? 2 : s;
-    j.out[j.n++] = a.sums[s];
+    j.set[n] = s;
+    j.out[n++] = a.sums[s];
   }
-  join_sums_kernel<<<dim3((a.cols + 63) / 64, j.n), 64 * kJoinWaves, 0, stream>>>(j);
+  join_sums_kernel<<<dim3((a.cols + 63) / 64, n), 64 * kJoinWaves, 0, stream>>>(j);
   return hipGetLastError();
 }
 
