@@ -395,31 +395,63 @@ def gather_params(psi: int, nd: int, lo: int, length: int, shards, out, stream=N
         psi, nd, lo, length, shards.data_ptr(), shards.stride(0), out.data_ptr(), h))
 
 
+import torch  # noqa: E402  (after _load, which decides which HIP runtime is mapped)
+
 # ---------------------------------------------------------------------------
 # Activations: 8-bit checkpoints, the weight gradient from them, block norms.
 
-def _dtype_code(t) -> int:
-    import torch
-    return {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}[t.dtype]
+_F16_BF16 = (torch.float16, torch.bfloat16)
+_FLOATS = (torch.float16, torch.bfloat16, torch.float32)
+_CODE = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
 
 
-def _matrix(t, name, dtypes, rows=None, cols=None):
-    """A device matrix with unit column stride and, if given, these sizes."""
-    _dev(t, name, dtypes)
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+def _matrix(t, name, dtypes, shape=None):
+    """(address, row stride) of a device matrix with unit column stride and, if
+    given, this shape."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
+    got = t.shape
+    if len(got) != 2:
         raise ValueError(f"{name} must be a matrix with unit column stride")
-    if rows is not None and tuple(t.shape) != (rows, cols):
-        raise ValueError(f"{name} is {tuple(t.shape)}, expected {(rows, cols)}")
-
-
-def _stride(t) -> int:
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    if shape is not None and got != shape:
+        raise ValueError(f"{name} is {tuple(got)}, expected {tuple(shape)}")
+    stride, unit = t.stride()
+    if unit != 1 and got[1] > 1:
+        raise ValueError(f"{name} must be a matrix with unit column stride")
+    return t.data_ptr(), stride if got[0] > 1 else got[1]
 
 
 def _row(t, name, dtype, cols):
-    _dev(t, name, (dtype,))
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if t.dim() != 1 or t.shape[0] != cols or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous row of {cols}")
+    return t.data_ptr()
+
+
+def _call(tensors, stream, call, *args) -> None:
+    """call(*args, stream handle) with the tensors' device current (as _launch)."""
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t.get_device() != dev:
+            raise ValueError(f"tensors of one call are on {tensors[0].device} and {t.device}")
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(dev)
+    elif stream.device.index != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {tensors[0].device}")
+    else:
+        handle = stream.cuda_stream
+    if torch.cuda.current_device() == dev:
+        rc = call(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            rc = call(*args, handle)
+    if rc != ZERO_OK:
+        raise ZeroError(rc, last_error())
 
 
 class Ckpt:
@@ -428,7 +460,6 @@ class Ckpt:
     or CKPT_E4M3."""
 
     def __init__(self, codes, scales, fmt: int):
-        import torch
         if fmt not in (CKPT_INT8, CKPT_E4M3):
             raise ValueError(f"unknown checkpoint format {fmt}")
         for name, t in (("codes", codes), ("scales", scales)):
@@ -464,63 +495,53 @@ class Ckpt:
         return Ckpt(self.codes[lo:hi], self.scales[lo:hi], self.fmt)
 
     def _arg(self):
-        for name, t in (("codes", self.codes), ("scales", self.scales)):
-            if not t.is_cuda:
-                raise ValueError(f"{name} must be a device tensor")
-        a = _CkptArg()
-        a.codes, a.scales = self.codes.data_ptr(), self.scales.data_ptr()
-        a.rows, a.cols = self.codes.shape
-        a.code_stride, a.scale_stride = _stride(self.codes), _stride(self.scales)
-        a.format = self.fmt
-        return a
+        codes, scales = self.codes, self.scales
+        if not codes.is_cuda or not scales.is_cuda:
+            raise ValueError("a checkpoint's codes and scales must be device tensors")
+        rows, cols = codes.shape
+        return _CkptArg(codes.data_ptr(), scales.data_ptr(), rows, cols,
+                        codes.stride(0) if rows > 1 else cols,
+                        scales.stride(0) if rows > 1 else scales.shape[1], self.fmt)
 
 
 def ckpt_empty(rows: int, cols: int, fmt: int = CKPT_INT8, device=None) -> Ckpt:
     """Uninitialised buffers of a checkpoint, code rows on 16 bytes."""
-    import torch
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else device
     codes = torch.empty((rows, -(-cols // 16) * 16), dtype=torch.uint8, device=dev)[:, :cols]
     scales = torch.empty((rows, -(-cols // CKPT_BLOCK)), dtype=torch.uint8, device=dev)
     return Ckpt(codes, scales, fmt)
 
 
-def _workspace(nbytes, dev, stream):
-    """Workspace of one call, from the caching allocator of the call's stream."""
-    import torch
-    if nbytes == 0:
-        return None
+def _workspace(given, need, dev, stream):
+    """(address, bytes, tensor) of a call's workspace: the caller's, or one from the
+    caching allocator of the call's stream."""
+    if given is not None:
+        _dev(given, "workspace", (torch.uint8,), need)
+        if not given.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+        return given.data_ptr(), given.numel(), given
+    if need == 0:
+        return None, 0, None
     if stream is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    with torch.cuda.stream(stream):
-        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
-
-
-def _given_workspace(workspace, need, dev, stream):
-    import torch
-    if workspace is None:
-        return _workspace(need, dev, stream)
-    _dev(workspace, "workspace", (torch.uint8,), need)
-    if not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-    return workspace
+        t = torch.empty(need, dtype=torch.uint8, device=dev)
+    else:
+        with torch.cuda.stream(stream):
+            t = torch.empty(need, dtype=torch.uint8, device=dev)
+    return t.data_ptr(), need, t
 
 
 def ckpt_write(x, ckpt: Ckpt, stream=None) -> None:
     """Stores x (float16/bfloat16 [rows, cols], any row stride) in 8 bits."""
-    import torch
-    _matrix(x, "x", (torch.float16, torch.bfloat16), ckpt.rows, ckpt.cols)
-    arg = ckpt._arg()
-    _launch((x, *ckpt.tensors()), stream, lambda h: lib.zero_ckpt_write(
-        x.data_ptr(), _dtype_code(x), _stride(x), ctypes.byref(arg), h))
+    ptr, stride = _matrix(x, "x", _F16_BF16, ckpt.codes.shape)
+    _call((x, ckpt.codes, ckpt.scales), stream, lib.zero_ckpt_write, ptr, _CODE[x.dtype], stride,
+          ctypes.byref(ckpt._arg()))
 
 
 def ckpt_read(ckpt: Ckpt, out, stream=None) -> None:
     """Reads the held values into out (float16/bfloat16/float32 [rows, cols])."""
-    import torch
-    _matrix(out, "out", (torch.float16, torch.bfloat16, torch.float32), ckpt.rows, ckpt.cols)
-    arg = ckpt._arg()
-    _launch((out, *ckpt.tensors()), stream, lambda h: lib.zero_ckpt_read(
-        ctypes.byref(arg), out.data_ptr(), _dtype_code(out), _stride(out), h))
+    ptr, stride = _matrix(out, "out", _FLOATS, ckpt.codes.shape)
+    _call((out, ckpt.codes, ckpt.scales), stream, lib.zero_ckpt_read, ctypes.byref(ckpt._arg()),
+          ptr, _CODE[out.dtype], stride)
 
 
 def ckpt_weight_grad_workspace(rows: int, cols: int, n: int) -> int:
@@ -536,20 +557,20 @@ def ckpt_weight_grad(ckpt: Ckpt, dy, dw, accumulate: bool = False, workspace=Non
     tensor's place in the flat local gradient.  workspace: uint8 device tensor of
     ckpt_weight_grad_workspace bytes, or None to take it from torch's allocator.
     """
-    import torch
-    _matrix(dy, "dy", (torch.float16, torch.bfloat16))
-    if dy.shape[0] != ckpt.rows:
-        raise ValueError(f"dy has {dy.shape[0]} rows, the checkpoint {ckpt.rows}")
+    rows, cols = ckpt.codes.shape
+    py, sy = _matrix(dy, "dy", _F16_BF16)
     n = dy.shape[1]
-    _matrix(dw, "dw", (dy.dtype, torch.float32), n, ckpt.cols)
-    _one_device((dy, dw, *ckpt.tensors()), stream)
-    arg = ckpt._arg()
-    ws = _given_workspace(workspace, ckpt_weight_grad_workspace(ckpt.rows, ckpt.cols, n),
-                          dy.device, stream)
-    _launch((dy, dw, ws, *ckpt.tensors()), stream, lambda h: lib.zero_ckpt_weight_grad(
-        ctypes.byref(arg), dy.data_ptr(), _dtype_code(dy), n, _stride(dy), dw.data_ptr(),
-        _dtype_code(dw), _stride(dw), int(bool(accumulate)),
-        ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0, h))
+    if dy.shape[0] != rows:
+        raise ValueError(f"dy has {dy.shape[0]} rows, the checkpoint {rows}")
+    pw, sw = _matrix(dw, "dw", (dy.dtype, torch.float32), (n, cols))
+    tensors = [dy, dw, ckpt.codes, ckpt.scales]
+    _one_device(tensors, stream)
+    ws, ws_bytes, held = _workspace(workspace, ckpt_weight_grad_workspace(rows, cols, n),
+                                    dy.device, stream)
+    if held is not None:
+        tensors.append(held)
+    _call(tensors, stream, lib.zero_ckpt_weight_grad, ctypes.byref(ckpt._arg()), py,
+          _CODE[dy.dtype], n, sy, pw, _CODE[dw.dtype], sw, int(bool(accumulate)), ws, ws_bytes)
 
 
 class Norm:
@@ -559,39 +580,56 @@ class Norm:
     def __init__(self, kind: int = NORM_NONE, eps: float = 1e-5, weight=None, bias=None):
         self.kind, self.eps, self.weight, self.bias = kind, eps, weight, bias
 
-    def tensors(self):
-        return tuple(t for t in (self.weight, self.bias) if t is not None)
-
-    def _arg(self, name, dtype, cols):
-        a = _NormArg()
-        a.kind, a.eps = self.kind, self.eps
-        for what in ("weight", "bias"):
-            t = getattr(self, what)
-            if t is not None:
-                _row(t, f"{name} {what}", dtype, cols)
-                setattr(a, what, t.data_ptr())
-        return a
+    def _arg(self, name, dtype, cols, tensors):
+        w, b = self.weight, self.bias
+        pw = pb = None
+        if w is not None:
+            pw = _row(w, name + " weight", dtype, cols)
+            tensors.append(w)
+        if b is not None:
+            pb = _row(b, name + " bias", dtype, cols)
+            tensors.append(b)
+        return _NormArg(self.kind, self.eps, pw, pb)
 
 
 _NO_NORM = Norm()
 
 
-def _gate_stride(gate, dtype, rows, cols) -> int:
-    if gate.dim() == 1:
-        _row(gate, "gate", dtype, cols)
-        return 0
-    _matrix(gate, "gate", (dtype,), rows, cols)
-    if _stride(gate) == 0:
+def _gate(gate, dtype, shape, tensors):
+    """(address, row stride): a stride of 0 for one row of gates."""
+    if gate is None:
+        return None, 0
+    tensors.append(gate)
+    if isinstance(gate, torch.Tensor) and gate.dim() == 1:
+        return _row(gate, "gate", dtype, shape[1]), 0
+    ptr, stride = _matrix(gate, "gate", (dtype,), shape)
+    if stride == 0:
         raise ValueError("gate: give one row for every token as a [cols] tensor")
-    return _stride(gate)
+    return ptr, stride
 
 
-def _stats(stats, rows):
-    import torch
+def _stats(stats, rows, tensors):
+    if stats is None:
+        return None
     _dev(stats, "stats", (torch.float32,))
-    if tuple(stats.shape) != (rows, 4) or not stats.is_contiguous():
+    if stats.shape != (rows, 4) or not stats.is_contiguous():
         raise ValueError(f"stats must be a contiguous [{rows}, 4] tensor")
+    tensors.append(stats)
     return stats.data_ptr()
+
+
+def _optional(t, name, dtypes, shape, tensors):
+    if t is None:
+        return None, 0
+    tensors.append(t)
+    return _matrix(t, name, dtypes, shape)
+
+
+def _ckpt(k, tensors):
+    if k is None:
+        return None
+    tensors += (k.codes, k.scales)
+    return ctypes.pointer(k._arg())
 
 
 def block_norm(res, block, out, z, stats, post: Optional[Norm] = None,
@@ -606,29 +644,20 @@ def block_norm(res, block, out, z, stats, post: Optional[Norm] = None,
     for the backward.  ckpt_*: checkpoints of block, out and z to write too.  out
     may be res and z may be block.
     """
-    import torch
-    _matrix(res, "res", (torch.float16, torch.bfloat16))
-    (rows, cols), dt = res.shape, res.dtype
-    post, pre = post or _NO_NORM, pre or _NO_NORM
-    a = _BlockNormArg()
-    a.dtype, a.rows, a.cols, a.scale = _dtype_code(res), rows, cols, scale
-    a.post, a.pre = post._arg("post", dt, cols), pre._arg("pre", dt, cols)
-    a.res, a.res_stride = res.data_ptr(), _stride(res)
-    for name, t in (("block", block), ("out", out), ("z", z)):
-        if t is not None:
-            _matrix(t, name, (dt,), rows, cols)
-            setattr(a, name, t.data_ptr())
-            setattr(a, name + "_stride", _stride(t))
-    if gate is not None:
-        a.gate, a.gate_stride = gate.data_ptr(), _gate_stride(gate, dt, rows, cols)
-    if stats is not None:
-        a.stats = _stats(stats, rows)
-    tensors = [res, block, out, z, stats, gate, *post.tensors(), *pre.tensors()]
-    for name, k in (("ckpt_block", ckpt_block), ("ckpt_out", ckpt_out), ("ckpt_z", ckpt_z)):
-        if k is not None:
-            setattr(a, name, ctypes.pointer(k._arg()))
-            tensors += k.tensors()
-    _launch(tensors, stream, lambda h: lib.zero_block_norm(ctypes.byref(a), h))
+    p_res, s_res = _matrix(res, "res", _F16_BF16)
+    shape, dt = res.shape, res.dtype
+    rows, cols = shape
+    own = (dt,)
+    tensors = [res]
+    a = _BlockNormArg(
+        _CODE[dt], rows, cols, p_res, s_res, *_optional(block, "block", own, shape, tensors),
+        *_gate(gate, dt, shape, tensors), scale,
+        (post or _NO_NORM)._arg("post", dt, cols, tensors),
+        (pre or _NO_NORM)._arg("pre", dt, cols, tensors),
+        *_optional(out, "out", own, shape, tensors), *_optional(z, "z", own, shape, tensors),
+        _stats(stats, rows, tensors), _ckpt(ckpt_block, tensors), _ckpt(ckpt_out, tensors),
+        _ckpt(ckpt_z, tensors))
+    _call(tensors, stream, lib.zero_block_norm, ctypes.byref(a))
 
 
 def block_norm_grad_workspace(rows: int, cols: int) -> int:
@@ -649,51 +678,52 @@ def block_norm_grad(dout, dz, ckpt_out: Optional[Ckpt], ckpt_block: Optional[Ckp
     of a [cols] gate) have one type, the call's or float32, and are added to with
     `accumulate`.  dres may be dout and dblock may be dz.
     """
-    import torch
     first = next((t for t in (dz, dout, dres, dblock) if t is not None), None)
     if first is None:
         raise ValueError("dout, dz, dres and dblock are all None")
-    _matrix(first, "the gradient", (torch.float16, torch.bfloat16))
-    (rows, cols), dt = first.shape, first.dtype
-    post, pre = post or _NO_NORM, pre or _NO_NORM
-    a = _BlockNormGradArg()
-    a.dtype, a.rows, a.cols, a.scale = _dtype_code(first), rows, cols, scale
-    a.post, a.pre = post._arg("post", dt, cols), pre._arg("pre", dt, cols)
-    for name, t in (("dout", dout), ("dz", dz), ("dres", dres), ("dblock", dblock)):
-        if t is not None:
-            _matrix(t, name, (dt,), rows, cols)
-            setattr(a, name, t.data_ptr())
-            setattr(a, name + "_stride", _stride(t))
-    sums = {"dw_pre": dw_pre, "db_pre": db_pre, "dw_post": dw_post, "db_post": db_post}
-    if gate is not None:
-        a.gate, a.gate_stride = gate.data_ptr(), _gate_stride(gate, dt, rows, cols)
-        if gate.dim() == 1:
+    _matrix(first, "the gradient", _F16_BF16)
+    shape, dt = first.shape, first.dtype
+    rows, cols = shape
+    own, code = (dt,), _CODE[dt]
+    tensors = []
+    p_gate, s_gate = _gate(gate, dt, shape, tensors)
+    p_dgate, s_dgate, sums = None, 0, {"dw_pre": dw_pre, "db_pre": db_pre, "dw_post": dw_post,
+                                       "db_post": db_post}
+    if dgate is not None:
+        if gate is None:
+            raise ValueError("dgate without a gate")
+        if s_gate == 0:
             sums["dgate"] = dgate
-        elif dgate is not None:
-            _matrix(dgate, "dgate", (dt,), rows, cols)
-            a.dgate, a.dgate_stride = dgate.data_ptr(), _stride(dgate)
-    elif dgate is not None:
-        raise ValueError("dgate without a gate")
-    sums = {k: t for k, t in sums.items() if t is not None}
-    grad_dtype = next(iter(sums.values())).dtype if sums else dt
-    if grad_dtype not in (dt, torch.float32):
-        raise ValueError(f"parameter gradients have dtype {grad_dtype}, expected {dt} or float32")
+        else:
+            p_dgate, s_dgate = _matrix(dgate, "dgate", own, shape)
+            tensors.append(dgate)
+    grad_dtype, places = None, {}
     for name, t in sums.items():
-        _row(t, name, grad_dtype, cols)
-        setattr(a, name, t.data_ptr())
-    a.grad_dtype = 2 if grad_dtype == torch.float32 else a.dtype
-    a.accumulate = int(bool(accumulate))
-    if stats is not None:
-        a.stats = _stats(stats, rows)
-    tensors = [dout, dz, stats, gate, dres, dblock, dgate, *sums.values(), *post.tensors(),
-               *pre.tensors()]
-    for name, k in (("ckpt_out", ckpt_out), ("ckpt_block", ckpt_block)):
-        if k is not None:
-            setattr(a, name, ctypes.pointer(k._arg()))
-            tensors += k.tensors()
-    _one_device([t for t in tensors if t is not None], stream)
-    need = block_norm_grad_workspace(rows, cols) if sums else 0
-    ws = _given_workspace(workspace, need, first.device, stream)
-    if ws is not None:
-        a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel()
-    _launch([*tensors, ws], stream, lambda h: lib.zero_block_norm_grad(ctypes.byref(a), h))
+        if t is None:
+            continue
+        if grad_dtype is None:
+            grad_dtype = t.dtype
+            if grad_dtype != dt and grad_dtype != torch.float32:
+                raise ValueError(f"parameter gradients have dtype {grad_dtype}, expected {dt} or "
+                                 f"float32")
+        places[name] = _row(t, name, grad_dtype, cols)
+        tensors.append(t)
+    need = lib.zero_block_norm_grad_workspace(rows, cols) if places else 0
+    p_out, p_block = _ckpt(ckpt_out, tensors), _ckpt(ckpt_block, tensors)
+    p_dout, s_dout = _optional(dout, "dout", own, shape, tensors)
+    p_dz, s_dz = _optional(dz, "dz", own, shape, tensors)
+    p_stats = _stats(stats, rows, tensors)
+    n_post = (post or _NO_NORM)._arg("post", dt, cols, tensors)
+    n_pre = (pre or _NO_NORM)._arg("pre", dt, cols, tensors)
+    p_dres, s_dres = _optional(dres, "dres", own, shape, tensors)
+    p_db, s_db = _optional(dblock, "dblock", own, shape, tensors)
+    _one_device(tensors, stream)
+    ws, ws_bytes, held = _workspace(workspace, need, first.device, stream)
+    if held is not None:
+        tensors.append(held)
+    a = _BlockNormGradArg(
+        code, rows, cols, p_dout, s_dout, p_dz, s_dz, p_out, p_block, p_stats, p_gate, s_gate,
+        scale, n_post, n_pre, p_dres, s_dres, p_db, s_db, places.get("dgate", p_dgate), s_dgate,
+        places.get("dw_pre"), places.get("db_pre"), places.get("dw_post"), places.get("db_post"),
+        2 if grad_dtype == torch.float32 else code, int(bool(accumulate)), ws, ws_bytes)
+    _call(tensors, stream, lib.zero_block_norm_grad, ctypes.byref(a))

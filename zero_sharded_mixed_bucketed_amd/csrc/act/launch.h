@@ -75,7 +75,8 @@ struct BlockNormGradLaunch {
   float scale;
   void* sums[kSums];            // nullable
   int grad_dtype, accumulate;
-  float* partial;               // norm_grad_workspace bytes
+  float* partial;               // norm_grad_workspace bytes, or nullptr
+  float* means;                 // inside it: two of each wide row
 };
 
 // Bytes of partial sums that launch_block_norm_grad needs at these sizes.

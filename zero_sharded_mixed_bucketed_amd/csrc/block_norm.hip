@@ -60,8 +60,9 @@ __device__ __forceinline__ void emit(const Ckpt& c, uint64_t row, uint32_t chunk
 
 // Up to eight chunks a thread: rows of up to 4096 columns take one wave, and its
 // sums no barrier.  Nothing is kept from row to row; many rows at once on a compute
-// unit hide the loads, and the norms' weights come from the caches.  At 16384 x
-// 4096 bf16 with a gate a channel this moves FORWARD_RATE.
+// unit hide the loads, and the norms' weights come from the caches.  16384 x 4096
+// bf16 with a gate a channel takes 111 us, 4.8 TB/s (165 us, 4.5 TB/s with all three
+// checkpoints).
 template <typename T, int WAVES, int HELD, bool FULL>
 __global__ __launch_bounds__(64 * WAVES, HELD > 5 ? 3 : 4) void block_norm_kernel(BlockNormLaunch a,
                                                                    uint64_t row0) {
@@ -206,11 +207,20 @@ int grad_waves(uint64_t cols) {
   return static_cast<int>((cols + per - 1) / per);
 }
 
-// Rows that are worked on at once, at most (eight waves on each of 256 compute
-// units); each keeps partial sums of the parameters' gradients.
-uint64_t grad_streams(uint64_t rows, uint64_t cols) {
-  const uint64_t most = 2048 / grad_waves(cols);
+bool wide_rows(uint64_t cols) { return grad_held(cols) > 2; }
+
+// Rows that are worked on at once, at most: what 256 compute units hold, with eight
+// waves each (a workgroup more would wait for the others' last rows).
+uint64_t grad_wgs(uint64_t rows, uint64_t cols) {
+  const uint64_t most = 256 * (8 / grad_waves(cols));
   return rows < most ? rows : most;
+}
+
+// Partial sums of each column of the parameters' gradients: one of each row that is
+// worked on, or of 128 stretches of wide rows.
+uint64_t grad_streams(uint64_t rows, uint64_t cols) {
+  if (!wide_rows(cols)) return grad_wgs(rows, cols);
+  return rows < 128 ? rows : 128;
 }
 
 // Everything of a row that a thread loads.
@@ -293,7 +303,7 @@ constexpr int kGradThreads = 512;  // of a workgroup, at most
 // One workgroup takes rows blockIdx.x, blockIdx.x + gridDim.x, ..., loading one
 // while it works on the one before, and keeps the parameters' gradients of its rows
 // in registers; SETS: 3 -- those of the weights and of a gate a channel; 5 -- and of
-// biases.  Two chunks a thread leave room for that.
+// biases; 0 -- none.  Two chunks a thread leave room for that.
 //
 // Both norms' row sums are taken together, behind one barrier.  The gradient of
 // post's input needs sums of v = y D and v x2 (y = s g w_post), where
@@ -302,10 +312,13 @@ constexpr int kGradThreads = 512;  // of a workgroup, at most
 // and their products with x2 give it afterwards.
 //
 // Up to 8192 columns a thread holds two chunks, and the values of the first half
-// stay in registers for the second; wider rows take four, load nothing ahead, read
-// the norms' weights from the caches and make those values again.  The biases' sums
-// lie in shared memory, each thread's in places of its own: with them in registers
-// the kernel ran out and took 2.5 times as long.
+// stay in registers for the second.  The biases' sums lie in shared memory, each
+// thread's in places of its own: with them in registers the kernel ran out and took
+// 2.5 times as long.  Wider rows (SETS == 0) take four chunks, load nothing ahead,
+// read the norms' weights from the caches, make those values again, and leave the
+// parameters' gradients to norm_sums_kernel, with mean(q x1) and [mean q] of each
+// row: kept here too, 4096 x 16384 took 520 us (RMS)
+// and 850 (layer norms) where it now takes 342 and 355.
 template <typename T, int FMT, int HELD, int SETS, bool FULL>
 __global__ __launch_bounds__(kGradThreads, 2) void block_norm_grad_kernel(BlockNormGradLaunch a,
                                                                           uint64_t pad) {
@@ -344,14 +357,16 @@ __global__ __launch_bounds__(kGradThreads, 2) void block_norm_grad_kernel(BlockN
 #pragma unroll
     for (int j = 0; j < HELD; ++j) load_rows(j);
   }
-  float sum[3][HELD][8];   // of the weights and the gate
+  float sum[3][SETS ? HELD : 1][8];   // of the weights and the gate
   constexpr int kGate = 2;
+  if constexpr (SETS > 0) {
 #pragma unroll
-  for (int s = 0; s < 3; ++s)
+    for (int s = 0; s < 3; ++s)
 #pragma unroll
-    for (int j = 0; j < HELD; ++j)
+      for (int j = 0; j < HELD; ++j)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum[s][j][i] = 0.f;
+        for (int i = 0; i < 8; ++i) sum[s][j][i] = 0.f;
+  }
   extern __shared__ f32x4 bias_sums[];   // SETS == 5: 4 HELD of each thread
   auto bias_at = [&](int set, int j, int half) -> f32x4& {
     return bias_sums[((set * HELD + j) * 2 + half) * lanes + threadIdx.x];
@@ -424,12 +439,12 @@ __global__ __launch_bounds__(kGradThreads, 2) void block_norm_grad_kernel(BlockN
       unpack8<T>(w2[j], w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        sum[kDwPre][j][i] += z[i] * x1[j][i];
+        if constexpr (SETS > 0) sum[kDwPre][j][i] += z[i] * x1[j][i];
         t[0] += q[i] * x1[j][i];
         const float y = a.scale * g[i] * w[i], yx = y * x2[j][i];
         t[2] += yx * e[j][i];
         t[3] += yx * x1[j][i];
-        if constexpr (SETS == 5) {
+        if constexpr (SETS != 3) {
           t[1] += q[i];
           t[4] += yx;
           t[5] += y * e[j][i];
@@ -442,7 +457,7 @@ __global__ __launch_bounds__(kGradThreads, 2) void block_norm_grad_kernel(BlockN
       if constexpr (HELD > 2) __builtin_amdgcn_sched_barrier(0);
     }
     float mean_qx, mean_q = 0.f, mean_vx, mean_v = 0.f;
-    if constexpr (SETS == 5) {
+    if constexpr (SETS != 3) {
       row_sums<kMaxWaves>(t, red, turn, waves);
       mean_qx = t[0] * inv_n;
       mean_q = layer1 ? t[1] * inv_n : 0.f;
@@ -457,6 +472,10 @@ __global__ __launch_bounds__(kGradThreads, 2) void block_norm_grad_kernel(BlockN
     if (!pre) mean_qx = mean_q = 0.f;
     if (!post) mean_vx = 0.f;
     if (!layer2) mean_v = 0.f;
+    if (SETS == 0 && a.means && threadIdx.x == 0) {
+      a.means[2 * row] = mean_qx;
+      a.means[2 * row + 1] = mean_q;
+    }
 
 #pragma unroll
     for (int j = 0; j < HELD; ++j) {
@@ -484,8 +503,10 @@ __global__ __launch_bounds__(kGradThreads, 2) void block_norm_grad_kernel(BlockN
         const float u = a.scale * d[i];
         p[i] = u * g[i];
         dg[i] = u * (x2[j][i] * w[i] + bias[i]);
-        sum[kGate][j][i] += dg[i];
-        sum[kDwPost][j][i] += p[i] * x2[j][i];
+        if constexpr (SETS > 0) {
+          sum[kGate][j][i] += dg[i];
+          sum[kDwPost][j][i] += p[i] * x2[j][i];
+        }
         db[i] = r2 * (p[i] * w[i] - x2[j][i] * mean_vx - mean_v);
       }
       add_bias(1, j, p);
@@ -495,6 +516,7 @@ __global__ __launch_bounds__(kGradThreads, 2) void block_norm_grad_kernel(BlockN
       if constexpr (HELD > 2) __builtin_amdgcn_sched_barrier(0);
     }
   }
+  if constexpr (SETS == 0) return;
   if (!a.partial) return;
   constexpr int kSetOf[kSums] = {kDwPre, kDwPost, kDgate, kDbPre, kDbPost};
 #pragma unroll
@@ -506,7 +528,7 @@ __global__ __launch_bounds__(kGradThreads, 2) void block_norm_grad_kernel(BlockN
       if (col >= pad) continue;
       f32x4 u, v;
       if (s < 3) {
-        const float (&x)[8] = sum[s < 3 ? s : 0][j];
+        const float (&x)[8] = sum[s < 3 ? s : 0][SETS ? j : 0];
         u = f32x4{x[0], x[1], x[2], x[3]};
         v = f32x4{x[4], x[5], x[6], x[7]};
       } else {
@@ -518,6 +540,93 @@ __global__ __launch_bounds__(kGradThreads, 2) void block_norm_grad_kernel(BlockN
       *reinterpret_cast<f32x4*>(p) = u;
       *reinterpret_cast<f32x4*>(p + 4) = v;
     }
+  }
+}
+
+// The parameters' gradients of wide rows, from the same inputs and each row's means:
+// a thread keeps the sums of eight columns over every gridDim.y-th row, so that
+// nothing passes between threads.
+constexpr int kSumThreads = 256;
+constexpr uint32_t kSumCols = kSumThreads * kChunk;
+
+template <typename T, int FMT>
+__global__ __launch_bounds__(kSumThreads, 3) void norm_sums_kernel(BlockNormGradLaunch a,
+                                                                uint64_t pad) {
+  const uint32_t c = (blockIdx.x * kSumThreads + threadIdx.x) * kChunk, cols = a.cols;
+  const bool token_gate = a.gate.p && a.gate.stride != 0;
+  const bool pre = a.c_out.codes != nullptr, block = a.c_block.codes != nullptr;
+  constexpr uint32_t kOne = T::kType == kF16 ? 0x3C003C00u : 0x3F803F80u;
+  const u32x4 ones = {kOne, kOne, kOne, kOne};
+  if (c >= cols) return;
+  float w1[8], w2[8], b2[8], gc[8];
+  unpack8<T>(a.pre.w.p ? load8(a.pre.w.p, c, cols) : ones, w1);
+  unpack8<T>(a.post.w.p ? load8(a.post.w.p, c, cols) : ones, w2);
+  unpack8<T>(a.post.b.p ? load8(a.post.b.p, c, cols) : u32x4{0, 0, 0, 0}, b2);
+  unpack8<T>(a.gate.p && !token_gate ? load8(a.gate.p, c, cols) : ones, gc);
+  float sum[kSums][8];
+#pragma unroll
+  for (int s = 0; s < kSums; ++s)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum[s][i] = 0.f;
+  const uint32_t scale_at = c / kBlock;
+#pragma unroll 2
+  for (uint64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
+    const uint16_t* pd = a.dout.p + row * a.dout.stride;
+    const uint16_t* pz = a.dz.p + row * a.dz.stride;
+    const uint16_t* pg = a.gate.p + row * a.gate.stride;
+    const uint8_t* po = a.c_out.codes + row * a.c_out.code_stride;
+    const uint8_t* pb = a.c_block.codes + row * a.c_block.code_stride;
+    u32x4 wd = {0, 0, 0, 0}, wz = wd, wg = wd;
+    u32x2 wo = {0, 0}, wb = wo;
+    uint32_t so = 0, sb = 0;
+    if (a.dout.p) wd = load8_early<false>(pd, c, cols);
+    if (pre) {
+      wz = load8_early<false>(pz, c, cols);
+      wo = load_codes_early<false>(po, c, cols);
+      so = a.c_out.scales[row * a.c_out.scale_stride + scale_at];
+    }
+    if (block) {
+      wb = load_codes_early<false>(pb, c, cols);
+      sb = a.c_block.scales[row * a.c_block.scale_stride + scale_at];
+    }
+    if (token_gate) wg = load8_early<false>(pg, c, cols);
+    const f32x4 st = a.stats ? *reinterpret_cast<const f32x4*>(a.stats + row * 4)
+                             : f32x4{0.f, 1.f, 0.f, 1.f};
+    const float mean_qx = a.means[2 * row], mean_q = a.means[2 * row + 1];
+    if (c + kChunk > cols) {
+      if (a.dout.p) mend8<false>(wd, pd, c, cols);
+      if (pre) {
+        mend8<false>(wz, pz, c, cols);
+        mend_codes<false>(wo, po, c, cols);
+      }
+      if (block) mend_codes<false>(wb, pb, c, cols);
+      if (token_gate) mend8<false>(wg, pg, c, cols);
+    }
+    float d[8], z[8], g[8], x1[8], x2[8];
+    unpack8<T>(wd, d);
+    unpack8<T>(wz, z);
+    unpack8<T>(wg, g);
+    decode8<FMT>(wo, scale_of(so), x1);
+    decode8<FMT>(wb, scale_of(sb), x2);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float n1 = (x1[i] - st[2]) * st[3], n2 = (x2[i] - st[0]) * st[1];
+      const float e = d[i] + st[3] * (z[i] * w1[i]);
+      const float u = a.scale * (e - st[3] * (n1 * mean_qx + mean_q));
+      const float p = u * (token_gate ? g[i] : gc[i]);
+      sum[kDwPre][i] += z[i] * n1;
+      sum[kDbPre][i] += z[i];
+      sum[kDwPost][i] += p * n2;
+      sum[kDbPost][i] += p;
+      sum[kDgate][i] += u * (n2 * w2[i] + b2[i]);
+    }
+  }
+#pragma unroll
+  for (int s = 0; s < kSums; ++s) {
+    if (!a.sums[s]) continue;
+    float* p = a.partial + (static_cast<uint64_t>(s) * gridDim.y + blockIdx.y) * pad + c;
+    *reinterpret_cast<f32x4*>(p) = f32x4{sum[s][0], sum[s][1], sum[s][2], sum[s][3]};
+    *reinterpret_cast<f32x4*>(p + 4) = f32x4{sum[s][4], sum[s][5], sum[s][6], sum[s][7]};
   }
 }
 
@@ -620,19 +729,21 @@ void backward(const BlockNormGradLaunch& a, int sets, uint32_t wgs, hipStream_t 
     else
       block_norm_grad_kernel<T, FMT, 2, 5, false><<<wgs, threads, shared, stream>>>(a, pad);
   } else {
-    if (full && sets == 3)
-      block_norm_grad_kernel<T, FMT, 4, 3, true><<<wgs, threads, 0, stream>>>(a, pad);
-    else if (sets == 3)
-      block_norm_grad_kernel<T, FMT, 4, 3, false><<<wgs, threads, 0, stream>>>(a, pad);
-    else
-      block_norm_grad_kernel<T, FMT, 4, 5, false><<<wgs, threads, shared, stream>>>(a, pad);
+    if (full) block_norm_grad_kernel<T, FMT, 4, 0, true><<<wgs, threads, 0, stream>>>(a, pad);
+    else block_norm_grad_kernel<T, FMT, 4, 0, false><<<wgs, threads, 0, stream>>>(a, pad);
+    if (a.partial)
+      norm_sums_kernel<T, FMT>
+          <<<dim3((a.cols + kSumCols - 1) / kSumCols,
+                  static_cast<uint32_t>(grad_streams(a.rows, a.cols))),
+             kSumThreads, 0, stream>>>(a, pad);
   }
 }
 
 }  // namespace
 
 uint64_t norm_grad_workspace(uint64_t rows, uint64_t cols) {
-  return grad_streams(rows, cols) * padded(cols) * kSums * sizeof(float);
+  const uint64_t means = wide_rows(cols) ? rows * 2 : 0;
+  return (grad_streams(rows, cols) * padded(cols) * kSums + means) * sizeof(float);
 }
 
 hipError_t launch_block_norm(const BlockNormLaunch& a, hipStream_t stream) {
@@ -646,7 +757,9 @@ hipError_t launch_block_norm_grad(const BlockNormGradLaunch& in, hipStream_t str
   bool any = false;
   for (void* p : a.sums) any = any || p != nullptr;
   if (!any) a.partial = nullptr;
-  const uint32_t wgs = static_cast<uint32_t>(grad_streams(a.rows, a.cols));
+  const uint32_t wgs = static_cast<uint32_t>(grad_wgs(a.rows, a.cols));
+  const uint64_t streams = grad_streams(a.rows, a.cols);
+  a.means = a.partial && wide_rows(a.cols) ? a.partial + streams * padded(a.cols) * kSums : nullptr;
   // layer norms need the row sums of the biases' path too
   const bool five = a.sums[kDbPre] || a.sums[kDbPost] || a.pre.kind == ZERO_NORM_LAYER ||
                     a.post.kind == ZERO_NORM_LAYER;
@@ -665,7 +778,7 @@ hipError_t launch_block_norm_grad(const BlockNormGradLaunch& in, hipStream_t str
   if (!any) return hipSuccess;
   JoinArgs j;
   j.partial = a.partial;
-  j.streams = wgs;
+  j.streams = streams;
   j.pad = padded(a.cols);
   j.cols = a.cols;
   j.dtype = a.grad_dtype;
