@@ -503,6 +503,44 @@ def test_block_norm_grad_partial_calls():
                                   block=False), "no block")
 
 
+@pytest.mark.parametrize("h", [8208, 9001, 16384])
+@pytest.mark.parametrize("kind,gate", [("rms", "channel"), ("layer", "token")])
+def test_block_norm_grad_of_wide_rows_in_place(h, kind, gate):
+    rng = np.random.default_rng(h)
+    _check_backward(_run_backward(rng, 150, h, "bf16", "int8", kind, kind, gate, inplace=True))
+
+
+def test_norms_past_32_bits():
+    """Rows 2^31 + 8 elements apart on every side."""
+    h, stride = 264, (1 << 31) + 8
+    rng = np.random.default_rng(1)
+
+    def far(fill):
+        t = torch.empty(stride + h, dtype=torch.float16, device="cuda").as_strided(
+            (2, h), (stride, 1))
+        if fill:
+            t.copy_(torch.from_numpy(rng.standard_normal((2, h))))
+        return t
+
+    res, block, out, z = far(True), far(True), far(False), far(False)
+    stats = torch.empty((2, 4), dtype=torch.float32, device="cuda")
+    n = Z.Norm(Z.NORM_LAYER, 1e-5)
+    Z.block_norm(res, block, out, z, stats, post=n, pre=n)
+    spec = ("layer", 1e-5, None, None)
+    _check_forward(dict(out=out, z=z, stats=stats), f64(res), f64(block), spec, spec, None, 1.0,
+                   "fp16", "far rows")
+    ko, xo = _stored(out, "int8", "fp16")
+    kb, xb = _stored(block, "int8", "fp16")
+    dw = torch.empty(h, dtype=torch.float32, device="cuda")
+    w = torch.ones(h, dtype=torch.float16, device="cuda")
+    Z.block_norm_grad(res, z, ko, kb, stats, post=n, pre=Z.Norm(Z.NORM_LAYER, 1e-5, w), dres=out,
+                      dblock=block, dw_pre=dw)
+    _check_backward(dict(outs={"dres": out, "dblock": block, "dw_pre": dw}, names=["dw_pre"],
+                         old={}, st=f64(stats), xo=xo, xb=xb, do=f64(res), dz=f64(z), gate=None,
+                         post=spec, pre=spec, scale=1.0, accumulate=False, grad="fp32",
+                         dtype="fp16", t=2))
+
+
 def test_block_norm_grad_without_rows():
     w = torch.ones(50, dtype=torch.float16, device="cuda")
     e = torch.empty((0, 50), dtype=torch.float16, device="cuda")
@@ -514,6 +552,8 @@ def test_block_norm_grad_without_rows():
     assert (dw == 1).all()
     Z.block_norm_grad(None, e, k, None, st, **args)
     assert (dw == 0).all()
+    Z.block_norm_grad(e, e, k, k, st, pre=Z.Norm(Z.NORM_RMS, 1e-5, w),
+                      post=Z.Norm(Z.NORM_RMS, 1e-5, w), dres=e, dblock=e)
     Z.block_norm(e, None, None, e, None, pre=Z.Norm(Z.NORM_RMS, 1e-5, w))
     Z.ckpt_write(e, k)
     Z.ckpt_read(k, e)

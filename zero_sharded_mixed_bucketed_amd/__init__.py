@@ -506,10 +506,15 @@ class Ckpt:
 
 def ckpt_empty(rows: int, cols: int, fmt: int = CKPT_INT8, device=None) -> Ckpt:
     """Uninitialised buffers of a checkpoint, code rows on 16 bytes."""
+    if fmt not in (CKPT_INT8, CKPT_E4M3):
+        raise ValueError(f"unknown checkpoint format {fmt}")
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else device
-    codes = torch.empty((rows, -(-cols // 16) * 16), dtype=torch.uint8, device=dev)[:, :cols]
-    scales = torch.empty((rows, -(-cols // CKPT_BLOCK)), dtype=torch.uint8, device=dev)
-    return Ckpt(codes, scales, fmt)
+    k = Ckpt.__new__(Ckpt)
+    k.codes = torch.empty_strided((rows, cols), (-(-cols // 16) * 16, 1), dtype=torch.uint8,
+                                  device=dev)
+    k.scales = torch.empty((rows, -(-cols // CKPT_BLOCK)), dtype=torch.uint8, device=dev)
+    k.fmt = fmt
+    return k
 
 
 def _workspace(given, need, dev, stream):

@@ -304,7 +304,8 @@ int zero_block_norm_grad(const zero_block_norm_grad_t* a, void* hip_stream) {
   const bool gate_row = a->gate_stride == 0;
   const bool block = a->dblock || a->dgate || a->dw_post || a->db_post;
   const bool need_block = block && (post || a->dgate);
-  if (!a->dres && !block && !a->dw_pre && !a->db_pre) return fail(ZERO_E_INVAL, "no output");
+  if (a->rows && !a->dres && !block && !a->dw_pre && !a->db_pre)
+    return fail(ZERO_E_INVAL, "no output");
   if ((rc = check_rows(n, "dout", a->dout, a->dout_stride)) ||
       (rc = check_rows(n, "dz", a->dz, a->dz_stride)) ||
       (rc = check_gate(n, a->gate, a->gate_stride)) ||

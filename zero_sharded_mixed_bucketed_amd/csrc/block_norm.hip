@@ -729,13 +729,26 @@ void backward(const BlockNormGradLaunch& a, int sets, uint32_t wgs, hipStream_t 
     else
       block_norm_grad_kernel<T, FMT, 2, 5, false><<<wgs, threads, shared, stream>>>(a, pad);
   } else {
-    if (full) block_norm_grad_kernel<T, FMT, 4, 0, true><<<wgs, threads, 0, stream>>>(a, pad);
-    else block_norm_grad_kernel<T, FMT, 4, 0, false><<<wgs, threads, 0, stream>>>(a, pad);
+    auto rows = [&](const BlockNormGradLaunch& l) {
+      if (full) block_norm_grad_kernel<T, FMT, 4, 0, true><<<wgs, threads, 0, stream>>>(l, pad);
+      else block_norm_grad_kernel<T, FMT, 4, 0, false><<<wgs, threads, 0, stream>>>(l, pad);
+    };
+    // outputs that replace inputs wait until the sums have read those: the means are
+    // then made first, by a pass that stores nothing else
+    const bool replaces = (a.dres.p && a.dres.p == a.dout.p) || (a.dblock.p && a.dblock.p == a.dz.p);
+    BlockNormGradLaunch first = a;
+    if (a.partial && replaces) first.dres.p = first.dblock.p = first.dgate.p = nullptr;
+    rows(first);
     if (a.partial)
       norm_sums_kernel<T, FMT>
           <<<dim3((a.cols + kSumCols - 1) / kSumCols,
                   static_cast<uint32_t>(grad_streams(a.rows, a.cols))),
              kSumThreads, 0, stream>>>(a, pad);
+    if (a.partial && replaces) {
+      BlockNormGradLaunch last = a;
+      last.means = nullptr;
+      rows(last);
+    }
   }
 }
 

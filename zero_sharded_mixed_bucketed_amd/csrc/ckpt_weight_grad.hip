@@ -465,8 +465,8 @@ Plan plan(uint64_t rows, uint64_t k, uint64_t n) {
     p.tile = tile;
     p.tn = (n + tile - 1) / tile;
     p.tk = (k + tile - 1) / tile;
-    const uint64_t most = rows / 256 < 64 ? (rows < 512 ? 1 : rows / 256) : 64;
-    for (uint64_t s = 1; s <= most; ++s) {
+    for (const uint64_t s : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64}) {
+      if (s > 1 && rows < 256 * s) break;   // a split sums 256 tokens at least
       p.per_split = rows ? ((rows + s - 1) / s + 63) / 64 * 64 : 64;
       p.splits = rows ? (rows + p.per_split - 1) / p.per_split : 1;
       const double us = estimate(tile, p.tn * p.tk * p.splits, p.splits, p.per_split, n * k);
