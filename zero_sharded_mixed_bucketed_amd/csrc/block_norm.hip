@@ -81,9 +81,9 @@ __global__ __launch_bounds__(64 * WAVES, HELD > 5 ? 3 : 4) void block_norm_kerne
 #pragma unroll
   for (int j = 0; j < HELD; ++j) {
     const uint32_t c = (j * kLanes + lane) * kChunk;
-    wx[j] = load8_early<FULL>(res, c, cols);
+    wx[j] = stream8_early<FULL>(res, c, cols);
     wb[j] = u32x4{0, 0, 0, 0};
-    if (has_block) wb[j] = load8_early<FULL>(block, c, cols);
+    if (has_block) wb[j] = stream8_early<FULL>(block, c, cols);
   }
 #pragma unroll
   for (int j = 0; j < HELD; ++j) {
@@ -255,17 +255,17 @@ struct GradRow {
     for (int j = 0; j < HELD; ++j) {
       const uint32_t chunk = j * lanes + threadIdx.x, c = chunk * kChunk;
       const uint32_t b = FULL || c < a.cols ? chunk / kQuad : 0;
-      if (a.dout.p) d[j] = load8_early<FULL>(pd, c, a.cols);
+      if (a.dout.p) d[j] = stream8_early<FULL>(pd, c, a.cols);
       if (a.c_out.codes) {
-        z[j] = load8_early<FULL>(pz, c, a.cols);
-        out[j] = load_codes_early<FULL>(po, c, a.cols);
+        z[j] = stream8_early<FULL>(pz, c, a.cols);
+        out[j] = stream_codes_early<FULL>(po, c, a.cols);
         s_out[j] = so[b];
       }
       if (a.c_block.codes) {
-        block[j] = load_codes_early<FULL>(pb, c, a.cols);
+        block[j] = stream_codes_early<FULL>(pb, c, a.cols);
         s_block[j] = sb[b];
       }
-      if (token_gate) g[j] = load8_early<FULL>(pg, c, a.cols);
+      if (token_gate) g[j] = stream8_early<FULL>(pg, c, a.cols);
     }
   }
 
@@ -579,17 +579,17 @@ __global__ __launch_bounds__(kSumThreads, 3) void norm_sums_kernel(BlockNormGrad
     u32x4 wd = {0, 0, 0, 0}, wz = wd, wg = wd;
     u32x2 wo = {0, 0}, wb = wo;
     uint32_t so = 0, sb = 0;
-    if (a.dout.p) wd = load8_early<false>(pd, c, cols);
+    if (a.dout.p) wd = stream8_early<false>(pd, c, cols);
     if (pre) {
-      wz = load8_early<false>(pz, c, cols);
-      wo = load_codes_early<false>(po, c, cols);
+      wz = stream8_early<false>(pz, c, cols);
+      wo = stream_codes_early<false>(po, c, cols);
       so = a.c_out.scales[row * a.c_out.scale_stride + scale_at];
     }
     if (block) {
-      wb = load_codes_early<false>(pb, c, cols);
+      wb = stream_codes_early<false>(pb, c, cols);
       sb = a.c_block.scales[row * a.c_block.scale_stride + scale_at];
     }
-    if (token_gate) wg = load8_early<false>(pg, c, cols);
+    if (token_gate) wg = stream8_early<false>(pg, c, cols);
     const f32x4 st = a.stats ? *reinterpret_cast<const f32x4*>(a.stats + row * 4)
                              : f32x4{0.f, 1.f, 0.f, 1.f};
     const float mean_qx = a.means[2 * row], mean_q = a.means[2 * row + 1];
