@@ -11,6 +11,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "act/format.h"
 #include "act/launch.h"
 #include "zero.h"
@@ -200,7 +202,9 @@ __global__ __launch_bounds__(64 * WAVES, HELD > 5 ? 3 : 4) void block_norm_kerne
 uint64_t padded(uint64_t cols) { return (cols + kChunk - 1) / kChunk * kChunk; }
 
 // Chunks a thread holds, and waves of a row (at most 8).
-int grad_held(uint64_t cols) { return cols <= 8 * 64 * 2 * kChunk ? 2 : 4; }
+int grad_held(uint64_t cols) {
+  return cols <= 64 * kChunk ? 1 : cols <= 8 * 64 * 2 * kChunk ? 2 : 4;
+}
 
 int grad_waves(uint64_t cols) {
   const uint64_t per = 64 * grad_held(cols) * kChunk;
@@ -210,9 +214,10 @@ int grad_waves(uint64_t cols) {
 bool wide_rows(uint64_t cols) { return grad_held(cols) > 2; }
 
 // Rows that are worked on at once, at most: what 256 compute units hold, with eight
-// waves each (a workgroup more would wait for the others' last rows).
+// waves each, or 12 of the smallest rows (a workgroup more would wait for the others'
+// last rows).
 uint64_t grad_wgs(uint64_t rows, uint64_t cols) {
-  const uint64_t most = 256 * (8 / grad_waves(cols));
+  const uint64_t most = 256 * ((grad_held(cols) == 1 ? 12 : 8) / grad_waves(cols));
   return rows < most ? rows : most;
 }
 
@@ -311,7 +316,7 @@ constexpr int kGradThreads = 512;  // of a workgroup, at most
 // is known only after pre's; but it is linear in a and m, so sums of y e, y x1, y
 // and their products with x2 give it afterwards.
 //
-// Up to 8192 columns a thread holds two chunks, and the values of the first half
+// Up to 8192 columns a thread holds two chunks (up to 512 columns, one), and the values of the first half
 // stay in registers for the second.  The biases' sums lie in shared memory, each
 // thread's in places of its own: with them in registers the kernel ran out and took
 // 2.5 times as long.  Wider rows (SETS == 0) take four chunks, load nothing ahead,
@@ -320,10 +325,10 @@ constexpr int kGradThreads = 512;  // of a workgroup, at most
 // row: kept here too, 4096 x 16384 took 520 us (RMS)
 // and 850 (layer norms) where it now takes 342 and 355.
 template <typename T, int FMT, int HELD, int SETS, bool FULL>
-__global__ __launch_bounds__(kGradThreads, 2) void block_norm_grad_kernel(BlockNormGradLaunch a,
-                                                                          uint64_t pad) {
-  constexpr bool kAhead = HELD == 2, kKeep = kAhead;
-  constexpr int kMaxWaves = kGradThreads / 64;
+__global__ __launch_bounds__(HELD == 1 ? 64 : kGradThreads, HELD == 1 ? 3 : 2) void
+block_norm_grad_kernel(BlockNormGradLaunch a, uint64_t pad) {
+  constexpr bool kAhead = HELD <= 2, kKeep = kAhead;
+  constexpr int kMaxWaves = HELD == 1 ? 1 : kGradThreads / 64;
   constexpr int kRowSums = 8;
   __shared__ float red[2 * kMaxWaves * kRowSums];
   int turn = 0;
@@ -718,16 +723,21 @@ void backward(const BlockNormGradLaunch& a, int sets, uint32_t wgs, hipStream_t 
   const int held = grad_held(a.cols);
   const uint32_t threads = 64 * grad_waves(a.cols);
   const bool full = a.cols == static_cast<uint32_t>(held) * threads * kChunk;
-  const uint32_t shared = 4 * held * threads * sizeof(f32x4);   // at most 128 KiB
-  if (held == 2) {
-    if (full && sets == 3)
-      block_norm_grad_kernel<T, FMT, 2, 3, true><<<wgs, threads, 0, stream>>>(a, pad);
-    else if (full)
-      block_norm_grad_kernel<T, FMT, 2, 5, true><<<wgs, threads, shared, stream>>>(a, pad);
-    else if (sets == 3)
-      block_norm_grad_kernel<T, FMT, 2, 3, false><<<wgs, threads, 0, stream>>>(a, pad);
-    else
-      block_norm_grad_kernel<T, FMT, 2, 5, false><<<wgs, threads, shared, stream>>>(a, pad);
+  const uint32_t shared = 4 * held * threads * sizeof(f32x4);   // at most 64 KiB
+  if (held <= 2) {
+    auto run = [&](auto h) {
+      constexpr int kHeld = decltype(h)::value;
+      if (full && sets == 3)
+        block_norm_grad_kernel<T, FMT, kHeld, 3, true><<<wgs, threads, 0, stream>>>(a, pad);
+      else if (full)
+        block_norm_grad_kernel<T, FMT, kHeld, 5, true><<<wgs, threads, shared, stream>>>(a, pad);
+      else if (sets == 3)
+        block_norm_grad_kernel<T, FMT, kHeld, 3, false><<<wgs, threads, 0, stream>>>(a, pad);
+      else
+        block_norm_grad_kernel<T, FMT, kHeld, 5, false><<<wgs, threads, shared, stream>>>(a, pad);
+    };
+    if (held == 1) run(std::integral_constant<int, 1>());
+    else run(std::integral_constant<int, 2>());
   } else {
     auto rows = [&](const BlockNormGradLaunch& l) {
       if (full) block_norm_grad_kernel<T, FMT, 4, 0, true><<<wgs, threads, 0, stream>>>(l, pad);
