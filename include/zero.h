@@ -328,7 +328,8 @@ int zero_launch_occupancy(int kernel, int *wgs_per_cu, uint32_t *lds_bytes);
  *   value(code) * 2^(b - 127),  b = scales[r * scale_stride + c / 32];
  * b = 255 stands for NaN.  int8 codes are two's complement
  * (-127..127), e4m3 codes are 8-bit floats with 4 exponent and 3 mantissa bits,
- * bias 7, no infinities.  Padding columns between rows are never touched.
+ * bias 7, no infinities.  Padding columns between rows are never touched.  A row
+ * has at most 2^31 columns.
  */
 typedef struct zero_ckpt {
   uint8_t *codes;
@@ -352,8 +353,8 @@ typedef struct zero_ckpt {
  * A block with an infinity or NaN is held as NaN throughout, so an overflow stays
  * visible in what is computed from it.  A held value of a finite block is
  * exactly representable in x's type.
- * Errors: ZERO_E_INVAL (NULL, dtype, format), ZERO_E_RANGE (a stride too small,
- * size overflow), ZERO_E_ALIGN, ZERO_E_DEVICE (launch failed).
+ * Errors: ZERO_E_INVAL (NULL, dtype, format), ZERO_E_RANGE (a stride too small, too
+ * many columns, size overflow), ZERO_E_ALIGN, ZERO_E_DEVICE (launch failed).
  */
 int zero_ckpt_write(const void *x, int dtype, uint64_t x_stride, const zero_ckpt_t *c,
                     void *hip_stream);
@@ -433,7 +434,8 @@ typedef struct zero_block_norm {
  * before its rounding to 16 bits; h' and z are rounded once each.  stats[row] =
  * {mean, 1/deviation} of post's and then of pre's input (mean 0 for RMS; 0 and 1
  * without the norm).  Checkpoints hold b, and h' and z after their rounding, as
- * zero_ckpt_write stores them.
+ * zero_ckpt_write stores them.  Statistics are fp32: a row whose squares pass its
+ * range (bf16 values beyond 1e19) has a deviation of infinity.
  * out may be res and z may be block (same address and stride); other overlaps of
  * an output are undefined.
  * Errors: ZERO_E_INVAL (NULL, dtype, kind, eps, a gate, post norm or ckpt_block

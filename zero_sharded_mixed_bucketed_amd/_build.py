@@ -4,10 +4,12 @@ Usage: python -m zero_sharded_mixed_bucketed_amd._build
 """
 from __future__ import annotations
 
+import concurrent.futures
 import glob
 import os
 import subprocess
 import sys
+import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -30,16 +32,28 @@ def sources():
     return sorted(glob.glob(os.path.join(HERE, "csrc", "*.hip")))
 
 
-def build(verbose: bool = False) -> str:
-    tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [HIPCC, *HIP_FLAGS, "-shared", "-I", os.path.join(ROOT, "include"),
-           "-I", os.path.join(HERE, "csrc"), *sources(), "-o", tmp]
-    if verbose:
-        print(" ".join(cmd), flush=True)
+def _run(cmd, what: str) -> None:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         sys.stderr.write(r.stdout + r.stderr)
-        raise RuntimeError("hipcc failed building libzero.so")
+        raise RuntimeError(f"hipcc failed building {what}")
+
+
+def build(verbose: bool = False) -> str:
+    """Compiles every source to an object, side by side, and links them."""
+    tmp = LIB + f".tmp{os.getpid()}"
+    inc = ["-I", os.path.join(ROOT, "include"), "-I", os.path.join(HERE, "csrc")]
+    with tempfile.TemporaryDirectory() as d:
+        objs = [os.path.join(d, os.path.basename(s) + ".o") for s in sources()]
+        cmds = [[HIPCC, *HIP_FLAGS, *inc, "-c", s, "-o", o] for s, o in zip(sources(), objs)]
+        if verbose:
+            print("\n".join(" ".join(c) for c in cmds), flush=True)
+        jobs = max(1, min(8, len(cmds), len(os.sched_getaffinity(0))))
+        with concurrent.futures.ThreadPoolExecutor(jobs) as pool:
+            for f in [pool.submit(_run, c, c[-3]) for c in cmds]:
+                f.result()
+        _run([HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp],
+             "libzero.so")
     os.replace(tmp, LIB)
     return LIB
 

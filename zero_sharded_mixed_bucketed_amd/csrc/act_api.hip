@@ -34,6 +34,7 @@ int check_ckpt(const char* name, const zero_ckpt_t* c) {
     return fail(ZERO_E_INVAL, "%s: unknown format %d", name, c->format);
   if (c->rows == 0 || c->cols == 0) return ZERO_OK;
   if (!c->codes || !c->scales) return fail(ZERO_E_INVAL, "%s: codes or scales is NULL", name);
+  if (c->cols > (1ull << 31)) return fail(ZERO_E_RANGE, "%s: more than 2^31 columns", name);
   int rc = check_matrix(name, c->rows, c->cols, c->code_stride);
   if (rc) return rc;
   return check_matrix(name, c->rows, (c->cols - 1) / ZERO_CKPT_BLOCK + 1, c->scale_stride);
