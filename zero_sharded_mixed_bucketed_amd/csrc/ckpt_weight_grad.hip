@@ -488,7 +488,7 @@ void run(const WeightGradLaunch& a, const Plan& p, uint32_t wgs, uint64_t safe,
     weight_grad_kernel<T, FMT, 256, 64>
         <<<wgs, kThreads, 0, stream>>>(a, safe, p.per_split, tk, tiles);
   else
-    weight_grad_kernel<T, FMT, 128, 32>
+    weight_grad_kernel<T, FMT, 128, 64>
         <<<wgs, kThreads, 0, stream>>>(a, safe, p.per_split, tk, tiles);
 }
 
