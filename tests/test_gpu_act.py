@@ -164,6 +164,10 @@ WSHAPES = [  # t, k, n, dy pad, dw pad
     (1, 1, 1, 0, 0), (1, 200, 3, 0, 0), (5, 32, 129, 0, 0), (31, 128, 128, 0, 0),
     (32, 136, 64, 8, 8), (33, 127, 130, 1, 3), (64, 256, 256, 0, 0), (100, 1032, 77, 3, 0),
     (257, 513, 260, 0, 1), (1000, 96, 520, 8, 0), (3001, 264, 136, 0, 0), (4096, 64, 40, 0, 0)]
+# enough output for tiles of 256 x 256: whole ones, ragged edges, lengths around the
+# tokens of a turn, and odd strides
+WLARGE = [(1, 2048, 4096, 0, 0), (200, 2080, 4100, 0, 0), (64, 4096, 2304, 8, 0),
+          (193, 2313, 2561, 1, 1), (320, 2560, 2048, 0, 0)]
 
 
 @pytest.mark.parametrize("t,k,n,pad,wpad", WSHAPES)
@@ -201,6 +205,14 @@ def test_weight_grad_reads_every_code_and_scale(fmt, dtype):
         held = oact.held(codes.cpu().numpy(), scales.cpu().numpy(), fmt)
         want = torch.from_numpy(held).float().to(TORCH[dtype]).double().numpy()
         assert np.array_equal(f64(dw), want, equal_nan=True), b
+
+
+@pytest.mark.parametrize("t,k,n,pad,wpad", WLARGE)
+@pytest.mark.parametrize("fmt,dtype,out,accumulate", [
+    ("int8", "fp16", "fp16", False), ("int8", "bf16", "fp32", True),
+    ("e4m3", "fp16", "fp32", False), ("e4m3", "bf16", "bf16", True)])
+def test_weight_grad_large_tiles(t, k, n, pad, wpad, fmt, dtype, out, accumulate):
+    test_weight_grad(t, k, n, pad, wpad, fmt, dtype, out, accumulate)
 
 
 def test_weight_grad_without_tokens():
@@ -361,7 +373,7 @@ def test_block_norm_in_place_and_without_a_block():
                    ("layer", 1e-5, None, None), None, 1.0, "fp16", "no block")
 
 
-@pytest.mark.parametrize("h", [40, 1024, 2051])
+@pytest.mark.parametrize("h", [40, 1024, 2051, 5120, 9000])
 @pytest.mark.parametrize("fmt", ["int8", "e4m3"])
 @pytest.mark.parametrize("dtype", ["fp16", "bf16"])
 def test_emitted_checkpoints_are_those_of_the_stored_outputs(h, fmt, dtype):
@@ -491,6 +503,30 @@ def test_block_norm_grad(t, h, pad, post, pre, gate, grad, acc, fmt, dtype):
 def test_block_norm_grad_more_rows_than_streams(t, h, kind):
     rng = np.random.default_rng(t)
     _check_backward(_run_backward(rng, t, h, "bf16", "int8", kind, kind, "channel"))
+
+
+@pytest.mark.parametrize("h", [7, 100, 512, 2300, 5120, 8191, 10000])
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_norms_without_weights_and_with_every_part(h, dtype):
+    """No weights (ones, also past the row's end) and a large mean, which would show
+    there; then every gradient of layer norms at once."""
+    rng = np.random.default_rng(h)
+    t = 40
+    x = torch.from_numpy(rng.standard_normal((t, h)) + 3.0).to(TORCH[dtype]).cuda()
+    k, xv = _stored(x, "int8", dtype)
+    st = np.concatenate([*oact.stats(f64(x), "layer", 1e-5)] * 2, axis=1).astype(np.float32)
+    stats = torch.from_numpy(st).cuda()
+    dz, do = acts(rng, t, h, dtype), acts(rng, t, h, dtype)
+    outs = {n: torch.empty(h, dtype=torch.float32, device="cuda")
+            for n in ("dw_pre", "db_pre", "dw_post", "db_post")}
+    names = list(outs)
+    outs["dres"], outs["dblock"] = torch.empty_like(dz), torch.empty_like(dz)
+    n = Z.Norm(Z.NORM_LAYER, 1e-5)
+    Z.block_norm_grad(do, dz, k, k, stats, post=n, pre=n, scale=1.5, **outs)
+    spec = ("layer", 1e-5, None, None)
+    _check_backward(dict(outs=outs, names=names, old={}, st=st.astype(np.float64), xo=xv, xb=xv,
+                         do=f64(do), dz=f64(dz), gate=None, post=spec, pre=spec, scale=1.5,
+                         accumulate=False, grad="fp32", dtype=dtype, t=t))
 
 
 def test_block_norm_grad_partial_calls():

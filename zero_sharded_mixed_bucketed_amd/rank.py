@@ -168,7 +168,9 @@ class RankState:
         """block_norm_grad with the parameters' gradients in the local gradient:
         places maps dw_pre, db_pre, dw_post, db_post and dgate (a gate of one row) to
         their flat indices."""
-        first = next(t for t in (dz, dout) if t is not None)
+        first = dout if dz is None else dz
+        if first is None:
+            raise ValueError("dout and dz are both None")
         slots = {name: self.grad_slot(lo, first.shape[1], bucket, bucket_offset)
                  for name, lo in places.items()}
         block_norm_grad(dout, dz, ckpt_out, ckpt_block, stats, **slots, **call)
