@@ -400,6 +400,7 @@ import torch  # noqa: E402  (after _load, which decides which HIP runtime is map
 # ---------------------------------------------------------------------------
 # Activations: 8-bit checkpoints, the weight gradient from them, block norms.
 
+_CUDA = torch.device("cuda")    # the current device
 _F16_BF16 = (torch.float16, torch.bfloat16)
 _FLOATS = (torch.float16, torch.bfloat16, torch.float32)
 _CODE = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
@@ -428,24 +429,27 @@ def _row(t, name, dtype, cols):
         raise ValueError(f"{name} must be a device tensor")
     if t.dtype != dtype:
         raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if t.dim() != 1 or t.shape[0] != cols or not t.is_contiguous():
+    if t.shape != (cols,) or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous row of {cols}")
     return t.data_ptr()
 
 
-def _call(tensors, stream, call, *args) -> None:
-    """call(*args, stream handle) with the tensors' device current (as _launch)."""
+def _index(tensors, stream) -> int:
+    """The index of the one device that a call's tensors (and stream) are on."""
     dev = tensors[0].get_device()
     for t in tensors:
         if t.get_device() != dev:
             raise ValueError(f"tensors of one call are on {tensors[0].device} and {t.device}")
-    if stream is None:
-        handle = torch._C._cuda_getCurrentRawStream(dev)
-    elif stream.device.index != dev:
+    if stream is not None and stream.device.index != dev:
         raise ValueError(f"the stream is on {stream.device}, the tensors on {tensors[0].device}")
-    else:
-        handle = stream.cuda_stream
-    if torch.cuda.current_device() == dev:
+    return dev
+
+
+def _call(dev, stream, call, *args) -> None:
+    """call(*args, stream handle) with device `dev` current: on the given stream, or on
+    that device's current one."""
+    handle = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if torch._C._cuda_getDevice() == dev:
         rc = call(*args, handle)
     else:
         with torch.cuda.device(dev):
@@ -508,7 +512,7 @@ def ckpt_empty(rows: int, cols: int, fmt: int = CKPT_INT8, device=None) -> Ckpt:
     """Uninitialised buffers of a checkpoint, code rows on 16 bytes."""
     if fmt not in (CKPT_INT8, CKPT_E4M3):
         raise ValueError(f"unknown checkpoint format {fmt}")
-    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else device
+    dev = _CUDA if device is None else device
     k = Ckpt.__new__(Ckpt)
     k.codes = torch.empty_strided((rows, cols), (-(-cols // 16) * 16, 1), dtype=torch.uint8,
                                   device=dev)
@@ -524,28 +528,32 @@ def _workspace(given, need, dev, stream):
         _dev(given, "workspace", (torch.uint8,), need)
         if not given.is_contiguous():
             raise ValueError("workspace must be contiguous")
+        if given.get_device() != dev:
+            raise ValueError(f"the workspace is on {given.device}, the tensors on device {dev}")
         return given.data_ptr(), given.numel(), given
     if need == 0:
         return None, 0, None
     if stream is None:
-        t = torch.empty(need, dtype=torch.uint8, device=dev)
+        t = torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", dev))
     else:
         with torch.cuda.stream(stream):
-            t = torch.empty(need, dtype=torch.uint8, device=dev)
+            t = torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", dev))
     return t.data_ptr(), need, t
 
 
 def ckpt_write(x, ckpt: Ckpt, stream=None) -> None:
     """Stores x (float16/bfloat16 [rows, cols], any row stride) in 8 bits."""
     ptr, stride = _matrix(x, "x", _F16_BF16, ckpt.codes.shape)
-    _call((x, ckpt.codes, ckpt.scales), stream, lib.zero_ckpt_write, ptr, _CODE[x.dtype], stride,
+    dev = _index((x, ckpt.codes, ckpt.scales), stream)
+    _call(dev, stream, lib.zero_ckpt_write, ptr, _CODE[x.dtype], stride,
           ctypes.byref(ckpt._arg()))
 
 
 def ckpt_read(ckpt: Ckpt, out, stream=None) -> None:
     """Reads the held values into out (float16/bfloat16/float32 [rows, cols])."""
     ptr, stride = _matrix(out, "out", _FLOATS, ckpt.codes.shape)
-    _call((out, ckpt.codes, ckpt.scales), stream, lib.zero_ckpt_read, ctypes.byref(ckpt._arg()),
+    dev = _index((out, ckpt.codes, ckpt.scales), stream)
+    _call(dev, stream, lib.zero_ckpt_read, ctypes.byref(ckpt._arg()),
           ptr, _CODE[out.dtype], stride)
 
 
@@ -568,13 +576,10 @@ def ckpt_weight_grad(ckpt: Ckpt, dy, dw, accumulate: bool = False, workspace=Non
     if dy.shape[0] != rows:
         raise ValueError(f"dy has {dy.shape[0]} rows, the checkpoint {rows}")
     pw, sw = _matrix(dw, "dw", (dy.dtype, torch.float32), (n, cols))
-    tensors = [dy, dw, ckpt.codes, ckpt.scales]
-    _one_device(tensors, stream)
-    ws, ws_bytes, held = _workspace(workspace, ckpt_weight_grad_workspace(rows, cols, n),
-                                    dy.device, stream)
-    if held is not None:
-        tensors.append(held)
-    _call(tensors, stream, lib.zero_ckpt_weight_grad, ctypes.byref(ckpt._arg()), py,
+    dev = _index((dy, dw, ckpt.codes, ckpt.scales), stream)
+    ws, ws_bytes, held = _workspace(workspace, lib.zero_ckpt_weight_grad_workspace(rows, cols, n),
+                                    dev, stream)
+    _call(dev, stream, lib.zero_ckpt_weight_grad, ctypes.byref(ckpt._arg()), py,
           _CODE[dy.dtype], n, sy, pw, _CODE[dw.dtype], sw, int(bool(accumulate)), ws, ws_bytes)
 
 
@@ -662,7 +667,7 @@ def block_norm(res, block, out, z, stats, post: Optional[Norm] = None,
         *_optional(out, "out", own, shape, tensors), *_optional(z, "z", own, shape, tensors),
         _stats(stats, rows, tensors), _ckpt(ckpt_block, tensors), _ckpt(ckpt_out, tensors),
         _ckpt(ckpt_z, tensors))
-    _call(tensors, stream, lib.zero_block_norm, ctypes.byref(a))
+    _call(_index(tensors, stream), stream, lib.zero_block_norm, ctypes.byref(a))
 
 
 def block_norm_grad_workspace(rows: int, cols: int) -> int:
@@ -686,7 +691,8 @@ def block_norm_grad(dout, dz, ckpt_out: Optional[Ckpt], ckpt_block: Optional[Ckp
     first = next((t for t in (dz, dout, dres, dblock) if t is not None), None)
     if first is None:
         raise ValueError("dout, dz, dres and dblock are all None")
-    _matrix(first, "the gradient", _F16_BF16)
+    if not isinstance(first, torch.Tensor) or first.dtype not in _F16_BF16 or first.dim() != 2:
+        raise ValueError("gradients must be float16 or bfloat16 matrices")
     shape, dt = first.shape, first.dtype
     rows, cols = shape
     own, code = (dt,), _CODE[dt]
@@ -722,13 +728,11 @@ def block_norm_grad(dout, dz, ckpt_out: Optional[Ckpt], ckpt_block: Optional[Ckp
     n_pre = (pre or _NO_NORM)._arg("pre", dt, cols, tensors)
     p_dres, s_dres = _optional(dres, "dres", own, shape, tensors)
     p_db, s_db = _optional(dblock, "dblock", own, shape, tensors)
-    _one_device(tensors, stream)
-    ws, ws_bytes, held = _workspace(workspace, need, first.device, stream)
-    if held is not None:
-        tensors.append(held)
+    dev = _index(tensors, stream)
+    ws, ws_bytes, held = _workspace(workspace, need, dev, stream)
     a = _BlockNormGradArg(
         code, rows, cols, p_dout, s_dout, p_dz, s_dz, p_out, p_block, p_stats, p_gate, s_gate,
         scale, n_post, n_pre, p_dres, s_dres, p_db, s_db, places.get("dgate", p_dgate), s_dgate,
         places.get("dw_pre"), places.get("db_pre"), places.get("dw_post"), places.get("db_post"),
         2 if grad_dtype == torch.float32 else code, int(bool(accumulate)), ws, ws_bytes)
-    _call(tensors, stream, lib.zero_block_norm_grad, ctypes.byref(a))
+    _call(dev, stream, lib.zero_block_norm_grad, ctypes.byref(a))
