@@ -118,9 +118,11 @@ __device__ __forceinline__ u32x4 stream8(const uint16_t* row, uint64_t c, uint64
 // larger than they are, and rows come in faster for it (16384 x 4096 bf16: reading a
 // checkpoint back 42 -> 31 us, the norms 111 -> 99 us).  Loads of what is read once
 // do too, where that measured faster.
+template <bool STREAM = true>
 __device__ __forceinline__ void store8(uint16_t* row, uint64_t c, uint64_t cols, u32x4 w) {
   if (c + kChunk <= cols) {
-    __builtin_nontemporal_store(w, reinterpret_cast<u32x4_at2*>(row + c));
+    if constexpr (STREAM) __builtin_nontemporal_store(w, reinterpret_cast<u32x4_at2*>(row + c));
+    else *reinterpret_cast<u32x4_at2*>(row + c) = w;
     return;
   }
 #pragma unroll
@@ -167,18 +169,20 @@ __device__ __forceinline__ u32x4 load8_early(const uint16_t* row, uint32_t c, ui
   return *reinterpret_cast<const u32x4_at2*>(row + early<FULL>(c, cols));
 }
 
-// Read once (see store8).
-template <bool FULL>
+// Read once (see store8); STREAM == false: as load8_early.
+template <bool FULL, bool STREAM = true>
 __device__ __forceinline__ u32x4 stream8_early(const uint16_t* row, uint32_t c, uint32_t cols) {
   if (!FULL && cols < kChunk) return u32x4{0, 0, 0, 0};
+  if (!STREAM) return load8_early<FULL>(row, c, cols);
   return __builtin_nontemporal_load(
       reinterpret_cast<const u32x4_at2*>(row + early<FULL>(c, cols)));
 }
 
-template <bool FULL>
+template <bool FULL, bool STREAM = true>
 __device__ __forceinline__ u32x2 stream_codes_early(const uint8_t* row, uint32_t c,
                                                     uint32_t cols) {
   if (!FULL && cols < kChunk) return u32x2{0, 0};
+  if (!STREAM) return *reinterpret_cast<const u32x2_at1*>(row + early<FULL>(c, cols));
   return __builtin_nontemporal_load(
       reinterpret_cast<const u32x2_at1*>(row + early<FULL>(c, cols)));
 }
@@ -208,10 +212,9 @@ __device__ __forceinline__ u32x4 load8_row(const uint16_t* row, uint32_t c, uint
   return w;
 }
 
-template <bool FULL>
+template <bool FULL, bool STREAM = true>
 __device__ __forceinline__ void store8_row(uint16_t* row, uint32_t c, uint32_t cols, u32x4 w) {
-  if constexpr (FULL) __builtin_nontemporal_store(w, reinterpret_cast<u32x4_at2*>(row + c));
-  else if (c < cols) store8(row, c, cols, w);
+  if (FULL || c < cols) store8<STREAM>(row, c, FULL ? UINT64_MAX : cols, w);
 }
 
 template <bool FULL>

@@ -69,6 +69,8 @@ template <typename T, int WAVES, int HELD, bool FULL>
 __global__ __launch_bounds__(64 * WAVES, HELD > 5 ? 3 : 4) void block_norm_kernel(BlockNormLaunch a,
                                                                    uint64_t row0) {
   constexpr uint32_t kLanes = 64 * WAVES;
+  // short rows that end inside a line share it, and meet in the caches
+  constexpr bool kStream = FULL || WAVES * HELD > 1;
   __shared__ float red[2 * WAVES];
   int turn = 0;
   const uint64_t row = row0 + blockIdx.x;
@@ -83,9 +85,9 @@ __global__ __launch_bounds__(64 * WAVES, HELD > 5 ? 3 : 4) void block_norm_kerne
 #pragma unroll
   for (int j = 0; j < HELD; ++j) {
     const uint32_t c = (j * kLanes + lane) * kChunk;
-    wx[j] = stream8_early<FULL>(res, c, cols);
+    wx[j] = stream8_early<FULL, kStream>(res, c, cols);
     wb[j] = u32x4{0, 0, 0, 0};
-    if (has_block) wb[j] = stream8_early<FULL>(block, c, cols);
+    if (has_block) wb[j] = stream8_early<FULL, kStream>(block, c, cols);
   }
 #pragma unroll
   for (int j = 0; j < HELD; ++j) {
@@ -162,7 +164,7 @@ __global__ __launch_bounds__(64 * WAVES, HELD > 5 ? 3 : 4) void block_norm_kerne
   if (a.out.p) {
 #pragma unroll
     for (int j = 0; j < HELD; ++j)
-      store8_row<FULL>(a.out.p + row * a.out.stride, (j * kLanes + lane) * kChunk, cols,
+      store8_row<FULL, kStream>(a.out.p + row * a.out.stride, (j * kLanes + lane) * kChunk, cols,
                        pack8<T>(x[j]));
   }
   if (a.c_out.codes) {
@@ -185,7 +187,7 @@ __global__ __launch_bounds__(64 * WAVES, HELD > 5 ? 3 : 4) void block_norm_kerne
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         x[j][i] = FULL || c + i < cols ? (x[j][i] - m1) * r1 * w[i] + bias[i] : 0.f;
-      store8_row<FULL>(a.z.p + row * a.z.stride, c, cols, pack8<T>(x[j]));
+      store8_row<FULL, kStream>(a.z.p + row * a.z.stride, c, cols, pack8<T>(x[j]));
     }
     if (a.c_z.codes) {
 #pragma unroll
@@ -231,6 +233,8 @@ uint64_t grad_streams(uint64_t rows, uint64_t cols) {
 // Everything of a row that a thread loads.
 template <int HELD, bool FULL>
 struct GradRow {
+  static constexpr bool kStream = FULL || HELD > 1;   // as in block_norm_kernel
+
   u32x4 d[HELD], z[HELD], g[HELD];
   u32x2 out[HELD], block[HELD];
   uint32_t s_out[HELD], s_block[HELD];
@@ -260,17 +264,17 @@ struct GradRow {
     for (int j = 0; j < HELD; ++j) {
       const uint32_t chunk = j * lanes + threadIdx.x, c = chunk * kChunk;
       const uint32_t b = FULL || c < a.cols ? chunk / kQuad : 0;
-      if (a.dout.p) d[j] = stream8_early<FULL>(pd, c, a.cols);
+      if (a.dout.p) d[j] = stream8_early<FULL, kStream>(pd, c, a.cols);
       if (a.c_out.codes) {
-        z[j] = stream8_early<FULL>(pz, c, a.cols);
-        out[j] = stream_codes_early<FULL>(po, c, a.cols);
+        z[j] = stream8_early<FULL, kStream>(pz, c, a.cols);
+        out[j] = stream_codes_early<FULL, kStream>(po, c, a.cols);
         s_out[j] = so[b];
       }
       if (a.c_block.codes) {
-        block[j] = stream_codes_early<FULL>(pb, c, a.cols);
+        block[j] = stream_codes_early<FULL, kStream>(pb, c, a.cols);
         s_block[j] = sb[b];
       }
-      if (token_gate) g[j] = stream8_early<FULL>(pg, c, a.cols);
+      if (token_gate) g[j] = stream8_early<FULL, kStream>(pg, c, a.cols);
     }
   }
 
@@ -515,9 +519,9 @@ block_norm_grad_kernel(BlockNormGradLaunch a, uint64_t pad) {
         db[i] = r2 * (p[i] * w[i] - x2[j][i] * mean_vx - mean_v);
       }
       add_bias(1, j, p);
-      if (a.dres.p) store8_row<FULL>(a.dres.p + row * a.dres.stride, c, cols, pack8<T>(d));
-      if (a.dblock.p) store8_row<FULL>(a.dblock.p + row * a.dblock.stride, c, cols, pack8<T>(db));
-      if (a.dgate.p) store8_row<FULL>(a.dgate.p + row * a.dgate.stride, c, cols, pack8<T>(dg));
+      if (a.dres.p) store8_row<FULL, (FULL || HELD > 1)>(a.dres.p + row * a.dres.stride, c, cols, pack8<T>(d));
+      if (a.dblock.p) store8_row<FULL, (FULL || HELD > 1)>(a.dblock.p + row * a.dblock.stride, c, cols, pack8<T>(db));
+      if (a.dgate.p) store8_row<FULL, (FULL || HELD > 1)>(a.dgate.p + row * a.dgate.stride, c, cols, pack8<T>(dg));
       if constexpr (HELD > 2) __builtin_amdgcn_sched_barrier(0);
     }
   }
