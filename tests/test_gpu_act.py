@@ -611,3 +611,29 @@ def test_nan_tokens_stay_in_their_rows():
     assert rows[7] and int(rows.sum()) == 1
     cols = torch.isnan(dw)
     assert cols[96:128].all() and int(cols.sum()) == 32
+
+
+@pytest.mark.parametrize("h", [100, 1000, 4096, 9000])
+@pytest.mark.parametrize("gate", ["channel", "token"])
+def test_nan_of_a_block_without_a_norm_stays_out_of_its_gradient(h, gate):
+    """Without a post norm the gradient of b does not depend on b: values that the
+    checkpoint holds as NaN reach the gate's gradient only, 32 columns each."""
+    rng = np.random.default_rng(h)
+    b = acts(rng, 6, h, "fp16")
+    b[2, 5] = float("nan")
+    b[4, h - 1] = float("inf")
+    kb = _ckpt(6, h, "int8")[0]
+    Z.ckpt_write(b, kb)
+    g = acts(rng, 1 if gate == "channel" else 6, h, "fp16")
+    dout = acts(rng, 6, h, "fp16")
+    dblock = torch.empty_like(dout)
+    dgate = torch.empty(h, dtype=torch.float32, device="cuda") if gate == "channel" \
+        else torch.empty_like(dout)
+    Z.block_norm_grad(dout, None, None, kb, None, gate=g[0] if gate == "channel" else g,
+                      scale=0.5, dblock=dblock, dgate=dgate)
+    want = 0.5 * f64(dout) * f64(g)
+    close(f64(dblock), want, 2 * U * np.abs(want), "fp16", "dblock")   # two products
+    nan = np.zeros((6, h), bool)
+    nan[2, :32] = True
+    nan[4, (h - 1) // 32 * 32:] = True
+    assert np.array_equal(np.isnan(f64(dgate)), nan.any(axis=0) if gate == "channel" else nan)
