@@ -637,3 +637,12 @@ def test_nan_of_a_block_without_a_norm_stays_out_of_its_gradient(h, gate):
     nan[2, :32] = True
     nan[4, (h - 1) // 32 * 32:] = True
     assert np.array_equal(np.isnan(f64(dgate)), nan.any(axis=0) if gate == "channel" else nan)
+
+
+@pytest.mark.parametrize("t,h", [(1, 1032), (1100, 1032), (40, 1536), (1000, 1900), (7, 2048),
+                                 (300, 4104), (520, 5001), (9, 5632), (600, 6144), (3, 6145)])
+@pytest.mark.parametrize("gate", ["channel", "token", "none"])
+@pytest.mark.parametrize("inplace", [False, True])
+def test_block_norm_grad_without_biases_at_widths_of_one_chunk_a_thread(t, h, gate, inplace):
+    rng = np.random.default_rng(h + t)
+    _check_backward(_run_backward(rng, t, h, "bf16", "int8", "rms", "rms", gate, inplace=inplace))

@@ -203,30 +203,39 @@ __global__ __launch_bounds__(64 * WAVES, HELD > 5 ? 3 : 4) void block_norm_kerne
 
 uint64_t padded(uint64_t cols) { return (cols + kChunk - 1) / kChunk * kChunk; }
 
-// Chunks a thread holds, and waves of a row (at most 8).
-int grad_held(uint64_t cols) {
-  return cols <= 64 * kChunk ? 1 : cols <= 8 * 64 * 2 * kChunk ? 2 : 4;
+// Chunks a thread holds, and waves of a row (at most 8, or 12 of one chunk).  Without
+// biases one chunk a thread leaves room for 12 waves on a compute unit, against 8 of
+// two chunks, and wastes less of a row's last wave.  That pays where the second
+// chunk's lanes lie idle or a row's two-chunk waves leave some of the 8 out: 16384 x
+// 4096 elements of bf16, RMS norms and a gate a channel take 197 us where two chunks
+// take 297 with 1100 columns, 160 (191) with 1900, 164 (206) with 5000, but 229 (222)
+// with 2304, 268 (223) with 2900 and 195 (191) with 768.
+int grad_held(uint64_t cols, int sets) {
+  if (cols > 8192) return 4;
+  if (cols <= 512) return 1;
+  return sets == 3 && ((cols > 1024 && cols <= 2048) || (cols > 4096 && cols <= 6144)) ? 1 : 2;
 }
 
-int grad_waves(uint64_t cols) {
-  const uint64_t per = 64 * grad_held(cols) * kChunk;
+int grad_waves(uint64_t cols, int sets) {
+  const uint64_t per = 64 * grad_held(cols, sets) * kChunk;
   return static_cast<int>((cols + per - 1) / per);
 }
 
-bool wide_rows(uint64_t cols) { return grad_held(cols) > 2; }
+bool wide_rows(uint64_t cols) { return cols > 8192; }
 
 // Rows that are worked on at once, at most: what 256 compute units hold, with eight
-// waves each, or 12 of the smallest rows (a workgroup more would wait for the others'
-// last rows).
-uint64_t grad_wgs(uint64_t rows, uint64_t cols) {
-  const uint64_t most = 256 * ((grad_held(cols) == 1 ? 12 : 8) / grad_waves(cols));
+// waves each, or 12 of one chunk a thread (a workgroup more would wait for the
+// others' last rows).
+uint64_t grad_wgs(uint64_t rows, uint64_t cols, int sets) {
+  const uint64_t most =
+      256 * ((grad_held(cols, sets) == 1 ? 12 : 8) / grad_waves(cols, sets));
   return rows < most ? rows : most;
 }
 
 // Partial sums of each column of the parameters' gradients: one of each row that is
 // worked on, or of 128 stretches of wide rows.
-uint64_t grad_streams(uint64_t rows, uint64_t cols) {
-  if (!wide_rows(cols)) return grad_wgs(rows, cols);
+uint64_t grad_streams(uint64_t rows, uint64_t cols, int sets) {
+  if (!wide_rows(cols)) return grad_wgs(rows, cols, sets);
   return rows < 128 ? rows : 128;
 }
 
@@ -307,7 +316,11 @@ struct GradRow {
   }
 };
 
-constexpr int kGradThreads = 512;  // of a workgroup, at most
+// Threads of a workgroup, at most, and waves on each of a compute unit's four units.
+constexpr int grad_threads(int held, int sets) {
+  return 64 * (held > 1 ? 8 : sets == 3 ? 12 : 1);
+}
+constexpr int grad_fit(int held) { return held == 1 ? 3 : 2; }
 
 // One workgroup takes rows blockIdx.x, blockIdx.x + gridDim.x, ..., loading one
 // while it works on the one before, and keeps the parameters' gradients of its rows
@@ -320,19 +333,20 @@ constexpr int kGradThreads = 512;  // of a workgroup, at most
 // is known only after pre's; but it is linear in a and m, so sums of y e, y x1, y
 // and their products with x2 give it afterwards.
 //
-// Up to 8192 columns a thread holds two chunks (up to 512 columns, one), and the values of the first half
-// stay in registers for the second.  The biases' sums lie in shared memory, each
-// thread's in places of its own: with them in registers the kernel ran out and took
-// 2.5 times as long.  Wider rows (SETS == 0) take four chunks, load nothing ahead,
-// read the norms' weights from the caches, make those values again, and leave the
-// parameters' gradients to norm_sums_kernel, with mean(q x1) and [mean q] of each
-// row: kept here too, 4096 x 16384 took 520 us (RMS)
+// Up to 8192 columns a thread holds one chunk or two (grad_held), and the values of
+// the first half stay in registers for the second.  The biases' sums lie in shared
+// memory, each thread's in places of its own: with them in registers the kernel ran
+// out and took 2.5 times as long.  16384 x 4096 bf16 with RMS norms and a gate a
+// channel takes 128 us and its join 5, 5.1 TB/s.  Wider rows (SETS == 0) take four
+// chunks, load nothing ahead, read the norms' weights from the caches, make those
+// values again, and leave the parameters' gradients to norm_sums_kernel, with
+// mean(q x1) and [mean q] of each row: kept here too, 4096 x 16384 took 520 us (RMS)
 // and 850 (layer norms) where it now takes 342 and 355.
 template <typename T, int FMT, int HELD, int SETS, bool FULL>
-__global__ __launch_bounds__(HELD == 1 ? 64 : kGradThreads, HELD == 1 ? 3 : 2) void
+__global__ __launch_bounds__(grad_threads(HELD, SETS), grad_fit(HELD)) void
 block_norm_grad_kernel(BlockNormGradLaunch a, uint64_t pad) {
   constexpr bool kAhead = HELD <= 2, kKeep = kAhead;
-  constexpr int kMaxWaves = HELD == 1 ? 1 : kGradThreads / 64;
+  constexpr int kMaxWaves = grad_threads(HELD, SETS) / 64;
   constexpr int kRowSums = 8;
   __shared__ float red[2 * kMaxWaves * kRowSums];
   int turn = 0;
@@ -730,8 +744,8 @@ void forward(const BlockNormLaunch& a, hipStream_t stream) {
 template <typename T, int FMT>
 void backward(const BlockNormGradLaunch& a, int sets, uint32_t wgs, hipStream_t stream) {
   const uint64_t pad = padded(a.cols);
-  const int held = grad_held(a.cols);
-  const uint32_t threads = 64 * grad_waves(a.cols);
+  const int held = grad_held(a.cols, sets);
+  const uint32_t threads = 64 * grad_waves(a.cols, sets);
   const bool full = a.cols == static_cast<uint32_t>(held) * threads * kChunk;
   const uint32_t shared = 4 * held * threads * sizeof(f32x4);   // at most 64 KiB
   if (held <= 2) {
@@ -762,7 +776,7 @@ void backward(const BlockNormGradLaunch& a, int sets, uint32_t wgs, hipStream_t 
     if (a.partial)
       norm_sums_kernel<T, FMT>
           <<<dim3((a.cols + kSumCols - 1) / kSumCols,
-                  static_cast<uint32_t>(grad_streams(a.rows, a.cols))),
+                  static_cast<uint32_t>(grad_streams(a.rows, a.cols, sets))),
              kSumThreads, 0, stream>>>(a, pad);
     if (a.partial && replaces) {
       BlockNormGradLaunch last = a;
@@ -776,7 +790,8 @@ void backward(const BlockNormGradLaunch& a, int sets, uint32_t wgs, hipStream_t 
 
 uint64_t norm_grad_workspace(uint64_t rows, uint64_t cols) {
   const uint64_t means = wide_rows(cols) ? rows * 2 : 0;
-  return (grad_streams(rows, cols) * padded(cols) * kSums + means) * sizeof(float);
+  const uint64_t three = grad_streams(rows, cols, 3), five = grad_streams(rows, cols, 5);
+  return ((three > five ? three : five) * padded(cols) * kSums + means) * sizeof(float);
 }
 
 hipError_t launch_block_norm(const BlockNormLaunch& a, hipStream_t stream) {
@@ -790,13 +805,13 @@ hipError_t launch_block_norm_grad(const BlockNormGradLaunch& in, hipStream_t str
   bool any = false;
   for (void* p : a.sums) any = any || p != nullptr;
   if (!any) a.partial = nullptr;
-  const uint32_t wgs = static_cast<uint32_t>(grad_wgs(a.rows, a.cols));
-  const uint64_t streams = grad_streams(a.rows, a.cols);
-  a.means = a.partial && wide_rows(a.cols) ? a.partial + streams * padded(a.cols) * kSums : nullptr;
   // layer norms need the row sums of the biases' path too
   const bool five = a.sums[kDbPre] || a.sums[kDbPost] || a.pre.kind == ZERO_NORM_LAYER ||
                     a.post.kind == ZERO_NORM_LAYER;
   const int sets = five ? 5 : 3;
+  const uint32_t wgs = static_cast<uint32_t>(grad_wgs(a.rows, a.cols, sets));
+  const uint64_t streams = grad_streams(a.rows, a.cols, sets);
+  a.means = a.partial && wide_rows(a.cols) ? a.partial + streams * padded(a.cols) * kSums : nullptr;
   if (wgs) {
     if (a.dtype == kF16) {
       if (a.format == kInt8) backward<F16, kInt8>(a, sets, wgs, stream);
