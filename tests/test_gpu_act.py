@@ -646,3 +646,20 @@ def test_nan_of_a_block_without_a_norm_stays_out_of_its_gradient(h, gate):
 def test_block_norm_grad_without_biases_at_widths_of_one_chunk_a_thread(t, h, gate, inplace):
     rng = np.random.default_rng(h + t)
     _check_backward(_run_backward(rng, t, h, "bf16", "int8", "rms", "rms", gate, inplace=inplace))
+
+
+@pytest.mark.parametrize("t,h", [(700, 2560), (5, 3584), (260, 4608), (2, 5120), (270, 5632),
+                                 (33, 6144)])
+@pytest.mark.parametrize("kind,gate", [("rms", "channel"), ("layer", "token"),
+                                       ("layer", "channel")])
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_block_norm_grad_at_widths_of_whole_waves(t, h, kind, gate, dtype):
+    rng = np.random.default_rng(h + t)
+    _check_backward(_run_backward(rng, t, h, dtype, "int8", kind, kind, gate, inplace=True))
+
+
+@pytest.mark.parametrize("t,h", [(2100, 1040), (300, 4095), (260, 8192), (260, 8190)])
+@pytest.mark.parametrize("gate", ["channel", "token"])
+def test_block_norm_grad_of_layer_norms_over_bf16(t, h, gate):
+    rng = np.random.default_rng(h + t)
+    _check_backward(_run_backward(rng, t, h, "bf16", "e4m3", "layer", "layer", gate))

@@ -63,7 +63,7 @@ __device__ __forceinline__ void emit(const Ckpt& c, uint64_t row, uint32_t chunk
 // Up to eight chunks a thread: rows of up to 4096 columns take one wave, and its
 // sums no barrier.  Nothing is kept from row to row; many rows at once on a compute
 // unit hide the loads, and the norms' weights come from the caches.  16384 x 4096
-// bf16 with a gate a channel takes 111 us, 4.8 TB/s (165 us, 4.5 TB/s with all three
+// bf16 with a gate a channel takes 97 us, 5.5 TB/s (143 us, 5.2 TB/s with all three
 // checkpoints).
 template <typename T, int WAVES, int HELD, bool FULL>
 __global__ __launch_bounds__(64 * WAVES, HELD > 5 ? 3 : 4) void block_norm_kernel(BlockNormLaunch a,
@@ -203,17 +203,22 @@ __global__ __launch_bounds__(64 * WAVES, HELD > 5 ? 3 : 4) void block_norm_kerne
 
 uint64_t padded(uint64_t cols) { return (cols + kChunk - 1) / kChunk * kChunk; }
 
-// Chunks a thread holds, and waves of a row (at most 8, or 12 of one chunk).  Without
-// biases one chunk a thread leaves room for 12 waves on a compute unit, against 8 of
-// two chunks, and wastes less of a row's last wave.  That pays where the second
-// chunk's lanes lie idle or a row's two-chunk waves leave some of the 8 out: 16384 x
-// 4096 elements of bf16, RMS norms and a gate a channel take 197 us where two chunks
-// take 297 with 1100 columns, 160 (191) with 1900, 164 (206) with 5000, but 229 (222)
-// with 2304, 268 (223) with 2900 and 195 (191) with 768.
+// Chunks a thread holds, and waves of a row (at most 8, or 12 of one chunk).  One
+// chunk a thread leaves room for 12 waves on a compute unit, against 8 of two chunks,
+// and wastes less of a row's last wave; two leave each wave more loads in flight.
+// Measured with 16384 x 4096 elements and a gate a channel, one chunk (two):
+//   RMS norms, bf16:   768 columns 195 (191) us, 1100: 197 (297), 1900: 160 (191),
+//     2304: 229 (222), 2560: 174 (193), 2900: 268 (223), 4096: 149 (144), 5000: 164 (206),
+//     5120: 146 (151)
+//   layer norms, fp16: 1100 columns 600 (336) us, 2560: 256 (238), 4096: 188 (151),
+//     4608: 199 (260), 5000: 300 (252), 5120: 190 (208); their rows that end inside a
+//     wave run out of registers with one chunk
 int grad_held(uint64_t cols, int sets) {
+  const bool whole = cols % (64 * kChunk) == 0;
   if (cols > 8192) return 4;
   if (cols <= 512) return 1;
-  return sets == 3 && ((cols > 1024 && cols <= 2048) || (cols > 4096 && cols <= 6144)) ? 1 : 2;
+  if (cols >= 4096) return cols > 4096 && cols <= 6144 && (sets == 3 || whole) ? 1 : 2;
+  return sets == 3 && cols > 1024 && (whole || cols <= 2048) ? 1 : 2;
 }
 
 int grad_waves(uint64_t cols, int sets) {
@@ -317,9 +322,11 @@ struct GradRow {
 };
 
 // Threads of a workgroup, at most, and waves on each of a compute unit's four units.
-constexpr int grad_threads(int held, int sets) {
-  return 64 * (held > 1 ? 8 : sets == 3 ? 12 : 1);
+constexpr int grad_threads(int held, int sets, bool full) {
+  return 64 * (held > 1 ? 8 : sets == 3 || full ? 12 : 1);
 }
+template <typename T>
+constexpr bool rows_shared(int sets) { return sets == 5 && T::kType == kBf16; }
 constexpr int grad_fit(int held) { return held == 1 ? 3 : 2; }
 
 // One workgroup takes rows blockIdx.x, blockIdx.x + gridDim.x, ..., loading one
@@ -336,17 +343,20 @@ constexpr int grad_fit(int held) { return held == 1 ? 3 : 2; }
 // Up to 8192 columns a thread holds one chunk or two (grad_held), and the values of
 // the first half stay in registers for the second.  The biases' sums lie in shared
 // memory, each thread's in places of its own: with them in registers the kernel ran
-// out and took 2.5 times as long.  16384 x 4096 bf16 with RMS norms and a gate a
+// out and took 2.5 times as long.  In bf16, whose values take a register each once
+// unpacked (fp16 ones are read by the multiply-adds as they are), the norms' rows lie
+// there too: layer norms over 4000 columns take 174 us instead of 271, over 4096 154
+// instead of 186, where fp16 takes 175 and 152 without and 176 and 155 with.  16384 x 4096 bf16 with RMS norms and a gate a
 // channel takes 128 us and its join 5, 5.1 TB/s.  Wider rows (SETS == 0) take four
 // chunks, load nothing ahead, read the norms' weights from the caches, make those
 // values again, and leave the parameters' gradients to norm_sums_kernel, with
 // mean(q x1) and [mean q] of each row: kept here too, 4096 x 16384 took 520 us (RMS)
 // and 850 (layer norms) where it now takes 342 and 355.
 template <typename T, int FMT, int HELD, int SETS, bool FULL>
-__global__ __launch_bounds__(grad_threads(HELD, SETS), grad_fit(HELD)) void
+__global__ __launch_bounds__(grad_threads(HELD, SETS, FULL), grad_fit(HELD)) void
 block_norm_grad_kernel(BlockNormGradLaunch a, uint64_t pad) {
   constexpr bool kAhead = HELD <= 2, kKeep = kAhead;
-  constexpr int kMaxWaves = grad_threads(HELD, SETS) / 64;
+  constexpr int kMaxWaves = grad_threads(HELD, SETS, FULL) / 64;
   constexpr int kRowSums = 8;
   __shared__ float red[2 * kMaxWaves * kRowSums];
   int turn = 0;
@@ -380,10 +390,32 @@ block_norm_grad_kernel(BlockNormGradLaunch a, uint64_t pad) {
     if (a.post.b.p) b2[j] = load8_row<FULL>(a.post.b.p, c, cols);
     if (a.gate.p && !token_gate) gc[j] = load8_row<FULL>(a.gate.p, c, cols);
   };
+  // SETS == 5: 4 HELD vectors of sums of each thread, and kShared: as many of the rows
+  extern __shared__ f32x4 shared[];
+  constexpr bool kShared = rows_shared<T>(SETS);
+  auto row_at = [&](int which, int j, uint32_t thread) -> u32x4& {
+    return reinterpret_cast<u32x4*>(shared)[(4 * HELD + which * HELD + j) * lanes + thread];
+  };
   if constexpr (kAhead) {
 #pragma unroll
-    for (int j = 0; j < HELD; ++j) load_rows(j);
+    for (int j = 0; j < HELD; ++j) {
+      load_rows(j);
+      if constexpr (kShared) {
+        row_at(0, j, threadIdx.x) = w1[j];
+        row_at(1, j, threadIdx.x) = w2[j];
+        row_at(2, j, threadIdx.x) = b2[j];
+        row_at(3, j, threadIdx.x) = gc[j];
+      }
+    }
   }
+  auto fetch_rows = [&](int j) {   // what is not used of them is not read
+    uint32_t thread = threadIdx.x;
+    forget(thread);
+    w1[j] = row_at(0, j, thread);
+    w2[j] = row_at(1, j, thread);
+    b2[j] = row_at(2, j, thread);
+    gc[j] = row_at(3, j, thread);
+  };
   float sum[3][SETS ? HELD : 1][8];   // of the weights and the gate
   constexpr int kGate = 2;
   if constexpr (SETS > 0) {
@@ -394,9 +426,8 @@ block_norm_grad_kernel(BlockNormGradLaunch a, uint64_t pad) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) sum[s][j][i] = 0.f;
   }
-  extern __shared__ f32x4 bias_sums[];   // SETS == 5: 4 HELD of each thread
   auto bias_at = [&](int set, int j, int half) -> f32x4& {
-    return bias_sums[((set * HELD + j) * 2 + half) * lanes + threadIdx.x];
+    return shared[((set * HELD + j) * 2 + half) * lanes + threadIdx.x];
   };
   if constexpr (SETS == 5) {
 #pragma unroll
@@ -420,6 +451,7 @@ block_norm_grad_kernel(BlockNormGradLaunch a, uint64_t pad) {
       r = next;
 #pragma unroll
       for (int j = 0; j < HELD; ++j) {
+        if constexpr (kShared) continue;
         forget(w1[j]);
         forget(w2[j]);
         forget(b2[j]);
@@ -461,6 +493,7 @@ block_norm_grad_kernel(BlockNormGradLaunch a, uint64_t pad) {
     for (int j = 0; j < HELD; ++j) {
       float z[8], q[8], g[8], w[8];
       if constexpr (!kAhead) load_rows(j);
+      if constexpr (kShared) fetch_rows(j);
       front(j, z, q);
       gates(j, g);
       unpack8<T>(w2[j], w);
@@ -507,6 +540,7 @@ block_norm_grad_kernel(BlockNormGradLaunch a, uint64_t pad) {
 #pragma unroll
     for (int j = 0; j < HELD; ++j) {
       const uint32_t c = (j * lanes + threadIdx.x) * kChunk;
+      if constexpr (kShared) fetch_rows(j);
       forget(w2[j]);
       forget(gc[j]);
       forget(r.g[j]);
@@ -720,7 +754,7 @@ void forward_rows(const BlockNormLaunch& a, hipStream_t stream) {
 template <typename T>
 void forward(const BlockNormLaunch& a, hipStream_t stream) {
   // the least waves whose threads hold the row in up to eight chunks, and the least
-  // chunks: 5120 columns in 2 x 5 take 160 us where 2 x 8 takes 335
+  // chunks: 16384 x 5120 in 2 x 5 takes 115 us where 2 x 8 took 335
   const uint32_t per = 64 * kChunk;
   const uint32_t waves = a.cols <= 8 * per ? 1 : a.cols <= 16 * per ? 2 : 4;
   const uint32_t held = (a.cols + waves * per - 1) / (waves * per);
@@ -747,7 +781,8 @@ void backward(const BlockNormGradLaunch& a, int sets, uint32_t wgs, hipStream_t 
   const int held = grad_held(a.cols, sets);
   const uint32_t threads = 64 * grad_waves(a.cols, sets);
   const bool full = a.cols == static_cast<uint32_t>(held) * threads * kChunk;
-  const uint32_t shared = 4 * held * threads * sizeof(f32x4);   // at most 64 KiB
+  const uint32_t shared =   // at most 128 KiB
+      (rows_shared<T>(sets) ? 8 : 4) * held * threads * sizeof(f32x4);
   if (held <= 2) {
     auto run = [&](auto h) {
       constexpr int kHeld = decltype(h)::value;
