@@ -3,10 +3,11 @@
 // wavefront.
 //
 // The checkpoint format: rows of 8-bit codes in blocks of 32 columns, one scale
-// byte b per block that stands for 2^(b - 127), or for NaN if b = 255.  A scale that is a power of two makes every held value exactly
-// representable in the 16-bit type it came from (7 significant bits of an int8
-// code, 4 of an e4m3 code, against 11 of fp16 and 8 of bf16), so whatever reads
-// a checkpoint back rounds nothing a second time.
+// byte b per block that stands for 2^(b - 127), or for NaN if b = 255.  A scale that
+// is a power of two makes every held value exactly representable in the 16-bit type
+// it came from (7 significant bits of an int8 code, 4 of an e4m3 code, against 11 of
+// fp16 and 8 of bf16), so whatever reads a checkpoint back rounds nothing a second
+// time.
 #ifndef ZERO_ACT_FORMAT_H_
 #define ZERO_ACT_FORMAT_H_
 

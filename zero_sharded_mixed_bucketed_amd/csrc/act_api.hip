@@ -117,7 +117,8 @@ int check_norm(const char* name, const zero_norm_t& n) {
     return ZERO_OK;
   }
   // in fp32 too: a smaller eps would let a row of zeros divide by zero
-  if (!isfinite(n.eps) || !(static_cast<float>(n.eps) > 0.f) || !isfinite(static_cast<float>(n.eps)))
+  const float eps = static_cast<float>(n.eps);
+  if (!isfinite(n.eps) || !(eps > 0.f) || !isfinite(eps))
     return fail(ZERO_E_INVAL, "%s: eps must be finite and > 0 in fp32", name);
   if (!aligned(n.weight, 2) || !aligned(n.bias, 2))
     return fail(ZERO_E_ALIGN, "%s: weight or bias is not 2-byte aligned", name);

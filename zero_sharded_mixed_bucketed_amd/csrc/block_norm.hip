@@ -66,8 +66,8 @@ __device__ __forceinline__ void emit(const Ckpt& c, uint64_t row, uint32_t chunk
 // bf16 with a gate a channel takes 97 us, 5.5 TB/s (143 us, 5.2 TB/s with all three
 // checkpoints).
 template <typename T, int WAVES, int HELD, bool FULL>
-__global__ __launch_bounds__(64 * WAVES, HELD > 5 ? 3 : 4) void block_norm_kernel(BlockNormLaunch a,
-                                                                   uint64_t row0) {
+__global__ __launch_bounds__(64 * WAVES, HELD > 5 ? 3 : 4) void block_norm_kernel(
+    BlockNormLaunch a, uint64_t row0) {
   constexpr uint32_t kLanes = 64 * WAVES;
   // short rows that end inside a line share it, and meet in the caches
   constexpr bool kStream = FULL || WAVES * HELD > 1;
@@ -138,7 +138,10 @@ __global__ __launch_bounds__(64 * WAVES, HELD > 5 ? 3 : 4) void block_norm_kerne
 
   float m2 = 0.f, r2 = 1.f, m1 = 0.f, r1 = 1.f;
   if (a.post.kind != ZERO_NORM_NONE)
-    stats([&](int j, float (&x)[8]) { forget(wb[j]); unpack8<T>(wb[j], x); }, a.post.kind, a.post.eps, &m2, &r2);
+    stats([&](int j, float (&x)[8]) {
+      forget(wb[j]);
+      unpack8<T>(wb[j], x);
+    }, a.post.kind, a.post.eps, &m2, &r2);
   if (a.c_block.codes) {
 #pragma unroll
     for (int j = 0; j < HELD; ++j) emit<T>(a.c_block, row, j * kLanes + lane, cols, wb[j]);
@@ -344,14 +347,15 @@ constexpr int grad_fit(int held) { return held == 1 ? 3 : 2; }
 // the first half stay in registers for the second.  The biases' sums lie in shared
 // memory, each thread's in places of its own: with them in registers the kernel ran
 // out and took 2.5 times as long.  In bf16, whose values take a register each once
-// unpacked (fp16 ones are read by the multiply-adds as they are), the norms' rows lie
-// there too: layer norms over 4000 columns take 174 us instead of 271, over 4096 154
-// instead of 186, where fp16 takes 175 and 152 without and 176 and 155 with.  16384 x 4096 bf16 with RMS norms and a gate a
-// channel takes 128 us and its join 5, 5.1 TB/s.  Wider rows (SETS == 0) take four
-// chunks, load nothing ahead, read the norms' weights from the caches, make those
-// values again, and leave the parameters' gradients to norm_sums_kernel, with
-// mean(q x1) and [mean q] of each row: kept here too, 4096 x 16384 took 520 us (RMS)
-// and 850 (layer norms) where it now takes 342 and 355.
+// unpacked (fp16 ones are read by the multiply-adds as they are), the norms' rows
+// lie there too: layer norms over 4000 columns take 174 us instead of 271, over
+// 4096 154 instead of 186, where fp16 takes 175 and 152 without and 176 and 155
+// with.  16384 x 4096 bf16 with RMS norms and a gate a channel takes 128 us and its
+// join 5, 5.1 TB/s.  Wider rows (SETS == 0) take four chunks, load nothing ahead,
+// read the norms' weights from the caches, make those values again, and leave the
+// parameters' gradients to norm_sums_kernel, with mean(q x1) and [mean q] of each
+// row: kept here too, 4096 x 16384 took 520 us (RMS) and 850 (layer norms) where it
+// now takes 342 and 355.
 template <typename T, int FMT, int HELD, int SETS, bool FULL>
 __global__ __launch_bounds__(grad_threads(HELD, SETS, FULL), grad_fit(HELD)) void
 block_norm_grad_kernel(BlockNormGradLaunch a, uint64_t pad) {
@@ -573,9 +577,13 @@ block_norm_grad_kernel(BlockNormGradLaunch a, uint64_t pad) {
         db[i] = r2 * (p[i] * w[i] - along * mean_vx - mean_v);
       }
       add_bias(1, j, p);
-      if (a.dres.p) store8_row<FULL, (FULL || HELD > 1)>(a.dres.p + row * a.dres.stride, c, cols, pack8<T>(d));
-      if (a.dblock.p) store8_row<FULL, (FULL || HELD > 1)>(a.dblock.p + row * a.dblock.stride, c, cols, pack8<T>(db));
-      if (a.dgate.p) store8_row<FULL, (FULL || HELD > 1)>(a.dgate.p + row * a.dgate.stride, c, cols, pack8<T>(dg));
+      constexpr bool kStream = GradRow<HELD, FULL>::kStream;
+      if (a.dres.p)
+        store8_row<FULL, kStream>(a.dres.p + row * a.dres.stride, c, cols, pack8<T>(d));
+      if (a.dblock.p)
+        store8_row<FULL, kStream>(a.dblock.p + row * a.dblock.stride, c, cols, pack8<T>(db));
+      if (a.dgate.p)
+        store8_row<FULL, kStream>(a.dgate.p + row * a.dgate.stride, c, cols, pack8<T>(dg));
       if constexpr (HELD > 2) __builtin_amdgcn_sched_barrier(0);
     }
   }
@@ -804,7 +812,8 @@ void backward(const BlockNormGradLaunch& a, int sets, uint32_t wgs, hipStream_t 
     };
     // outputs that replace inputs wait until the sums have read those: the means are
     // then made first, by a pass that stores nothing else
-    const bool replaces = (a.dres.p && a.dres.p == a.dout.p) || (a.dblock.p && a.dblock.p == a.dz.p);
+    const bool replaces =
+        (a.dres.p && a.dres.p == a.dout.p) || (a.dblock.p && a.dblock.p == a.dz.p);
     BlockNormGradLaunch first = a;
     if (a.partial && replaces) first.dres.p = first.dblock.p = first.dgate.p = nullptr;
     rows(first);
