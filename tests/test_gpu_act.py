@@ -663,3 +663,48 @@ def test_block_norm_grad_at_widths_of_whole_waves(t, h, kind, gate, dtype):
 def test_block_norm_grad_of_layer_norms_over_bf16(t, h, gate):
     rng = np.random.default_rng(h + t)
     _check_backward(_run_backward(rng, t, h, "bf16", "e4m3", "layer", "layer", gate))
+
+
+def test_block_norm_of_more_rows_than_one_launch():
+    """2^26 + 5 rows of 72 columns, a wave each: 2^32 threads and more."""
+    t, h = (1 << 26) + 5, 72
+    res = torch.zeros((t, h), dtype=torch.float16, device="cuda")
+    rows = torch.tensor([0, 1, (1 << 26) - 2, (1 << 26) - 1, 1 << 26, t - 1], device="cuda")
+    res[rows] = torch.randn((6, h), device="cuda").half()
+    b = torch.full((h,), 0.5, dtype=torch.float16, device="cuda")
+    z = torch.zeros_like(res)
+    stats = torch.empty((t, 4), dtype=torch.float32, device="cuda")
+    Z.block_norm(res, None, None, z, stats, pre=Z.Norm(Z.NORM_RMS, 1e-5, None, b))
+    spec = ("rms", 1e-5, None, f64(b))
+    _check_forward({"z": z[rows], "stats": stats[rows]}, f64(res[rows]), None,
+                   ("none", 0, None, None), spec, None, 1.0, "fp16", "long")
+    live = torch.zeros(t, dtype=torch.bool, device="cuda")
+    live[rows] = True
+    bad = 0
+    for lo in range(0, t, 1 << 24):            # rows of zeros give the bias
+        part = (z[lo:lo + (1 << 24)] != b).any(dim=1)
+        bad += int((part & ~live[lo:lo + (1 << 24)]).sum())
+    assert bad == 0
+
+
+def test_checkpoint_of_more_rows_than_one_launch():
+    """2^32 + 17 rows of one column, 16 rows a piece of a wave."""
+    t = (1 << 32) + 17
+    x = torch.zeros((t, 1), dtype=torch.float16, device="cuda")
+    rows = torch.tensor([0, 1, (1 << 32) - 257, (1 << 32) - 256, 1 << 32, t - 1], device="cuda")
+    x[rows] = torch.randn((6, 1), device="cuda").half()
+    codes = torch.full((t, 1), 0x55, dtype=torch.uint8, device="cuda")
+    k = Z.Ckpt(codes, torch.full_like(codes, 0xAA), Z.CKPT_INT8)
+    Z.ckpt_write(x, k)
+    want_c, want_s = oact.store(f64(x[rows]), "int8", "fp16")
+    assert np.array_equal(codes[rows].cpu().numpy(), want_c)
+    assert np.array_equal(k.scales[rows].cpu().numpy(), want_s)
+    for lo in range(0, t, 1 << 30):            # zeros elsewhere, at the least scale
+        part = slice(lo, min(t, lo + (1 << 30)))
+        inside = int(((rows >= part.start) & (rows < part.stop)).sum())
+        assert int((codes[part] != 0).sum()) == inside
+        assert int((k.scales[part] != 1).sum()) == inside
+    x.fill_(7.0)
+    Z.ckpt_read(k, x)
+    assert np.array_equal(f64(x[rows]), oact.held(want_c, want_s, "int8"))
+    assert sum(int((x[lo:lo + (1 << 30)] != 0).sum()) for lo in range(0, t, 1 << 30)) == 6

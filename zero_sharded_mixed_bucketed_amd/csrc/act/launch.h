@@ -14,6 +14,10 @@ int ok();
 
 namespace act {
 
+// Workgroups of one launch, at most: HIP takes fewer than 2^32 threads in a grid's
+// dimension.
+constexpr uint64_t most_workgroups(uint32_t threads) { return 0xFFFFFFFFull / threads; }
+
 // 8-bit checkpoint rows in device memory; codes == nullptr: none.
 struct Ckpt {
   uint8_t* codes;

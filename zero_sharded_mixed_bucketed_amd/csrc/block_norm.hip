@@ -748,39 +748,42 @@ __global__ __launch_bounds__(64 * kJoinWaves) void join_sums_kernel(JoinArgs a) 
 // ------------------------------------------------------------ launches
 
 template <typename T, int WAVES, int HELD>
-void forward_rows(const BlockNormLaunch& a, hipStream_t stream) {
-  constexpr uint64_t kMost = 1ull << 30;   // rows of a launch
+hipError_t forward_rows(const BlockNormLaunch& a, hipStream_t stream) {
+  constexpr uint64_t kMost = most_workgroups(64 * WAVES);   // rows of a launch
   const bool full = a.cols == 64u * WAVES * HELD * kChunk;
   for (uint64_t row0 = 0; row0 < a.rows; row0 += kMost) {
     const uint64_t left = a.rows - row0;
     const uint32_t wgs = static_cast<uint32_t>(left < kMost ? left : kMost);
     if (full) block_norm_kernel<T, WAVES, HELD, true><<<wgs, 64 * WAVES, 0, stream>>>(a, row0);
     else block_norm_kernel<T, WAVES, HELD, false><<<wgs, 64 * WAVES, 0, stream>>>(a, row0);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
   }
+  return hipSuccess;
 }
 
 template <typename T>
-void forward(const BlockNormLaunch& a, hipStream_t stream) {
+hipError_t forward(const BlockNormLaunch& a, hipStream_t stream) {
   // the least waves whose threads hold the row in up to eight chunks, and the least
   // chunks: 16384 x 5120 in 2 x 5 takes 115 us where 2 x 8 took 335
   const uint32_t per = 64 * kChunk;
   const uint32_t waves = a.cols <= 8 * per ? 1 : a.cols <= 16 * per ? 2 : 4;
   const uint32_t held = (a.cols + waves * per - 1) / (waves * per);
   if (waves == 1) {
-    if (held <= 1) forward_rows<T, 1, 1>(a, stream);
-    else if (held <= 2) forward_rows<T, 1, 2>(a, stream);
-    else if (held <= 4) forward_rows<T, 1, 4>(a, stream);
-    else if (held <= 6) forward_rows<T, 1, 6>(a, stream);
-    else forward_rows<T, 1, 8>(a, stream);
-  } else if (waves == 2) {
-    if (held <= 5) forward_rows<T, 2, 5>(a, stream);
-    else if (held <= 6) forward_rows<T, 2, 6>(a, stream);
-    else forward_rows<T, 2, 8>(a, stream);
-  } else {
-    if (held <= 5) forward_rows<T, 4, 5>(a, stream);
-    else if (held <= 6) forward_rows<T, 4, 6>(a, stream);
-    else forward_rows<T, 4, 8>(a, stream);
+    if (held <= 1) return forward_rows<T, 1, 1>(a, stream);
+    if (held <= 2) return forward_rows<T, 1, 2>(a, stream);
+    if (held <= 4) return forward_rows<T, 1, 4>(a, stream);
+    if (held <= 6) return forward_rows<T, 1, 6>(a, stream);
+    return forward_rows<T, 1, 8>(a, stream);
   }
+  if (waves == 2) {
+    if (held <= 5) return forward_rows<T, 2, 5>(a, stream);
+    if (held <= 6) return forward_rows<T, 2, 6>(a, stream);
+    return forward_rows<T, 2, 8>(a, stream);
+  }
+  if (held <= 5) return forward_rows<T, 4, 5>(a, stream);
+  if (held <= 6) return forward_rows<T, 4, 6>(a, stream);
+  return forward_rows<T, 4, 8>(a, stream);
 }
 
 template <typename T, int FMT>
@@ -839,9 +842,7 @@ uint64_t norm_grad_workspace(uint64_t rows, uint64_t cols) {
 }
 
 hipError_t launch_block_norm(const BlockNormLaunch& a, hipStream_t stream) {
-  if (a.dtype == kF16) forward<F16>(a, stream);
-  else forward<Bf16>(a, stream);
-  return hipGetLastError();
+  return a.dtype == kF16 ? forward<F16>(a, stream) : forward<Bf16>(a, stream);
 }
 
 hipError_t launch_block_norm_grad(const BlockNormGradLaunch& in, hipStream_t stream) {

@@ -21,7 +21,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kUnits = 4;                        // units a wave takes, loaded together
-constexpr uint64_t kMostUnits = 1ull << 31;      // of a launch
+constexpr uint64_t kMostUnits = most_workgroups(kThreads) * kWaves * kUnits;  // of a launch
 
 // A wave's unit: 512 columns of a row (64 lanes of eight), or, where rows have at
 // most 256 columns, 64 / lanes whole rows, lanes the least power of two that holds

@@ -510,8 +510,12 @@ uint64_t weight_grad_workspace(uint64_t rows, uint64_t k, uint64_t n) {
 
 hipError_t launch_weight_grad(const WeightGradLaunch& a, hipStream_t stream) {
   const Plan p = plan(a.rows, a.k, a.n);
-  const uint64_t wgs = p.tn * p.tk * p.splits;   // at most 2^30 tiles of 128 x 128
-  if (wgs > 0x7FFFFFFFull) return hipErrorInvalidConfiguration;
+  const uint64_t wgs = p.tn * p.tk * p.splits;
+  const uint64_t joins = (a.n * ((a.k + kChunk - 1) / kChunk) + kThreads - 1) / kThreads;
+  // past what one launch holds dw would take 2^38 elements, or its splits' sums 2^38
+  // bytes beside it: more memory than the chip has
+  constexpr uint64_t kMost = most_workgroups(kThreads);
+  if (wgs > kMost || (p.splits > 1 && joins > kMost)) return hipErrorInvalidConfiguration;
   const uint64_t of_y = safe_rows(a.rows, a.n, a.dy_stride);
   const uint64_t of_x = safe_rows(a.rows, a.k, a.x.code_stride);
   uint64_t safe = of_y < of_x ? of_y : of_x;
@@ -527,7 +531,6 @@ hipError_t launch_weight_grad(const WeightGradLaunch& a, hipStream_t stream) {
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
-  const uint64_t joins = (a.n * ((a.k + kChunk - 1) / kChunk) + kThreads - 1) / kThreads;
   weight_grad_join_kernel<<<static_cast<uint32_t>(joins), kThreads, 0, stream>>>(
       a, static_cast<uint32_t>(p.splits));
   return hipGetLastError();
