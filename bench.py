@@ -585,7 +585,8 @@ def environment(torch, dev):
             "rocm": read_text("/opt/rocm/.info/version"),
             "amdgpu_driver": read_text("/sys/module/amdgpu/version"),
             "host_cpu_model": host_cpu_model(),
-            "library_sources_sha256": library_sources_sha256()}
+            "library_sources_sha256": library_sources_sha256(),
+            "library_tree_sha256": library_tree_sha256()}
 
 
 def read_text(path):
@@ -610,7 +611,8 @@ def host_cpu_model():
 
 
 def library_sources_sha256():
-    """One digest over the library's header and HIP sources: which build ran."""
+    """One digest over include/ and the top level of csrc/ (names and bytes);
+    library_tree_sha256 also covers what lies in folders below."""
     import hashlib
     here = os.path.dirname(os.path.abspath(__file__))
     h = hashlib.sha256()
@@ -621,6 +623,24 @@ def library_sources_sha256():
     for path in paths:
         h.update(os.path.basename(path).encode())
         h.update(open(path, "rb").read())
+    return h.hexdigest()
+
+
+def library_tree_sha256(root=None):
+    """One digest over every header and HIP source that libzero.so is built from,
+    at any depth (paths under include/ and csrc/, and bytes): which build ran."""
+    import hashlib
+    root = root or os.path.dirname(os.path.abspath(__file__))
+    h = hashlib.sha256()
+    for d in ("include", os.path.join("zero_sharded_mixed_bucketed_amd", "csrc")):
+        paths = []
+        for base, _, files in os.walk(os.path.join(root, d)):
+            paths += [os.path.join(base, f) for f in files if f.endswith((".h", ".hip"))]
+        for path in sorted(paths):
+            with open(path, "rb") as f:
+                data = f.read()
+            h.update(f"{os.path.relpath(path, root)}\n{len(data)}\n".encode())
+            h.update(data)
     return h.hexdigest()
 
 

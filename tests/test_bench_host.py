@@ -7,6 +7,7 @@ import hashlib
 import importlib.util
 import os
 import re
+import shutil
 import subprocess
 import sys
 
@@ -124,6 +125,29 @@ def test_library_sources_digest_tracks_the_sources(tmp_path):
                 h.update(f.encode())
                 h.update(open(os.path.join(d, f), "rb").read())
     assert d1 == h.hexdigest()
+
+
+@pytest.mark.parametrize("rel", ["include/zero.h", "csrc/act/format.h", "csrc/act/launch.h",
+                                 "csrc/block_norm.hip"])
+def test_library_tree_digest_tracks_sources_at_any_depth(tmp_path, rel):
+    """The build's identity changes with every file that libzero.so is built from,
+    the headers below csrc/ among them, and with its name."""
+    b = _bench()
+    pkg = "zero_sharded_mixed_bucketed_amd"
+    for d in ("include", os.path.join(pkg, "csrc")):
+        shutil.copytree(os.path.join(ROOT, d), tmp_path / d)
+    d1 = b.library_tree_sha256()
+    assert len(d1) == 64 and d1 == b.library_tree_sha256(str(tmp_path))
+    path = tmp_path / (rel if rel.startswith("include") else os.path.join(pkg, rel))
+    text = path.read_bytes()
+    path.write_bytes(text + b"\n")
+    assert b.library_tree_sha256(str(tmp_path)) != d1
+    path.write_bytes(text)
+    assert b.library_tree_sha256(str(tmp_path)) == d1
+    path.rename(path.with_name("other_" + path.name))
+    assert b.library_tree_sha256(str(tmp_path)) != d1
+    src = open(os.path.join(ROOT, "bench.py")).read()
+    assert '"library_tree_sha256": library_tree_sha256()' in src
 
 
 def test_host_cpu_model_is_named():
