@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import zero_sharded_mixed_bucketed_amd as Z
-from act_util import U, acts, close, f64
+from act_util import EPS, U, acts, close, f64
 from gpu_util import assert_bits, f32, need_gpu, u16
 from oracle import act as oact
 from oracle import adam as oadam
@@ -115,6 +115,37 @@ def test_accumulating_micro_batches_equals_their_sum():
                           accumulate=True)
     close(f64(dw), want, 200 * 2 * U * mag, "fp32", "dw")
     assert (row != 0).any()
+
+
+@pytest.mark.parametrize("h", [96, 1100, 9000])
+@pytest.mark.parametrize("grad", ["fp32", "bf16"])
+def test_norm_gradients_accumulated_over_micro_batches_equal_their_sum(h, grad):
+    """Each call adds its rows' sums once to what is there and replaces nothing."""
+    rng = np.random.default_rng(h)
+    t, calls = 50, 3
+    dt = torch.float32 if grad == "fp32" else torch.bfloat16
+    got = {n: torch.from_numpy(rng.standard_normal(h)).to(dt).cuda() for n in ("dw_pre", "db_pre")}
+    want = {n: f64(v) for n, v in got.items()}
+    mag = {n: np.abs(v) for n, v in want.items()}
+    kept = {n: 0.0 for n in got}                       # roundings between the calls
+    for i in range(calls):
+        x, dz = acts(rng, t, h, "bf16"), acts(rng, t, h, "bf16")
+        k = Z.ckpt_empty(t, h, Z.CKPT_E4M3)
+        Z.ckpt_write(x, k)
+        st = torch.tensor([[0.0, 1.0, 0.0, 1.0]], device="cuda").repeat(t, 1)
+        Z.block_norm_grad(None, dz, k, None, st, pre=Z.Norm(Z.NORM_RMS, 1e-5), accumulate=True,
+                          **got)
+        hx, d = oact.held(*oact.store(f64(x), "e4m3", "bf16"), "e4m3"), f64(dz)
+        for n, s in (("dw_pre", d * hx), ("db_pre", d)):
+            want[n], mag[n] = want[n] + s.sum(0), mag[n] + np.abs(s).sum(0)
+            if i + 1 < calls and grad == "bf16":
+                kept[n] = kept[n] + EPS["bf16"] * np.abs(want[n])
+    for n, v in got.items():
+        # in fp32: at most two roundings of a product, one addition a token, 16 in the
+        # join and one a call; a kept value's rounding may itself be of one off by that
+        bound = (t + 2 + 16 + calls) * U * mag[n]
+        close(f64(v), want[n], bound + kept[n] * (1 + EPS["bf16"]) + 2 * EPS["bf16"] * bound,
+              grad, n)
 
 
 @pytest.mark.parametrize("tokens,group", [(96, 4), (50, 7)])
