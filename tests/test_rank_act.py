@@ -37,3 +37,11 @@ def test_slots_outside_the_bucket_are_refused(args):
 def test_checkpoint_bytes():
     k = _rank(2).checkpoint(64, 256)
     assert k.resident_bytes() == 64 * 256 * 33 // 32
+
+
+@pytest.mark.parametrize("lo,offset", [(-5, -10), (-1, -1), (3, -2)])
+def test_slots_before_the_flat_vector_are_refused(lo, offset):
+    """A place or a bucket that begins before flat index 0 is no part of the local
+    gradient, wherever it lies in the bucket."""
+    with pytest.raises(ValueError):
+        _rank(2).grad_slot(lo, 4, torch.zeros(400, dtype=torch.int16), offset)

@@ -150,7 +150,7 @@ class RankState:
                 or not bucket.is_contiguous():
             raise ValueError("bucket must be a contiguous fp16 row")
         lo = flat_lo - bucket_offset
-        if count < 0 or lo < 0 or lo + count > bucket.numel() \
+        if count < 0 or bucket_offset < 0 or lo < 0 or lo + count > bucket.numel() \
                 or flat_lo + count > self.geom.psi:
             raise ValueError(f"flat [{flat_lo}, +{count}) lies outside the local gradient")
         return bucket[lo:lo + count].view(torch.float16)
