@@ -307,8 +307,9 @@ int zero_launch_occupancy(int kernel, int *wgs_per_cu, uint32_t *lds_bytes);
  * gradient is made in backward, then reduced).  The entry points below follow
  * the conventions at the top of this file.  16-bit matrices are rows x cols with
  * a row stride in elements (stride >= cols unless there is at most one row);
- * any stride and any base that its element size divides is accepted, and rows
- * that start on 16 bytes (8 for codes) are read with wide loads.  Sums are fp32
+ * any stride and any base that its element size divides is accepted.  Columns
+ * between the rows of a matrix or checkpoint are never written; the weight
+ * gradient may read those of its inputs, which reach no result.  Sums are fp32
  * in a fixed order, so equal inputs give equal bits.
  * ------------------------------------------------------------------------ */
 
@@ -328,8 +329,7 @@ int zero_launch_occupancy(int kernel, int *wgs_per_cu, uint32_t *lds_bytes);
  *   value(code) * 2^(b - 127),  b = scales[r * scale_stride + c / 32];
  * b = 255 stands for NaN.  int8 codes are two's complement
  * (-127..127), e4m3 codes are 8-bit floats with 4 exponent and 3 mantissa bits,
- * bias 7, no infinities.  Padding columns between rows are never touched.  A row
- * has at most 2^31 columns.
+ * bias 7, no infinities.  A row has at most 2^31 columns.
  */
 typedef struct zero_ckpt {
   uint8_t *codes;
@@ -438,8 +438,8 @@ typedef struct zero_block_norm {
  * range (bf16 values beyond 1e19) has a deviation of infinity.
  * out may be res and z may be block (same address and stride); other overlaps of
  * an output are undefined.
- * Errors: ZERO_E_INVAL (NULL, dtype, kind, eps, a gate, post norm or ckpt_block
- * without a block, nothing to write), ZERO_E_RANGE (cols > ZERO_NORM_MAX_COLS, a
+ * Errors: ZERO_E_INVAL (NULL, dtype, kind, eps, no columns, a gate, post norm or
+ * ckpt_block without a block, nothing to write), ZERO_E_RANGE (cols > ZERO_NORM_MAX_COLS, a
  * stride too small, a checkpoint of other sizes, size overflow), ZERO_E_ALIGN,
  * ZERO_E_DEVICE.
  */

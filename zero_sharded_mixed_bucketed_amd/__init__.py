@@ -490,6 +490,7 @@ class Ckpt:
         return self.codes, self.scales
 
     def resident_bytes(self) -> int:
+        """Bytes of codes and scales, without what lies between rows."""
         return self.codes.numel() + self.scales.numel()
 
     def row_range(self, lo: int, hi: int) -> "Ckpt":

@@ -117,7 +117,7 @@ __device__ __forceinline__ u32x4 stream8(const uint16_t* row, uint64_t c, uint64
 
 // Stores of whole activations bypass the caches' keeping: what is written here is
 // larger than they are, and rows come in faster for it (16384 x 4096 bf16: reading a
-// checkpoint back 42 -> 31 us, the norms 111 -> 99 us).  Loads of what is read once
+// checkpoint back that was just written 42 -> 31 us, the norms 111 -> 99 us).  Loads of what is read once
 // do too, where that measured faster.
 template <bool STREAM = true>
 __device__ __forceinline__ void store8(uint16_t* row, uint64_t c, uint64_t cols, u32x4 w) {

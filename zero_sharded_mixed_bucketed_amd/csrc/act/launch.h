@@ -87,7 +87,7 @@ struct BlockNormGradLaunch {
 uint64_t norm_grad_workspace(uint64_t rows, uint64_t cols);
 hipError_t launch_block_norm_grad(const BlockNormGradLaunch& a, hipStream_t stream);
 
-// The widest row that the norms take: 16 waves of 16 columns a thread.
+// The widest row that the norms take: forward four waves of eight chunks a thread.
 constexpr uint64_t kMaxNormCols = 16384;
 
 struct WeightGradLaunch {

@@ -5,9 +5,12 @@
 // 8-bit checkpoints of b and h'.
 //
 // One workgroup holds a row from the first load to the last store: each input is
-// read once and each output written once.  A thread holds chunks of eight columns;
-// row sums go through lane exchanges and, where a row has several waves, shared
-// memory.  Bound by memory: 8 bytes an element forward, about 10 backward.
+// read once and each output written once, but for the backward of rows over 8192
+// columns, which reads its inputs again for the parameters' gradients (and a third
+// time where outputs replace them).  A thread holds chunks of eight columns; row sums
+// go through lane exchanges and, where a row has several waves, shared memory.  Bound
+// by memory at whole widths from 4096 columns on (8 bytes an element forward, about
+// 10 backward); elsewhere by empty lanes, registers and latency, as noted below.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -63,8 +66,11 @@ __device__ __forceinline__ void emit(const Ckpt& c, uint64_t row, uint32_t chunk
 // Up to eight chunks a thread: rows of up to 4096 columns take one wave, and its
 // sums no barrier.  Nothing is kept from row to row; many rows at once on a compute
 // unit hide the loads, and the norms' weights come from the caches.  16384 x 4096
-// bf16 with a gate a channel takes 97 us, 5.5 TB/s (143 us, 5.2 TB/s with all three
-// checkpoints).
+// bf16 with a gate a channel takes 97-100 us with RMS norms, 5.4-5.5 TB/s (143 us, 5.2
+// TB/s with all three checkpoints), and 103 with layer norms.  As many elements in rows
+// of 2560 columns take 118 and 135 us (a sixth of the lanes hold nothing), of 5000 108
+// and 118, of 8191 156 and 174 (every lane shifts its last chunk, and eight chunks a
+// thread spill in rows that are not whole), of 16384 97 and 102.
 template <typename T, int WAVES, int HELD, bool FULL>
 __global__ __launch_bounds__(64 * WAVES, HELD > 5 ? 3 : 4) void block_norm_kernel(
     BlockNormLaunch a, uint64_t row0) {
@@ -216,6 +222,9 @@ uint64_t padded(uint64_t cols) { return (cols + kChunk - 1) / kChunk * kChunk; }
 //   layer norms, fp16: 1100 columns 600 (336) us, 2560: 256 (238), 4096: 188 (151),
 //     4608: 199 (260), 5000: 300 (252), 5120: 190 (208); their rows that end inside a
 //     wave run out of registers with one chunk
+// Rows of up to 512 columns are one wave's, so short ones leave lanes empty, and layer
+// norms' spill there too (48-58 registers): as many elements in rows of 72 columns take
+// 678 us (RMS) and 993 (layer norms), of 200 266 and 385, of 300 231 and 316.
 int grad_held(uint64_t cols, int sets) {
   const bool whole = cols % (64 * kChunk) == 0;
   if (cols > 8192) return 4;
@@ -355,7 +364,8 @@ constexpr int grad_fit(int held) { return held == 1 ? 3 : 2; }
 // read the norms' weights from the caches, make those values again, and leave the
 // parameters' gradients to norm_sums_kernel, with mean(q x1) and [mean q] of each
 // row: kept here too, 4096 x 16384 took 520 us (RMS) and 850 (layer norms) where it
-// now takes 342 and 355.
+// now takes 328 and 337 (its bytes alone: 102).  Rows that are not whole cost more:
+// 7455 x 9001 takes 566 and 583.
 template <typename T, int FMT, int HELD, int SETS, bool FULL>
 __global__ __launch_bounds__(grad_threads(HELD, SETS, FULL), grad_fit(HELD)) void
 block_norm_grad_kernel(BlockNormGradLaunch a, uint64_t pad) {
@@ -616,7 +626,8 @@ block_norm_grad_kernel(BlockNormGradLaunch a, uint64_t pad) {
 
 // The parameters' gradients of wide rows, from the same inputs and each row's means:
 // a thread keeps the sums of eight columns over every gridDim.y-th row, so that
-// nothing passes between threads.
+// nothing passes between threads.  Those sums, the norms' rows and two rows in hand
+// are more than the registers of three waves a unit: 118-122 spill.
 constexpr int kSumThreads = 256;
 constexpr uint32_t kSumCols = kSumThreads * kChunk;
 

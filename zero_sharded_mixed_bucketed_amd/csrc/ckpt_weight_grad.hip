@@ -3,11 +3,14 @@
 // the checkpoint holds.
 //
 // Every held value is exact in 16 bits, so the products run on the 16-bit matrix
-// instructions with the dequantised values themselves, and sums are fp32.  Bound by
-// the matrix unit and, on random data, by the power it may draw: 8192 tokens,
-// 4096 -> 16384 takes 0.88-1.0 ms in bf16 and 0.90-1.12 ms in fp16 (e4m3 - int8
-// codes), 0.98-1.25 PFLOP/s, where a library's plain 16-bit product of the same
-// values, dequantised beforehand, takes 0.90-1.0 ms.  The
+// instructions with the dequantised values themselves, and sums are fp32.  8192
+// tokens, 4096 -> 16384 takes 0.93-0.95 ms with e4m3 codes and 1.03-1.10 ms with int8
+// ones, 1.00-1.18 PFLOP/s, where a library's plain 16-bit product of the same values,
+// dequantised beforehand, takes 0.92-0.97 ms.  Bound by the matrix unit, which is busy
+// in half of the cycles beside the codes' arithmetic, and by the clock: 2.05 million
+// cycles a pass whatever it takes, 1.09-1.36 ms at 1.9-1.5 GHz in a row of traced
+// passes.  Over few tokens the prologue and epilogue of a tile overlap with nothing:
+// 256 tokens, 4096 -> 16384 takes 75-78 us, the library 61-63.  The
 // long axis t is the slow one of both operands; the matrix instructions want it
 // in each lane's registers, so tiles lie in shared memory as they come (t by
 // columns, 16 bits) and are read with the transposing shared-memory loads.
