@@ -298,7 +298,9 @@ int zero_launch_occupancy(int kernel, int *wgs_per_cu, uint32_t *lds_bytes);
 
 /* ------------------------------------------------------------------------
  * Residual states: activations kept for the backward pass in 8 bits, the
- * weight gradient taken from them, and the norms around a block.
+ * weight gradient taken from them, the norms around a block, the gated block between
+ * them, and the losses over the vocabulary (whose logits are the largest of a step's
+ * temporaries).
  *
  * The guide's third class of training memory after optimizer states, gradients
  * and parameters (section "Como funciona": ZeRO-R treats the residual states,
@@ -496,6 +498,159 @@ uint64_t zero_block_norm_grad_workspace(uint64_t rows, uint64_t cols);
  * gradient of a weight or bias of a norm of kind NONE, or no output.
  */
 int zero_block_norm_grad(const zero_block_norm_grad_t *a, void *hip_stream);
+
+/* Activations of a gated block. */
+#define ZERO_ACT_SILU 0      /* g / (1 + exp(-g)) */
+#define ZERO_ACT_GELU 1      /* g (1 + erf(g / sqrt 2)) / 2 */
+#define ZERO_ACT_GELU_TANH 2 /* g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2 */
+
+/* A layer's gated feed-forward block up to its last projection (zero_gated_ffn). */
+typedef struct zero_gated_ffn {
+  int dtype; /* ZERO_F16 or ZERO_BF16: x, w and out */
+  int act;
+  uint64_t rows, cols, width;
+  const void *x; /* rows x cols */
+  uint64_t x_stride;
+  const void *w; /* 2 width x cols: the gate's rows, then the other projection's */
+  uint64_t w_stride;
+  void *out; /* rows x width, or NULL */
+  uint64_t out_stride;
+  const zero_ckpt_t *ckpt_gate; /* each rows x width: a checkpoint to write, or NULL; */
+  const zero_ckpt_t *ckpt_up;   /* all of one format */
+  const zero_ckpt_t *ckpt_out;
+} zero_gated_ffn_t;
+
+/*
+ * With w = [wg; wu], for each of the rows:
+ *   g = x wg^T;  u = x wu^T;  out = act(g) . u
+ * in one kernel: exact products, fp32 sums, out from the sums themselves and rounded
+ * once.  The checkpoints hold g, u and out after their rounding to dtype, as
+ * zero_ckpt_write stores them: what the backward needs of the block, in 8 bits.  An
+ * output must not overlap an input or another output.
+ * rows at most 2^25, cols and width at most 2^22, and both > 0.
+ * Errors: ZERO_E_INVAL (NULL, dtype, act, format, no columns, nothing to write),
+ * ZERO_E_RANGE (sizes, a stride too small, a checkpoint of other sizes, size overflow),
+ * ZERO_E_ALIGN, ZERO_E_DEVICE.
+ */
+int zero_gated_ffn(const zero_gated_ffn_t *a, void *hip_stream);
+
+/* The backward of zero_gated_ffn (zero_gated_ffn_grad). */
+typedef struct zero_gated_ffn_grad {
+  int dtype;
+  int act;
+  uint64_t rows, cols, width;
+  const void *dout; /* rows x width: gradient of out */
+  uint64_t dout_stride;
+  const zero_ckpt_t *ckpt_gate; /* as zero_gated_ffn left them, of one format */
+  const zero_ckpt_t *ckpt_up;
+  const void *w; /* needed for dx */
+  uint64_t w_stride;
+  void *dx; /* rows x cols, or NULL */
+  uint64_t dx_stride;
+  const zero_ckpt_t *ckpt_x; /* rows x cols: of x; needed for dw */
+  void *dw;                  /* 2 width x cols of dw_dtype, or NULL */
+  uint64_t dw_stride;
+  int dw_dtype;   /* dtype or ZERO_F32 */
+  int accumulate; /* add to dw instead of setting it */
+  void *workspace;
+  uint64_t workspace_bytes;
+} zero_gated_ffn_grad_t;
+
+/* Bytes of workspace of zero_gated_ffn_grad at these sizes (0: sizes it refuses). */
+uint64_t zero_gated_ffn_grad_workspace(uint64_t rows, uint64_t cols, uint64_t width);
+
+/*
+ * With the held values g and u:
+ *   dg = dout . u . act'(g);  du = dout . act(g)     (each rounded to dtype)
+ *   dx = dg wg + du wu;  dw = [dg du]^T held(x)      (fp32 sums, one rounding)
+ * dw is zero_ckpt_weight_grad's of the rounded dg and du.  rows == 0 gives a dw of 0,
+ * or leaves it with `accumulate`.  workspace: 16-byte aligned device memory, written
+ * by the call; calls that may run at the same time need one each.  An output must not
+ * overlap an input or another output.  Sizes as zero_gated_ffn.
+ * Errors: as zero_gated_ffn, and ZERO_E_INVAL for a needed input or workspace that is
+ * NULL, ZERO_E_RANGE for a workspace too small.
+ */
+int zero_gated_ffn_grad(const zero_gated_ffn_grad_t *a, void *hip_stream);
+
+/* What a loss over the vocabulary has in common (zero_vocab_loss, zero_distill_loss). */
+typedef struct zero_loss {
+  int dtype; /* ZERO_F16 or ZERO_BF16: x, w and dx */
+  uint64_t rows, cols, vocab;
+  const void *x; /* rows x cols: the last hidden states */
+  uint64_t x_stride;
+  const void *w; /* vocab x cols: the projection onto the vocabulary */
+  uint64_t w_stride;
+  const float *weights; /* of each row, or NULL (ones) */
+  float *loss;          /* of each row */
+  double scale;         /* of the gradients: loss scaling, 1 / the number of tokens */
+  void *dx;             /* rows x cols, or NULL */
+  uint64_t dx_stride;
+  void *dw; /* vocab x cols of dw_dtype, or NULL */
+  uint64_t dw_stride;
+  int dw_dtype;   /* dtype or ZERO_F32 */
+  int accumulate; /* add to dw instead of setting it */
+  void *workspace;
+  uint64_t workspace_bytes;
+} zero_loss_t;
+
+/* Bytes of workspace of either loss at these sizes; with_dx, with_dw: whether that
+ * gradient is wanted (0: sizes that the losses refuse). */
+uint64_t zero_loss_workspace(uint64_t rows, uint64_t cols, uint64_t vocab, int with_dx,
+                             int with_dw);
+
+/*
+ * Softmax cross entropy over the vocabulary, from the last hidden states, with its
+ * gradients: with z = x w^T (fp32 sums, not rounded),
+ *   loss[t] = weights[t] (log(sum over v of exp z[t][v]) - z[t][y]),  y = targets[t]
+ *   d[t][v] = weights[t] (softmax(z[t])[v] - (v == y))       (rounded to dtype)
+ *   dx = scale d w;  dw = scale d^T x                        (fp32 sums, one rounding)
+ * The logits are never kept: the workspace holds those of a piece of the tokens, 4
+ * bytes each and 2 GiB at most (or 256 tokens), a copy of their x and, if there are
+ * several pieces, fp32 sums of dw.  Before its rounding d
+ * is divided by the weights' largest power of two and multiplied by 2^14, which fp16's
+ * range asks for, and the products multiplied back.
+ * A row whose target is negative or whose weight is 0 is left out: its loss and dx are
+ * 0, and nothing of it is read into another's result.  A target of vocab or more makes
+ * the row's loss NaN and its gradients with it.  targets: id_bytes (4 or 8) wide signed
+ * whole numbers.  Sums are in a fixed order.  rows == 0 gives a dw of 0, or leaves it
+ * with `accumulate`.  workspace: 16-byte aligned device memory, written by the call;
+ * calls that may run at the same time need one each.  An output must not overlap an
+ * input or another output.  rows at most 2^25, cols at most 2^22, vocab at most 2^24,
+ * both > 0.
+ * Errors: ZERO_E_INVAL (NULL, dtype, id_bytes, scale, no columns, workspace missing),
+ * ZERO_E_RANGE (sizes, a stride or the workspace too small, size overflow),
+ * ZERO_E_ALIGN, ZERO_E_DEVICE.
+ */
+int zero_vocab_loss(const zero_loss_t *a, const void *targets, int id_bytes, void *hip_stream);
+
+#define ZERO_DISTILL_MAX_TOP 1024
+
+/* A teacher's top logits. */
+typedef struct zero_top_logits {
+  uint32_t top; /* entries of a row, 1 to ZERO_DISTILL_MAX_TOP */
+  const void *ids; /* rows x top signed whole numbers of id_bytes; negative: no entry */
+  uint64_t ids_stride;
+  int id_bytes; /* 4 or 8 */
+  const void *logits; /* rows x top of logits_dtype */
+  uint64_t logits_stride;
+  int logits_dtype; /* ZERO_F16, ZERO_BF16 or ZERO_F32 */
+  double temperature; /* tau > 0 */
+} zero_top_logits_t;
+
+/*
+ * Distillation from a teacher's top logits s[t][j] of the ids i[t][j], as
+ * zero_vocab_loss otherwise: with q[t] = softmax over a row's entries of s[t] / tau and
+ * p[t] = softmax over the vocabulary of z[t] / tau,
+ *   loss[t] = weights[t] tau^2 sum over j of q[t][j] (log q[t][j] - log p[t][i[t][j]])
+ *   d[t][v] = weights[t] (p[t][v] - sum over j with i[t][j] == v of q[t][j])
+ *   dx = scale tau d w;  dw = scale tau d^T x
+ * A row without entries is left out.  An entry of -infinity has no share; an id that
+ * stands in a row twice has both shares.  An id of vocab or more, and logits that give
+ * no softmax (NaN, +infinity, -infinity alone), make the row's loss NaN and its
+ * gradients with it.
+ * Errors: as zero_vocab_loss, and ZERO_E_INVAL for top, temperature or a dtype.
+ */
+int zero_distill_loss(const zero_loss_t *a, const zero_top_logits_t *t, void *hip_stream);
 
 /* Message of the calling thread's last error ("" if none).  Valid until the
  * thread's next call into the library. */

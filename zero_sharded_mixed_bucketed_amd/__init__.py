@@ -26,6 +26,10 @@ gradient they give:
     ckpt_weight_grad(ckpt, dy, dw)              a linear layer's weight gradient
     block_norm(res, block, out, z, stats)       the norms around a block, gate, residual scale
     block_norm_grad(dout, dz, ckpt_out, ckpt_block, stats)   their backward
+    gated_ffn(x, w, out, act)                   a gated feed-forward block, with checkpoints
+    gated_ffn_grad(dout, ckpt_gate, ckpt_up, w, act, dx, ckpt_x, dw)   its backward
+    vocab_loss(x, w, targets, loss, dx=, dw=)   cross entropy of x w^T, with its gradients
+    distill_loss(x, w, ids, logits, loss, dx=, dw=)   against a teacher's top logits
 
 Importing this package fails if libzero.so has not been built: there is no
 fallback path.
@@ -54,7 +58,9 @@ EXPORTS = ("zero_memory_model", "zero_memory_model_k", "zero_comm_volume",
            "zero_gather_params", "zero_launch_occupancy", "zero_last_error",
            "zero_ckpt_write", "zero_ckpt_read", "zero_ckpt_weight_grad",
            "zero_ckpt_weight_grad_workspace", "zero_block_norm", "zero_block_norm_grad",
-           "zero_block_norm_grad_workspace")
+           "zero_block_norm_grad_workspace", "zero_gated_ffn", "zero_gated_ffn_grad",
+           "zero_gated_ffn_grad_workspace", "zero_vocab_loss", "zero_distill_loss",
+           "zero_loss_workspace")
 
 # Kernels of zero_launch_occupancy.
 KERNEL_REDUCE_W16, KERNEL_REDUCE_W8, KERNEL_REDUCE_W4, KERNEL_REDUCE_W2 = 0, 1, 2, 3
@@ -67,6 +73,10 @@ CKPT_BLOCK = 32
 # Kinds of norm, and the widest row they take.
 NORM_NONE, NORM_RMS, NORM_LAYER = 0, 1, 2
 NORM_MAX_COLS = 16384
+
+# Activations of a gated block.
+ACT_SILU, ACT_GELU, ACT_GELU_TANH = 0, 1, 2
+DISTILL_MAX_TOP = 1024
 
 
 class ZeroError(RuntimeError):
@@ -138,6 +148,48 @@ class _BlockNormGradArg(ctypes.Structure):
                 ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_uint64)]
 
 
+class _GatedFfnArg(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("act", ctypes.c_int), ("rows", ctypes.c_uint64),
+                ("cols", ctypes.c_uint64), ("width", ctypes.c_uint64),
+                ("x", ctypes.c_void_p), ("x_stride", ctypes.c_uint64),
+                ("w", ctypes.c_void_p), ("w_stride", ctypes.c_uint64),
+                ("out", ctypes.c_void_p), ("out_stride", ctypes.c_uint64),
+                ("ckpt_gate", ctypes.POINTER(_CkptArg)),
+                ("ckpt_up", ctypes.POINTER(_CkptArg)), ("ckpt_out", ctypes.POINTER(_CkptArg))]
+
+
+class _GatedFfnGradArg(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("act", ctypes.c_int), ("rows", ctypes.c_uint64),
+                ("cols", ctypes.c_uint64), ("width", ctypes.c_uint64),
+                ("dout", ctypes.c_void_p), ("dout_stride", ctypes.c_uint64),
+                ("ckpt_gate", ctypes.POINTER(_CkptArg)), ("ckpt_up", ctypes.POINTER(_CkptArg)),
+                ("w", ctypes.c_void_p), ("w_stride", ctypes.c_uint64),
+                ("dx", ctypes.c_void_p), ("dx_stride", ctypes.c_uint64),
+                ("ckpt_x", ctypes.POINTER(_CkptArg)), ("dw", ctypes.c_void_p),
+                ("dw_stride", ctypes.c_uint64), ("dw_dtype", ctypes.c_int),
+                ("accumulate", ctypes.c_int), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_uint64)]
+
+
+class _LossArg(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("rows", ctypes.c_uint64), ("cols", ctypes.c_uint64),
+                ("vocab", ctypes.c_uint64), ("x", ctypes.c_void_p), ("x_stride", ctypes.c_uint64),
+                ("w", ctypes.c_void_p), ("w_stride", ctypes.c_uint64),
+                ("weights", ctypes.c_void_p), ("loss", ctypes.c_void_p),
+                ("scale", ctypes.c_double), ("dx", ctypes.c_void_p),
+                ("dx_stride", ctypes.c_uint64), ("dw", ctypes.c_void_p),
+                ("dw_stride", ctypes.c_uint64), ("dw_dtype", ctypes.c_int),
+                ("accumulate", ctypes.c_int), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_uint64)]
+
+
+class _TopLogitsArg(ctypes.Structure):
+    _fields_ = [("top", ctypes.c_uint32), ("ids", ctypes.c_void_p),
+                ("ids_stride", ctypes.c_uint64), ("id_bytes", ctypes.c_int),
+                ("logits", ctypes.c_void_p), ("logits_stride", ctypes.c_uint64),
+                ("logits_dtype", ctypes.c_int), ("temperature", ctypes.c_double)]
+
+
 def hip_runtimes() -> set:
     """Paths of every HIP runtime library mapped into this process."""
     try:
@@ -200,6 +252,18 @@ def _load() -> ctypes.CDLL:
     lib.zero_block_norm_grad_workspace.restype = u64
     lib.zero_block_norm_grad.argtypes = [ctypes.POINTER(_BlockNormGradArg), vp]
     lib.zero_block_norm_grad.restype = ci
+    lib.zero_gated_ffn.argtypes = [ctypes.POINTER(_GatedFfnArg), vp]
+    lib.zero_gated_ffn.restype = ci
+    lib.zero_gated_ffn_grad_workspace.argtypes = [u64, u64, u64]
+    lib.zero_gated_ffn_grad_workspace.restype = u64
+    lib.zero_gated_ffn_grad.argtypes = [ctypes.POINTER(_GatedFfnGradArg), vp]
+    lib.zero_gated_ffn_grad.restype = ci
+    lib.zero_loss_workspace.argtypes = [u64, u64, u64, ci, ci]
+    lib.zero_loss_workspace.restype = u64
+    lib.zero_vocab_loss.argtypes = [ctypes.POINTER(_LossArg), vp, ci, vp]
+    lib.zero_vocab_loss.restype = ci
+    lib.zero_distill_loss.argtypes = [ctypes.POINTER(_LossArg), ctypes.POINTER(_TopLogitsArg), vp]
+    lib.zero_distill_loss.restype = ci
     lib.zero_last_error.argtypes = []
     lib.zero_last_error.restype = ctypes.c_char_p
     return lib
@@ -419,7 +483,7 @@ def _matrix(t, name, dtypes, shape=None):
     if shape is not None and got != shape:
         raise ValueError(f"{name} is {tuple(got)}, expected {tuple(shape)}")
     stride, unit = t.stride()
-    if unit != 1 and got[1] > 1:
+    if unit != 1 and got[1] > 1 and got[0] > 0:      # without rows any strides are those
         raise ValueError(f"{name} must be a matrix with unit column stride")
     return t.data_ptr(), stride if got[0] > 1 else got[1]
 
@@ -737,3 +801,142 @@ def block_norm_grad(dout, dz, ckpt_out: Optional[Ckpt], ckpt_block: Optional[Ckp
         places.get("dw_pre"), places.get("db_pre"), places.get("dw_post"), places.get("db_post"),
         2 if grad_dtype == torch.float32 else code, int(bool(accumulate)), ws, ws_bytes)
     _call(dev, stream, lib.zero_block_norm_grad, ctypes.byref(a))
+
+
+def gated_ffn(x, w, out, act: int = ACT_SILU, ckpt_gate: Optional[Ckpt] = None,
+              ckpt_up: Optional[Ckpt] = None, ckpt_out: Optional[Ckpt] = None,
+              stream=None) -> None:
+    """out = act(x wg^T) . (x wu^T) of a gated block, w = [wg; wu], in one kernel.
+
+    x: float16 or bfloat16 [rows, cols]; w [2 width, cols] and out [rows, width] (or
+    None) of its type, any row strides.  ckpt_gate, ckpt_up, ckpt_out: checkpoints
+    [rows, width] of x wg^T, x wu^T and out to write too, of one format.
+    """
+    p_x, s_x = _matrix(x, "x", _F16_BF16)
+    (rows, cols), own = x.shape, (x.dtype,)
+    p_w, s_w = _matrix(w, "w", own)
+    if w.shape[0] % 2 or w.shape[1] != cols:
+        raise ValueError(f"w is {tuple(w.shape)}, expected [2 width, {cols}]")
+    width = w.shape[0] // 2
+    tensors = [x, w]
+    a = _GatedFfnArg(_CODE[x.dtype], act, rows, cols, width, p_x, s_x, p_w, s_w,
+                     *_optional(out, "out", own, (rows, width), tensors),
+                     _ckpt(ckpt_gate, tensors), _ckpt(ckpt_up, tensors), _ckpt(ckpt_out, tensors))
+    _call(_index(tensors, stream), stream, lib.zero_gated_ffn, ctypes.byref(a))
+
+
+def gated_ffn_grad_workspace(rows: int, cols: int, width: int) -> int:
+    """Bytes of workspace of gated_ffn_grad at these sizes."""
+    return lib.zero_gated_ffn_grad_workspace(rows, cols, width)
+
+
+def gated_ffn_grad(dout, ckpt_gate: Ckpt, ckpt_up: Ckpt, w, act: int = ACT_SILU, dx=None,
+                   ckpt_x: Optional[Ckpt] = None, dw=None, accumulate: bool = False,
+                   workspace=None, stream=None) -> None:
+    """The backward of gated_ffn from its checkpoints.
+
+    dout: float16 or bfloat16 [rows, width]; w: as in the forward (None if only dw is
+    wanted); dx: [rows, cols] of dout's type, or None; dw: dout's type or float32
+    [2 width, cols], or None, from ckpt_x, the checkpoint of the block's input; added to
+    with `accumulate`.  workspace: uint8 device tensor of gated_ffn_grad_workspace
+    bytes, or None to take it from torch's allocator.
+    """
+    p_do, s_do = _matrix(dout, "dout", _F16_BF16)
+    (rows, width), own = dout.shape, (dout.dtype,)
+    given = next((t for t in (w, dx, dw) if isinstance(t, torch.Tensor) and t.dim() == 2), None)
+    if given is None or (w is None and dx is not None):
+        raise ValueError("give w for dx, and dx or dw")
+    cols = given.shape[1]
+    tensors = [dout]
+    p_w, s_w = _optional(w, "w", own, (2 * width, cols), tensors)
+    p_dx, s_dx = _optional(dx, "dx", own, (rows, cols), tensors)
+    p_dw, s_dw = _optional(dw, "dw", own + (torch.float32,), (2 * width, cols), tensors)
+    p_g, p_u, p_k = (_ckpt(k, tensors) for k in (ckpt_gate, ckpt_up, ckpt_x))
+    dev = _index(tensors, stream)
+    ws, ws_bytes, held = _workspace(
+        workspace, lib.zero_gated_ffn_grad_workspace(rows, cols, width), dev, stream)
+    a = _GatedFfnGradArg(_CODE[dout.dtype], act, rows, cols, width, p_do, s_do, p_g, p_u, p_w, s_w,
+                         p_dx, s_dx, p_k, p_dw, s_dw,
+                         _CODE[dout.dtype if dw is None else dw.dtype], int(bool(accumulate)), ws,
+                         ws_bytes)
+    _call(dev, stream, lib.zero_gated_ffn_grad, ctypes.byref(a))
+
+
+_IDS = {torch.int32: 4, torch.int64: 8}
+
+
+def loss_workspace(rows: int, cols: int, vocab: int, with_dx: bool = True,
+                   with_dw: bool = True) -> int:
+    """Bytes of workspace of vocab_loss and distill_loss at these sizes."""
+    return lib.zero_loss_workspace(rows, cols, vocab, int(bool(with_dx)), int(bool(with_dw)))
+
+
+def _loss_arg(x, w, loss, weights, scale, dx, dw, accumulate, workspace, stream, tensors):
+    """(argument, device index, workspace tensor) of a loss; tensors: its other ones."""
+    p_x, s_x = _matrix(x, "x", _F16_BF16)
+    (rows, cols), own = x.shape, (x.dtype,)
+    p_w, s_w = _matrix(w, "w", own)
+    vocab = w.shape[0]
+    if w.shape[1] != cols:
+        raise ValueError(f"w is {tuple(w.shape)}, expected [vocab, {cols}]")
+    tensors += [x, w, loss]
+    p_loss = _row(loss, "loss", torch.float32, rows)
+    p_weights = None
+    if weights is not None:
+        p_weights = _row(weights, "weights", torch.float32, rows)
+        tensors.append(weights)
+    p_dx, s_dx = _optional(dx, "dx", own, (rows, cols), tensors)
+    p_dw, s_dw = _optional(dw, "dw", own + (torch.float32,), (vocab, cols), tensors)
+    dev = _index(tensors, stream)
+    ws, ws_bytes, held = _workspace(
+        workspace, lib.zero_loss_workspace(rows, cols, vocab, dx is not None, dw is not None),
+        dev, stream)
+    a = _LossArg(_CODE[x.dtype], rows, cols, vocab, p_x, s_x, p_w, s_w, p_weights, p_loss, scale,
+                 p_dx, s_dx, p_dw, s_dw, _CODE[x.dtype if dw is None else dw.dtype],
+                 int(bool(accumulate)), ws, ws_bytes)
+    return a, dev, held
+
+
+def vocab_loss(x, w, targets, loss, weights=None, scale: float = 1.0, dx=None, dw=None,
+               accumulate: bool = False, workspace=None, stream=None) -> None:
+    """loss = weights . cross entropy of x w^T against targets, and the gradients of
+    scale * sum(loss), without keeping the logits.
+
+    x: float16 or bfloat16 [rows, cols], the last hidden states; w: of its type
+    [vocab, cols]; targets: contiguous int32 or int64 [rows], negative where a token has
+    no loss; loss and weights (or None: ones): float32 [rows].  dx: [rows, cols] of x's
+    type, or None; dw: x's type or float32 [vocab, cols], or None, added to with
+    `accumulate`.  workspace: uint8 device tensor of loss_workspace bytes, or None to take
+    it from torch's allocator.
+    """
+    rows = x.shape[0] if isinstance(x, torch.Tensor) and x.dim() == 2 else 0
+    if not isinstance(targets, torch.Tensor) or targets.dtype not in _IDS:
+        raise ValueError("targets must be an int32 or int64 device tensor")
+    p_ids = _row(targets, "targets", targets.dtype, rows)
+    a, dev, held = _loss_arg(x, w, loss, weights, scale, dx, dw, accumulate, workspace, stream,
+                             [targets])
+    _call(dev, stream, lib.zero_vocab_loss, ctypes.byref(a), p_ids, _IDS[targets.dtype])
+
+
+def distill_loss(x, w, ids, logits, loss, temperature: float = 1.0, weights=None,
+                 scale: float = 1.0, dx=None, dw=None, accumulate: bool = False, workspace=None,
+                 stream=None) -> None:
+    """loss = weights . temperature^2 . KL(q || p), q the softmax of a teacher's top
+    logits and p that of x w^T over the whole vocabulary, both at the temperature, and
+    the gradients of scale * sum(loss).
+
+    ids: int32 or int64 [rows, top], negative where a row has fewer entries; logits:
+    float16, bfloat16 or float32 [rows, top]; the rest as vocab_loss.
+    """
+    if not isinstance(ids, torch.Tensor) or ids.dtype not in _IDS:
+        raise ValueError("ids must be an int32 or int64 device tensor")
+    p_ids, s_ids = _matrix(ids, "ids", tuple(_IDS))
+    shape = ids.shape
+    if isinstance(x, torch.Tensor) and x.dim() == 2 and x.shape[0] != shape[0]:
+        raise ValueError(f"ids has {shape[0]} rows, x {x.shape[0]}")
+    p_top, s_top = _matrix(logits, "logits", _FLOATS, shape)
+    a, dev, held = _loss_arg(x, w, loss, weights, scale, dx, dw, accumulate, workspace, stream,
+                             [ids, logits])
+    t = _TopLogitsArg(shape[1], p_ids, s_ids, _IDS[ids.dtype], p_top, s_top, _CODE[logits.dtype],
+                      temperature)
+    _call(dev, stream, lib.zero_distill_loss, ctypes.byref(a), ctypes.byref(t))

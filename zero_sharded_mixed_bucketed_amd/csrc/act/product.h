@@ -1,0 +1,598 @@
+// Products of 16-bit matrices on the matrix instructions, with the reduction axis k
+// either fast (rows of neighbouring k) or slow (rows of neighbouring outputs) in
+// each operand, and a caller's own epilogue:
+//   c(m, n) = sum over k of a(m, k) b(n, k),  fp32 sums of exact products.
+//
+// A workgroup of four waves makes a TM x TN tile of c, 64 of k at a time, through two
+// buffers of shared memory and one barrier a turn.  While the matrix unit works on
+// one tile, the next one goes from registers to the other buffer and the one after
+// it is loaded into those registers; the operands of a matrix step are read from
+// shared memory during the step before it.
+//   - k fast: a row's 64 k are eight 16-byte chunks, placed by chunk ^ (row / 2 % 8),
+//     so that sixteen neighbouring rows of one chunk lie in different banks; a lane
+//     reads its eight k with one load.
+//   - k slow: rows of TILE columns as they come, in 64-byte granules permuted by k,
+//     read with the transposing loads.
+#ifndef ZERO_ACT_PRODUCT_H_
+#define ZERO_ACT_PRODUCT_H_
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "act/format.h"
+#include "act/launch.h"
+
+namespace zero {
+namespace act {
+
+typedef _Float16 half8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bhalf8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kMulThreads = 256;  // four waves
+constexpr int kMulFrag = 32;      // rows and columns of a matrix instruction
+constexpr int kMulStep = 16;      // k of a matrix instruction
+constexpr int kMulDepth = 64;     // k of a turn
+
+// One operand in device memory.  extent: rows (k fast) or columns (k slow) that
+// exist; of two stacked matrices (an epilogue of pairs) those of each.
+struct Operand {
+  const uint16_t* p;
+  uint64_t stride, extent;
+};
+
+// The sizes of a product.  A count in device memory, where there is one, says how
+// many rows of c (or, with count_k, how many k) there are past `first`, at most m
+// (k): the host knows the most only.
+struct Extents {
+  uint64_t m, n, k;
+  uint32_t splits;          // of k, each a range of whole turns
+  const uint32_t* count;
+  uint64_t first;
+  int count_k;
+};
+
+template <typename T>
+__device__ __forceinline__ f32x16 mul(u32x4 a, u32x4 b, f32x16 c) {
+  if constexpr (T::kType == kF16)
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8, a),
+                                                  __builtin_bit_cast(half8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bhalf8, a),
+                                                   __builtin_bit_cast(bhalf8, b), c, 0, 0, 0);
+}
+
+// Orders one wave's shared-memory accesses before and after this point.
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// One operand's side of a workgroup: its loads, its shared tile and its fragments.
+// PAIR != 0: the operand is two stacked matrices, and a tile holds PAIR rows of the
+// first, the same rows of the second, the next PAIR rows of the first, and so on.
+template <bool FAST, int TILE, int PAIR = 0>
+struct Side {
+  static_assert(FAST ? TILE % 32 == 0 : TILE >= 128 && !PAIR, "granules are permuted in fours");
+  static constexpr int kPass = TILE / 32;                   // loads of a thread a turn
+  static constexpr uint32_t kLanes = FAST ? kMulDepth / kChunk : TILE / kChunk;
+  static constexpr uint32_t kStep = kMulThreads / kLanes;   // rows of memory a pass
+  static constexpr uint32_t kElems = TILE * kMulDepth;
+  static constexpr int kReads = FAST ? 1 : 2;               // shared loads a fragment
+
+  const uint16_t* p;       // row (k fast) or row 0 (k slow) of the tile
+  uint64_t stride, extent, first;
+  uint32_t row, chunk;     // of this thread in a pass
+  uint32_t off[FAST ? kPass : 1];
+
+  __device__ __forceinline__ uint64_t row_of(uint32_t r) const {   // k fast
+    if constexpr (PAIR != 0) {
+      const uint64_t at = first + r / (2 * PAIR) * PAIR + r % PAIR;
+      return (at < extent ? at : extent - 1) + (r / PAIR % 2 ? extent : 0);
+    }
+    const uint64_t at = first + r;
+    return at < extent ? at : extent - 1;
+  }
+
+  // Rows and columns past the matrix's edge take the last row or column 0: they reach
+  // only sums that are not kept.
+  __device__ __forceinline__ void begin(const Operand& o, uint64_t at) {
+    stride = o.stride;
+    extent = o.extent;
+    first = at;
+    row = threadIdx.x / kLanes;
+    chunk = threadIdx.x % kLanes * kChunk;
+    if constexpr (FAST) {
+      p = o.p + first * stride;
+#pragma unroll
+      for (int i = 0; i < kPass; ++i)
+        off[i] = static_cast<uint32_t>(((row_of(i * kStep + row) - first) * stride + chunk) * 2);
+    } else {
+      p = o.p;
+      off[0] = (row * static_cast<uint32_t>(stride) +
+                static_cast<uint32_t>(first + chunk < extent ? first + chunk : 0)) * 2;
+    }
+  }
+
+  // Without a check: turns that end before k `safe` (see safe_k).
+  __device__ __forceinline__ u32x4 load(uint64_t k, int i) const {
+    const uint8_t* at;
+    if constexpr (FAST)
+      at = reinterpret_cast<const uint8_t*>(p + k) + off[i];
+    else
+      at = reinterpret_cast<const uint8_t*>(p + (k + i * kStep) * stride) + off[0];
+    return *reinterpret_cast<const u32x4_at2*>(at);
+  }
+
+  // With every check: 0 from k_hi on and past the columns' edge.
+  __device__ __forceinline__ u32x4 load_checked(uint64_t k, uint64_t k_hi, int i) const {
+    if constexpr (FAST) {
+      if (k + chunk >= k_hi) return u32x4{0, 0, 0, 0};
+      return load8(p + (row_of(i * kStep + row) - first) * stride, k + chunk, k_hi);
+    } else {
+      const uint64_t t = k + i * kStep + row;
+      if (t >= k_hi || first + chunk >= extent) return u32x4{0, 0, 0, 0};
+      return load8(p + t * stride, first + chunk, extent);
+    }
+  }
+
+  __device__ __forceinline__ void stage(uint16_t* tile, int i, u32x4 w) const {
+    const uint32_t r = i * kStep + row;
+    uint16_t* at;
+    if constexpr (FAST)
+      at = tile + r * kMulDepth + (chunk ^ ((r / 2 % 8) * kChunk));
+    else
+      at = tile + r * TILE + ((((chunk >> 5) ^ (r & 3)) << 5) | (chunk & 31));
+    *reinterpret_cast<u32x4*>(at) = w;
+  }
+
+  // Part q of kReads of a fragment: 32 rows from `at` on, 16 k from `step` * 16 on.
+  // Lane l gets row l % 32 of eight k, from 8 (l / 32) on.
+  static __device__ __forceinline__ void read(const uint16_t* tile, int step, uint32_t at, int q,
+                                              u32x4& to) {
+    const uint32_t lane = threadIdx.x % 64;
+    if constexpr (FAST) {
+      const uint32_t r = at + lane % 32, c = step * 2 + lane / 32;
+      to = *reinterpret_cast<const u32x4*>(tile + r * kMulDepth + ((c ^ (r / 2 % 8)) * kChunk));
+    } else {
+      typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+      const uint32_t r = step * kMulStep + (lane / 32) * 8 + (lane % 16) / 4 + q * 4;
+      const uint32_t c = at + (lane / 16 % 2) * 16 + lane % 4 * 4;
+      const uint16_t* from = tile + r * TILE + ((((c >> 5) ^ (r & 3)) << 5) | (c & 31));
+      const u32x2 v = __builtin_bit_cast(
+          u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                     (lds_s16x4*)(__attribute__((address_space(3))) uint16_t*)from));
+      to[2 * q] = v[0];
+      to[2 * q + 1] = v[1];
+    }
+  }
+};
+
+// The k below which an operand's turns may be loaded without a check: whole chunks
+// stay inside the matrix's memory, and offsets inside a tile within 32 bits.
+inline uint64_t safe_k(const Operand& o, bool fast, uint64_t k, bool pairs = false) {
+  constexpr uint64_t kFar = 1ull << 30;
+  if (o.stride >= kFar / 512) return 0;
+  if (fast) return ((pairs ? o.extent : 0) + 256) * o.stride < kFar * 2 - kMulDepth ? k : 0;
+  const uint64_t over = (kChunk - o.extent % kChunk) % kChunk;
+  if (over == 0) return k;
+  const uint64_t back = k > 1 ? (over + o.stride - 1) / o.stride : k;
+  return back < k ? k - back : 0;
+}
+
+// The tile and split of a workgroup.  Workgroups go to the eight dies in turn, each
+// with an L2 of its own: die x takes the x-th eighth of the pieces, and pieces run
+// down groups of eight tile rows, so that the 32 that a die has in hand together
+// read 8 + 4 strips of the operands.
+struct Spot {
+  uint32_t split, m, n;
+};
+
+__device__ __forceinline__ Spot spot_of(uint32_t wg, uint32_t wgs, uint32_t tiles_m,
+                                        uint32_t tiles_n) {
+  constexpr uint32_t kDies = 8, kGroup = 8;
+  const uint32_t die = wg % kDies, each = wgs / kDies, more = wgs % kDies;
+  const uint32_t id = die * each + (die < more ? die : more) + wg / kDies;
+  const uint32_t tiles = tiles_m * tiles_n;
+  const uint32_t split = id / tiles, tile = id % tiles;
+  const uint32_t group = tile / (kGroup * tiles_n), rest = tile % (kGroup * tiles_n);
+  const uint32_t row0 = group * kGroup;
+  const uint32_t rows = tiles_m - row0 < kGroup ? tiles_m - row0 : kGroup;
+  return {split, row0 + rest % rows, rest / rows};
+}
+
+// WM x WN waves.  An epilogue E holds what it writes and
+//   put<T>(split, m, n, rows, x):  eight neighbouring sums x of row m, from column n on
+//     (a multiple of eight; rows from `rows` on and columns past the edge among them),
+//     or, with E::kPairs, put<T>(split, m, n, rows, x, y) of the same columns of both
+//     stacked matrices.
+// All lanes of a wave call it together.
+template <typename T, bool AF, bool BF, int TM, int TN, int WM, int WN, typename E>
+__global__ __launch_bounds__(kMulThreads) void product_kernel(Operand a, Operand b, Extents x,
+                                                              uint64_t safe, E epilogue) {
+  static_assert(WM * WN == 4, "four waves");
+  typedef Side<AF, TM> A;
+  typedef Side<BF, TN, E::kPairs ? TN / WN / 2 : 0> B;
+  constexpr int kFm = TM / WM / kMulFrag, kFn = TN / WN / kMulFrag;
+  constexpr int kSub = kMulDepth / kMulStep, kMul = kFm * kFn;
+  constexpr uint32_t kCols = TN / WN, kPitch = kCols + 8;
+  constexpr uint32_t kTiles = A::kElems + B::kElems;        // 32-bit words of two buffers
+  constexpr uint32_t kOut = 4 * kMulFrag * kPitch;
+  __shared__ __attribute__((aligned(16))) float lds[kTiles > kOut ? kTiles : kOut];
+  uint16_t* la = reinterpret_cast<uint16_t*>(lds);
+  uint16_t* lb = la + 2 * A::kElems;
+
+  uint64_t m_all = x.m, k_all = x.k;
+  if (x.count) {
+    const uint64_t c = *x.count;
+    const uint64_t left = c > x.first ? c - x.first : 0;
+    uint64_t& of = x.count_k ? k_all : m_all;
+    of = left < of ? left : of;
+  }
+  const uint32_t tiles_m = static_cast<uint32_t>((m_all + TM - 1) / TM);
+  constexpr int kOutN = E::kPairs ? TN / 2 : TN;            // columns of c a tile
+  const uint32_t tiles_n = static_cast<uint32_t>((x.n + kOutN - 1) / kOutN);
+  const uint32_t wgs = tiles_m * tiles_n * x.splits;
+  if (blockIdx.x >= wgs) return;
+  const Spot at = spot_of(blockIdx.x, wgs, tiles_m, tiles_n);
+  const uint64_t m0 = static_cast<uint64_t>(at.m) * TM, n0 = static_cast<uint64_t>(at.n) * kOutN;
+  const uint64_t per = ((k_all + x.splits - 1) / x.splits + kMulDepth - 1) / kMulDepth * kMulDepth;
+  const uint64_t k_lo = at.split * per < k_all ? at.split * per : k_all;
+  const uint64_t k_hi = k_lo + per < k_all ? k_lo + per : k_all;
+  const uint32_t tid = threadIdx.x, wave = tid / 64;
+  const uint32_t wm = wave / WN * (TM / WM), wn = wave % WN * kCols;
+
+  A sa;
+  B sb;
+  sa.begin(a, m0);
+  sb.begin(b, n0);
+  constexpr int kItems = A::kPass + B::kPass;
+  u32x4 reg[kItems];                                        // a's loads, then b's
+  auto load_any = [&](uint64_t k) __attribute__((always_inline)) {
+#pragma unroll (kItems % 8 ? kItems : 1)
+    for (int i = 0; i < kItems; ++i) {
+      const u32x4 v = i < A::kPass ? sa.load_checked(k, k_hi, i)
+                                   : sb.load_checked(k, k_hi, i - A::kPass);
+#pragma unroll
+      for (int q = 0; q < kItems; ++q)                      // registers take fixed indexes
+        if (q == i) reg[q] = v;
+    }
+  };
+  auto load_one = [&](uint64_t k, int i) __attribute__((always_inline)) {
+    reg[i] = i < A::kPass ? sa.load(k, i) : sb.load(k, i - A::kPass);
+  };
+  auto stage = [&](int buf, int i) __attribute__((always_inline)) {
+    if (i < A::kPass) sa.stage(la + buf * A::kElems, i, reg[i]);
+    else sb.stage(lb + buf * B::kElems, i - A::kPass, reg[i]);
+  };
+  const uint64_t whole = k_hi < safe ? k_hi : safe;
+  auto load = [&](uint64_t k) __attribute__((always_inline)) {
+    if (k + kMulDepth <= whole) {
+#pragma unroll
+      for (int i = 0; i < kItems; ++i) load_one(k, i);
+    } else {
+      load_any(k);
+    }
+  };
+
+  f32x16 acc[kFm][kFn];
+#pragma unroll
+  for (int i = 0; i < kFm; ++i)
+#pragma unroll
+    for (int j = 0; j < kFn; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+
+  // Fragments of a step in the order of their use: a0, b0 .. b(kFn-1), a1 .. a(kFm-1).
+  u32x4 fa[2][kFm], fb[2][kFn];
+  constexpr int kReads = kFm * A::kReads + kFn * B::kReads;
+  auto read = [&](int buf, int s, int to, int q) __attribute__((always_inline)) {
+    if (q < A::kReads) {
+      A::read(la + buf * A::kElems, s, wm, q, fa[to][0]);
+    } else if (q < A::kReads + kFn * B::kReads) {
+      const int i = (q - A::kReads) / B::kReads;
+      B::read(lb + buf * B::kElems, s, wn + i * kMulFrag, (q - A::kReads) % B::kReads, fb[to][i]);
+    } else {
+      const int w = q - kFn * B::kReads, i = w / A::kReads;
+      A::read(la + buf * A::kElems, s, wm + i * kMulFrag, w % A::kReads, fa[to][i]);
+    }
+  };
+
+  load(k_lo);
+#pragma unroll
+  for (int i = 0; i < kItems; ++i) stage(0, i);
+  load(k_lo + kMulDepth);
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < kReads; ++q) read(0, 0, 0, q);
+  uint32_t buf = 0;
+  uint64_t k0 = k_lo;
+  static_assert(kSub % 2 == 0, "the operands' registers take turns");
+  // A turn: all of tile k0's steps; tile k0 + 64 from registers to the other buffer
+  // (last read before the barrier of the turn before) over all steps but the last;
+  // then the barrier, behind which the next tile's first operands are read while the
+  // last step runs.  Other work goes between the matrix instructions in equal parts,
+  // and the compiler keeps it there.
+  constexpr int kSlots = (kSub - 1) * kMul;
+  constexpr int kItemsEach = (kItems + kSlots - 1) / kSlots;
+  constexpr int kReadsEach = (kReads + kMul - 1) / kMul;
+  auto turn = [&](auto refill) __attribute__((always_inline)) {
+#pragma unroll
+    for (int s = 0; s < kSub; ++s) {
+      const bool last = s + 1 == kSub;
+      if (last) __syncthreads();
+#pragma unroll
+      for (int w = 0; w < kMul; ++w) {
+        const int i = w / kFn, j = w % kFn;
+        acc[i][j] = mul<T>(fa[s & 1][i], fb[s & 1][j], acc[i][j]);
+#pragma unroll
+        for (int d = 0; d < kReadsEach; ++d) {
+          const int q = w * kReads / kMul + d;
+          if (q < (w + 1) * kReads / kMul)
+            read(last ? buf ^ 1 : buf, last ? 0 : s + 1, (s + 1) & 1, q);
+        }
+#pragma unroll
+        for (int d = 0; d < kItemsEach; ++d) {
+          const int slot = s * kMul + w, q = slot * kItems / kSlots + d;
+          if (last || q >= (slot + 1) * kItems / kSlots) continue;
+          stage(buf ^ 1, q);
+          refill(q);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    buf ^= 1;
+  };
+#pragma unroll 1
+  for (; k0 + 3 * kMulDepth <= whole; k0 += kMulDepth)
+    turn([&](int i) { load_one(k0 + 2 * kMulDepth, i); });
+#pragma unroll 1
+  for (; k0 < k_hi; k0 += kMulDepth) {
+    turn([](int) {});
+    load_any(k0 + 2 * kMulDepth);                           // zeros past the end
+  }
+  __syncthreads();
+
+  // Through shared memory, so that a lane has eight neighbouring columns: each wave
+  // turns 32 rows at a time in a piece of its own, whose rows lie kPitch words apart
+  // (4 kPitch = 32 mod 64: the two halves of a wave, four rows apart, meet different
+  // banks).
+  const uint32_t lane = tid % 64;
+  static_assert((4 * kPitch) % 64 == 32, "");
+  float* piece = lds + wave * kMulFrag * kPitch;
+#pragma unroll
+  for (int i = 0; i < kFm; ++i) {
+#pragma unroll
+    for (int j = 0; j < kFn; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        piece[(r / 4 * 8 + lane / 32 * 4 + r % 4) * kPitch + j * kMulFrag + lane % 32] =
+            acc[i][j][r];
+    wave_fence();
+    constexpr uint32_t kWide = E::kPairs ? kCols / 2 : kCols;  // columns of c a wave
+    constexpr uint32_t kLanes = kWide / kChunk;             // lanes of a row
+    constexpr int kRows = kMulFrag * kLanes / 64;           // passes over the 32 rows
+    const uint32_t q = lane / kLanes, c = lane % kLanes * kChunk;
+#pragma unroll 2
+    for (int r = 0; r < kRows; ++r) {
+      const uint32_t line = q + r * (64 / kLanes);
+      const float* p = piece + line * kPitch + c;
+      const uint64_t m = m0 + wm + i * kMulFrag + line;
+      const uint64_t n = n0 + (E::kPairs ? wn / 2 : wn) + c;
+      const f32x4 u = *reinterpret_cast<const f32x4*>(p);
+      const f32x4 v = *reinterpret_cast<const f32x4*>(p + 4);
+      float s[8] = {u[0], u[1], u[2], u[3], v[0], v[1], v[2], v[3]};
+      if constexpr (E::kPairs) {
+        const f32x4 u2 = *reinterpret_cast<const f32x4*>(p + kWide);
+        const f32x4 v2 = *reinterpret_cast<const f32x4*>(p + kWide + 4);
+        float s2[8] = {u2[0], u2[1], u2[2], u2[3], v2[0], v2[1], v2[2], v2[3]};
+        epilogue.template put<T>(at.split, m, n, m_all, s, s2);
+      } else {
+        epilogue.template put<T>(at.split, m, n, m_all, s);
+      }
+    }
+    wave_fence();
+  }
+}
+
+// Where sums go: partial sums of splits (fp32, `lead` apart, joined afterwards by
+// join_kernel), running sums over several products, or the result itself, scaled and
+// rounded once.
+struct Sink {
+  static constexpr bool kPairs = false, kJoins = true;
+  void* out;
+  uint64_t stride;
+  int dtype, accumulate;   // kF16, kBf16 or kF32
+  uint64_t cols;
+  const uint32_t* rows;    // the result's row of row m, or nullptr: m
+  const float* factor;     // in device memory, or nullptr
+  float* partial;          // [splits][most rows][lead], or nullptr: one split
+  uint64_t split_size;
+  float* sums;             // [rows][lead] running sums, or nullptr
+  int add, last;           // add what `sums` holds; the result is final
+  uint64_t lead;           // cols, rounded up to a chunk
+
+  template <typename T>
+  __device__ __forceinline__ void finish(uint64_t m, uint64_t n, float (&x)[8]) const {
+    if (sums) {
+      f32x4* s = reinterpret_cast<f32x4*>(sums + m * lead + n);
+      if (add) {
+        const f32x4 u = s[0], v = s[1];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[i] = u[i] + x[i];
+          x[4 + i] = v[i] + x[4 + i];
+        }
+      }
+      if (!last) {
+        s[0] = f32x4{x[0], x[1], x[2], x[3]};
+        s[1] = f32x4{x[4], x[5], x[6], x[7]};
+        return;
+      }
+    }
+    if (factor) {
+      const float f = *factor;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] *= f;
+    }
+    const uint64_t row = (rows ? rows[m] : m) * stride;
+    if (dtype == kF32) {
+      float* o = static_cast<float*>(out) + row + n;
+      if (n + kChunk <= cols) {
+        f32x4_at4* w = reinterpret_cast<f32x4_at4*>(o);
+        f32x4 u = {x[0], x[1], x[2], x[3]}, v = {x[4], x[5], x[6], x[7]};
+        if (accumulate) {
+          u += w[0];
+          v += w[1];
+        }
+        w[0] = u;
+        w[1] = v;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (n + i < cols) o[i] = accumulate ? o[i] + x[i] : x[i];
+      }
+      return;
+    }
+    uint16_t* o = static_cast<uint16_t*>(out) + row;
+    if (accumulate) {
+      float old[8];
+      unpack8<T>(load8(o, n, cols), old);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] += old[i];
+    }
+    store8<false>(o, n, cols, pack8<T>(x));
+  }
+
+  template <typename T>
+  __device__ __forceinline__ void put(uint32_t split, uint64_t m, uint64_t n, uint64_t m_all,
+                                      float (&x)[8]) const {
+    if (m >= m_all || n >= cols) return;
+    if (partial) {
+      f32x4* p = reinterpret_cast<f32x4*>(partial + split * split_size + m * lead + n);
+      p[0] = f32x4{x[0], x[1], x[2], x[3]};
+      p[1] = f32x4{x[4], x[5], x[6], x[7]};
+      return;
+    }
+    finish<T>(m, n, x);
+  }
+};
+
+// Adds the splits' partial sums in their order, eight neighbouring columns a thread.
+template <typename T>
+__global__ __launch_bounds__(kMulThreads) void join_kernel(Sink s, Extents x) {
+  uint64_t m_all = x.m;
+  if (x.count && !x.count_k) {
+    const uint64_t c = *x.count;
+    const uint64_t left = c > x.first ? c - x.first : 0;
+    m_all = left < m_all ? left : m_all;
+  }
+  const uint64_t per_row = s.lead / kChunk;
+  const uint64_t id = static_cast<uint64_t>(blockIdx.x) * kMulThreads + threadIdx.x;
+  const uint64_t m = id / per_row, n = id % per_row * kChunk;
+  if (m >= m_all) return;
+  f32x4 u = {0.f, 0.f, 0.f, 0.f}, v = u;
+  const float* p = s.partial + m * s.lead + n;
+#pragma unroll 8
+  for (uint32_t i = 0; i < x.splits; ++i, p += s.split_size) {
+    u += *reinterpret_cast<const f32x4*>(p);
+    v += *reinterpret_cast<const f32x4*>(p + 4);
+  }
+  float sum[8] = {u[0], u[1], u[2], u[3], v[0], v[1], v[2], v[3]};
+  s.finish<T>(m, n, sum);
+}
+
+// How a product is cut: the tile of c (256 x 256, 128 x 128, or 32 rows x 128) and the
+// splits of k.
+struct MulPlan {
+  int tile;
+  uint32_t splits;
+  uint64_t tiles;
+};
+
+// The cut with the least estimated time, in microseconds as measured on MI355X: a
+// workgroup of 256 x 256 has a compute unit to itself and takes 14 us and 0.028 a k;
+// one of 128 x 128 takes 7 us and 0.015 a k alone on its unit, 0.021 beside a second
+// one; a join costs a launch, and its partial sums' way out and back.  n counts
+// columns of b's tile; few_rows: tiles of 32 rows are built (k fast in a).
+inline MulPlan plan_product(uint64_t m, uint64_t n, uint64_t k, bool may_split, bool few_rows) {
+  constexpr uint64_t kUnits = 256;
+  MulPlan best = {128, 1, 0};
+  double least = 0;
+  for (const int tile : {256, 128, 32}) {
+    if (tile == 32 && (m > 32 || !few_rows)) continue;
+    const uint64_t tn = tile == 256 ? 256 : 128;
+    const uint64_t tiles = ((m + tile - 1) / tile) * ((n + tn - 1) / tn);
+    for (const uint32_t s : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
+      if (s > 1 && (!may_split || k < 256 * s)) break;
+      const uint64_t per = ((k + s - 1) / s + 63) / 64 * 64, wgs = tiles * s;
+      const uint64_t at_once = tile == 256 ? kUnits : tile == 128 ? 2 * kUnits : 4 * kUnits;
+      const double rounds = static_cast<double>((wgs + at_once - 1) / at_once);
+      const double each = tile == 256 ? 0.028 : tile == 128 ? (wgs > kUnits ? 0.021 : 0.015)
+                                                            : (wgs > 2 * kUnits ? 0.02 : 0.01);
+      const double fix = tile == 256 ? 14.0 : tile == 128 ? 7.0 : 4.0;
+      double us = rounds * (fix + each * static_cast<double>(per));
+      if (s > 1) us += 3.0 + s * static_cast<double>(m) * static_cast<double>(n) * 8 / 6e6;
+      if (best.tiles == 0 || us < least) {
+        least = us;
+        best = {tile, s, tiles};
+      }
+    }
+  }
+  return best;
+}
+
+// The same cut over fewer rows of c.
+inline MulPlan plan_of(MulPlan p, uint64_t m, uint64_t n) {
+  const uint64_t tn = p.tile == 256 ? 256 : 128;
+  p.tiles = ((m + p.tile - 1) / p.tile) * ((n + tn - 1) / tn);
+  return p;
+}
+
+inline uint64_t chunks_up(uint64_t n, uint64_t to) { return (n + to - 1) / to * to; }
+
+// Whether a product, and the join of its splits, is one launch each.
+inline bool product_fits(const MulPlan& p, uint64_t m, uint64_t n) {
+  constexpr uint64_t kMost = most_workgroups(kMulThreads);
+  const uint64_t joins = p.splits > 1 ? (m * (chunks_up(n, kChunk) / kChunk)) / kMulThreads + 1 : 0;
+  return p.tiles <= kMost / p.splits && joins <= kMost;
+}
+
+// Enqueues the product (and the join of its splits, if E is a Sink).  m, n and k are
+// not 0.  n: columns of c.
+template <typename T, bool AF, bool BF, typename E>
+hipError_t run_product(const MulPlan& p, const Operand& a, const Operand& b, Extents x, const E& e,
+                       hipStream_t stream) {
+  x.splits = p.splits;
+  const uint64_t wgs = p.tiles * p.splits;
+  if (!product_fits(p, x.m, x.n)) return hipErrorInvalidConfiguration;
+  const uint64_t sa = safe_k(a, AF, x.k), sb = safe_k(b, BF, x.k, E::kPairs);
+  const uint64_t safe = sa < sb ? sa : sb;
+  const uint32_t grid = static_cast<uint32_t>(wgs);
+  if (p.tile == 256)
+    product_kernel<T, AF, BF, 256, 256, 2, 2, E>
+        <<<grid, kMulThreads, 0, stream>>>(a, b, x, safe, e);
+  else if (p.tile == 128)
+    product_kernel<T, AF, BF, 128, 128, 2, 2, E>
+        <<<grid, kMulThreads, 0, stream>>>(a, b, x, safe, e);
+  else if constexpr (AF && E::kPairs)
+    product_kernel<T, AF, BF, 32, 256, 1, 4, E>
+        <<<grid, kMulThreads, 0, stream>>>(a, b, x, safe, e);
+  else if constexpr (AF)
+    product_kernel<T, AF, BF, 32, 128, 1, 4, E>
+        <<<grid, kMulThreads, 0, stream>>>(a, b, x, safe, e);
+  hipError_t err = hipGetLastError();
+  if constexpr (!E::kPairs && E::kJoins) {
+    if (err != hipSuccess || p.splits == 1) return err;
+    const uint64_t joins = (x.m * (e.lead / kChunk) + kMulThreads - 1) / kMulThreads;
+    join_kernel<T><<<static_cast<uint32_t>(joins), kMulThreads, 0, stream>>>(e, x);
+    err = hipGetLastError();
+  }
+  return err;
+}
+
+}  // namespace act
+}  // namespace zero
+
+#endif  // ZERO_ACT_PRODUCT_H_

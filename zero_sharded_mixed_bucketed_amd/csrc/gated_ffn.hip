@@ -1,0 +1,232 @@
+// A layer's gated feed-forward block and its backward:
+//   a = act(x Wg^T) . (x Wu^T),  W = [Wg; Wu]
+// forward in one kernel (both projections, the activation, their product and the
+// 8-bit checkpoints of the two projections and of a); backward from the checkpoints:
+//   dg = da . u . act'(g), du = da . act(g);  dx = [dg du] W;  dW = [dg du]^T x^.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "act/format.h"
+#include "act/launch.h"
+#include "act/layer.h"
+#include "act/product.h"
+
+namespace zero {
+namespace act {
+namespace {
+
+constexpr float kLog2e = 1.44269504088896341f;
+
+__device__ __forceinline__ float sigmoid(float g) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * g));
+}
+
+// The share p of g that passes, act(g) = g p, and its slope dp/dg.  Powers that
+// overflow give p = 0 or 1; the slope's product with g is then 0.
+__device__ __forceinline__ float passed(float g, int act, float* slope) {
+  if (act == kSilu) {
+    const float p = sigmoid(g);
+    *slope = p * (1.0f - p);
+    return p;
+  }
+  if (act == kGelu) {
+    *slope = 0.398942280401432678f * __builtin_amdgcn_exp2f(-0.5f * kLog2e * g * g);
+    return 0.5f * erfcf(-0.707106781186547524f * g);
+  }
+  // (1 + tanh(y)) / 2 = sigmoid(2 y)
+  const float y2 = 1.59576912160573071f * (g + 0.044715f * g * g * g);
+  const float p = sigmoid(y2);
+  *slope = p * (1.0f - p) * (1.59576912160573071f + 0.214069822634528751f * g * g);
+  return p;
+}
+
+// act(g), and act'(g).  A slope of 0 stays 0 beside an infinite factor (g or g^2
+// past fp32's range) only where p has reached its end, so it is kept there.
+__device__ __forceinline__ float activate(float g, int act) {
+  float slope;
+  const float p = passed(g, act, &slope);
+  return p == 0.0f ? (g != g ? g : -0.0f) : g * p;
+}
+
+__device__ __forceinline__ float activate(float g, int act, float* derivative) {
+  float slope;
+  const float p = passed(g, act, &slope);
+  *derivative = p == 0.0f || p == 1.0f ? p : p + g * slope;
+  return p == 0.0f ? -0.0f : g * p;
+}
+
+// The forward's epilogue: both sums of a column to a, and their checkpoints.
+struct Gated {
+  static constexpr bool kPairs = true, kJoins = false;
+  Rows out;
+  Ckpt c_gate, c_up, c_out;
+  uint64_t cols;
+  int act, format;
+
+  template <typename T>
+  __device__ __forceinline__ void keep(const Ckpt& c, uint64_t m, uint64_t n, bool in,
+                                       u32x4 w) const {
+    if (!c.codes) return;
+    uint32_t scale;
+    const u32x2 codes = format == kInt8 ? encode8<T, kInt8>(w, &scale)
+                                        : encode8<T, kE4m3>(w, &scale);
+    if (!in) return;
+    store_codes(c.codes + m * c.code_stride, n, cols, codes);
+    if (n % kBlock == 0) c.scales[m * c.scale_stride + n / kBlock] = static_cast<uint8_t>(scale);
+  }
+
+  template <typename T>
+  __device__ __forceinline__ void put(uint32_t, uint64_t m, uint64_t n, uint64_t m_all,
+                                      float (&g)[8], float (&u)[8]) const {
+    const bool in = m < m_all && n < cols;
+    float a[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      // columns past the edge hold another row's sums: 0 in their block's scale
+      if (n + i >= cols) g[i] = u[i] = 0.0f;
+      a[i] = activate(g[i], act) * u[i];
+    }
+    const u32x4 held = pack8<T>(a);
+    if (in && out.p) store8(out.p + m * out.stride, n, cols, held);
+    keep<T>(c_gate, m, n, in, pack8<T>(g));
+    keep<T>(c_up, m, n, in, pack8<T>(u));
+    keep<T>(c_out, m, n, in, held);
+  }
+};
+
+template <typename T>
+hipError_t forward(const GatedLaunch& a, hipStream_t stream) {
+  const MulPlan p = plan_product(a.rows, 2 * a.width, a.cols, false, true);
+  const Operand x = {a.x.p, a.x.stride, a.rows}, w = {a.w.p, a.w.stride, a.width};
+  const Extents e = {a.rows, a.width, a.cols, 1, nullptr, 0, 0};
+  const Gated g = {a.out, a.c_gate, a.c_up, a.c_out, a.width, a.act, a.format};
+  return run_product<T, true, true>(p, x, w, e, g, stream);
+}
+
+// [dg du] of 512 columns of a row a wave: 8-bit codes and one 16-bit row in, two
+// 16-bit rows out, bound by memory.
+template <typename T, int FMT>
+__global__ __launch_bounds__(kMulThreads) void gated_slopes_kernel(GatedGradLaunch a, uint16_t* to,
+                                                                   uint64_t lead, uint64_t unit0,
+                                                                   uint64_t units,
+                                                                   uint32_t segments) {
+  const uint64_t unit = unit0 + static_cast<uint64_t>(blockIdx.x) * 4 +
+                        __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  if (unit >= units) return;
+  const uint64_t row = unit / segments;
+  const uint64_t c = unit % segments * 512 + threadIdx.x % 64 * kChunk;
+  if (c >= a.width) return;
+  float g[8], u[8], d[8], dg[8], du[8];
+  const u32x4 w = stream8(a.dout.p + row * a.dout.stride, c, a.width);
+  const u32x2 kg = load_codes(a.c_gate.codes + row * a.c_gate.code_stride, c, a.width);
+  const u32x2 ku = load_codes(a.c_up.codes + row * a.c_up.code_stride, c, a.width);
+  const uint32_t bg = a.c_gate.scales[row * a.c_gate.scale_stride + c / kBlock];
+  const uint32_t bu = a.c_up.scales[row * a.c_up.scale_stride + c / kBlock];
+  unpack8<T>(w, d);
+  decode8<FMT>(kg, scale_of(bg), g);
+  decode8<FMT>(ku, scale_of(bu), u);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float slope;
+    const float held = activate(g[i], a.act, &slope);
+    dg[i] = d[i] * u[i] * slope;
+    du[i] = d[i] * held;
+  }
+  uint16_t* o = to + row * lead;
+  store8<false>(o, c, a.width, pack8<T>(dg));
+  store8<false>(o + a.width, c, a.width, pack8<T>(du));
+}
+
+struct GradRoom {
+  uint64_t lead;            // of [dg du], in elements
+  MulPlan plan;             // of dx
+  uint64_t slopes, bytes;
+};
+
+GradRoom grad_room(uint64_t rows, uint64_t cols, uint64_t width) {
+  GradRoom r;
+  r.lead = chunks_up(2 * width, 64);
+  r.plan = plan_product(rows, cols, 2 * width, true, true);
+  r.slopes = chunks_up(rows * r.lead * 2, 256);
+  const uint64_t partial =
+      r.plan.splits > 1 ? r.plan.splits * rows * chunks_up(cols, kChunk) * 4 : 0;
+  const uint64_t weight = weight_grad_workspace(rows, cols, 2 * width);
+  r.bytes = r.slopes + (partial > weight ? partial : weight);
+  return r;
+}
+
+template <typename T>
+hipError_t backward(const GatedGradLaunch& a, hipStream_t stream) {
+  const GradRoom room = grad_room(a.rows, a.cols, a.width);
+  uint16_t* slopes = reinterpret_cast<uint16_t*>(a.workspace);
+  float* rest = reinterpret_cast<float*>(a.workspace + room.slopes);
+  if (a.rows) {
+    const uint64_t segments = (a.width + 511) / 512, units = a.rows * segments;
+    constexpr uint64_t kMost = most_workgroups(kMulThreads);
+    for (uint64_t unit = 0; unit < units; unit += 4 * kMost) {
+      const uint64_t left = (units - unit + 3) / 4;
+      const uint32_t grid = static_cast<uint32_t>(left < kMost ? left : kMost);
+      if (a.format == kInt8)
+        gated_slopes_kernel<T, kInt8><<<grid, kMulThreads, 0, stream>>>(
+            a, slopes, room.lead, unit, units, static_cast<uint32_t>(segments));
+      else
+        gated_slopes_kernel<T, kE4m3><<<grid, kMulThreads, 0, stream>>>(
+            a, slopes, room.lead, unit, units, static_cast<uint32_t>(segments));
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
+  }
+  if (a.dx.p && a.rows) {
+    const Operand d = {slopes, room.lead, a.rows}, w = {a.w.p, a.w.stride, a.cols};
+    const Extents x = {a.rows, a.cols, 2 * a.width, 1, nullptr, 0, 0};
+    Sink s = {};
+    s.out = a.dx.p;
+    s.stride = a.dx.stride;
+    s.dtype = T::kType;
+    s.cols = a.cols;
+    s.lead = chunks_up(a.cols, kChunk);
+    if (room.plan.splits > 1) {
+      s.partial = rest;
+      s.split_size = a.rows * s.lead;
+    }
+    const hipError_t e = run_product<T, true, false>(room.plan, d, w, x, s, stream);
+    if (e != hipSuccess) return e;
+  }
+  if (!a.dw) return hipSuccess;
+  WeightGradLaunch L;
+  L.x = a.c_x;
+  L.rows = a.rows;
+  L.k = a.cols;
+  L.n = 2 * a.width;
+  L.dy = slopes;
+  L.dy_stride = room.lead;
+  L.dtype = T::kType;
+  L.dw = a.dw;
+  L.dw_stride = a.dw_stride;
+  L.dw_dtype = a.dw_dtype;
+  L.accumulate = a.accumulate;
+  L.partial = rest;
+  return launch_weight_grad(L, stream);
+}
+
+}  // namespace
+
+uint64_t gated_grad_workspace(uint64_t rows, uint64_t cols, uint64_t width) {
+  return grad_room(rows, cols, width).bytes;
+}
+
+bool gated_fits(uint64_t rows, uint64_t cols, uint64_t width, bool dx) {
+  if (dx) return product_fits(grad_room(rows, cols, width).plan, rows, cols);
+  return product_fits(plan_product(rows, 2 * width, cols, false, true), 0, 0);
+}
+
+hipError_t launch_gated_ffn(const GatedLaunch& a, hipStream_t stream) {
+  return a.dtype == kF16 ? forward<F16>(a, stream) : forward<Bf16>(a, stream);
+}
+
+hipError_t launch_gated_ffn_grad(const GatedGradLaunch& a, hipStream_t stream) {
+  return a.dtype == kF16 ? backward<F16>(a, stream) : backward<Bf16>(a, stream);
+}
+
+}  // namespace act
+}  // namespace zero

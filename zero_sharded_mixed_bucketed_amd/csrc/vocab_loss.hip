@@ -1,0 +1,486 @@
+// Losses over a vocabulary, from the last hidden states x and the projection W, and
+// their gradients, without keeping the logits z = x W^T / tau:
+//   cross entropy  l_t = w_t (lse_t - z_ty)
+//   distillation   l_t = w_t tau^2 sum over j of q_tj (log q_tj - (z_tj - lse_t)),
+//                  q_t the softmax of a teacher's top logits / tau
+//   g_t = w_t (p_t - q_t) (p_t the softmax of z_t; q_t is 1 at the target for the first)
+//   dx = c g W,  dW = c g^T x,  c = scale * tau
+//
+// Tokens go in pieces whose logits fit a bounded workspace: the logits of a piece in
+// fp32, one pass over each row that replaces them with g in 16 bits, and the two
+// products with it.  That is three products for the three that the definition has;
+// pieces of the vocabulary with all tokens in each would need a fourth (g needs the
+// whole row's sum first).  g is the only value that is rounded on the way: at a
+// target p - q is formed in fp32 from fp32 logits, so what cancels there is not lost.
+//
+// Tokens without a target are left out of everything: the others are first brought
+// together, so what a left-out token holds (NaN and infinities too) reaches nothing.
+#include <hip/hip_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "act/format.h"
+#include "act/launch.h"
+#include "act/layer.h"
+#include "act/product.h"
+
+namespace zero {
+namespace act {
+namespace {
+
+constexpr float kLog2e = 1.44269504088896341f;
+constexpr float kLowest = -3.402823466e38f;
+constexpr int kPickThreads = 1024, kRowThreads = 512;
+
+// fp16 holds g as 2^14 g / 2^e, e the least with all weights at most 2^e: |g| 2^-e <= 1
+// leaves the probabilities 28 binary places above its smallest normal value.  bf16
+// needs no such factor and takes the same.
+constexpr int kGradBits = 14;
+
+struct Head {
+  uint32_t count;           // tokens with a loss
+  float held;               // 2^14 / 2^e
+  float unit;               // c 2^e / 2^14
+};
+
+// The workspace: what lies where.
+struct Room {
+  uint64_t piece, pieces;   // tokens of a piece
+  uint64_t lead_x, lead_z, lead_w;
+  uint64_t rows, slots, flags, x, z, sums, partial, bytes;
+  MulPlan logits, dx, dw;
+};
+
+// Bytes of a piece's logits, at most (a piece has 256 tokens at least).  Larger pieces
+// add to dW's running sums less often.
+constexpr uint64_t kPieceBytes = 1ull << 31;
+constexpr uint64_t kMostRows = 1ull << 22;  // of a piece: a workgroup a row in one launch
+
+Room room_of(uint64_t rows, uint64_t cols, uint64_t vocab, bool dx, bool dw) {
+  Room r = {};
+  r.lead_x = chunks_up(cols, 64);
+  r.lead_z = chunks_up(vocab, 128);  // whole tiles of the logits' product
+  r.lead_w = chunks_up(cols, kChunk);
+  uint64_t most = kPieceBytes / (4 * r.lead_z) / 256 * 256;
+  if (most < 256) most = 256;
+  if (most > kMostRows) most = kMostRows;
+  r.piece = rows < most ? rows : most;
+  r.pieces = rows ? (rows + r.piece - 1) / r.piece : 1;
+  uint64_t at = 256;
+  const auto take = [&](uint64_t bytes) {
+    const uint64_t from = at;
+    at = chunks_up(at + bytes, 256);
+    return from;
+  };
+  r.rows = take(rows * 4);
+  r.slots = take(rows * 4);
+  r.flags = take(rows);
+  r.x = take(r.piece * r.lead_x * 2);
+  r.z = take(r.piece * r.lead_z * 4);
+  r.logits = plan_product(r.piece, vocab, cols, false, true);
+  uint64_t partial = 0;
+  if (dx) {
+    r.dx = plan_product(r.piece, cols, vocab, true, true);
+    if (r.dx.splits > 1) partial = r.dx.splits * r.piece * r.lead_w * 4;
+  }
+  if (dw) {
+    r.dw = plan_product(vocab, cols, r.piece, true, false);
+    const uint64_t more = r.dw.splits > 1 ? r.dw.splits * vocab * r.lead_w * 4 : 0;
+    if (more > partial) partial = more;
+    if (r.pieces > 1) r.sums = take(vocab * r.lead_w * 4);
+  }
+  r.partial = take(partial);
+  r.bytes = at;
+  return r;
+}
+
+__device__ __forceinline__ int64_t id_at(const VocabLaunch& a, uint64_t t, uint32_t j) {
+  const uint64_t i = t * a.ids_stride + j;
+  return a.ids_64 ? static_cast<const int64_t*>(a.ids)[i] : static_cast<const int32_t*>(a.ids)[i];
+}
+
+// Whether a token has entries: a wave a token.
+__global__ __launch_bounds__(256) void loss_flags_kernel(VocabLaunch a, uint8_t* flags) {
+  const uint64_t t = static_cast<uint64_t>(blockIdx.x) * 4 + threadIdx.x / 64;
+  if (t >= a.rows) return;
+  bool any = false;
+  for (uint32_t j = threadIdx.x % 64; j < a.top; j += 64) any |= id_at(a, t, j) >= 0;
+  const bool some = __builtin_amdgcn_ballot_w64(any) != 0;
+  if (threadIdx.x % 64 == 0) flags[t] = some;
+}
+
+// The tokens that have a loss, in their order; each token's place among them; the
+// largest weight's power of two.  One workgroup.
+__global__ __launch_bounds__(kPickThreads) void loss_pick_kernel(VocabLaunch a,
+                                                                 const uint8_t* flags,
+                                                                 uint32_t* rows, uint32_t* slots,
+                                                                 Head* head, float c) {
+  __shared__ uint32_t counts[kPickThreads / 64];
+  __shared__ float tops[kPickThreads / 64];
+  const uint32_t lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+  uint32_t before = 0;
+  float top = 0.0f;
+  for (uint64_t t0 = 0; t0 < a.rows; t0 += kPickThreads) {
+    const uint64_t t = t0 + threadIdx.x;
+    bool in = t < a.rows && (a.top ? flags[t] != 0 : id_at(a, t, 0) >= 0);
+    if (in && a.weights) {
+      const float w = a.weights[t];
+      in = w != 0.0f;                                   // NaN is a weight
+      top = fabsf(w) > top || w != w ? fabsf(w) : top;
+    }
+    const uint64_t votes = __builtin_amdgcn_ballot_w64(in);
+    if (lane == 0) counts[wave] = __popcll(votes);
+    __syncthreads();
+    uint32_t at = before + __popcll(votes & ((1ull << lane) - 1));
+    for (uint32_t i = 0; i < kPickThreads / 64; ++i) {
+      if (i < wave) at += counts[i];
+      before += counts[i];
+    }
+    if (t < a.rows) slots[t] = in ? at : UINT32_MAX;
+    if (in) rows[at] = static_cast<uint32_t>(t);
+    __syncthreads();
+  }
+  for (int i = 1; i < 64; i *= 2) top = fmaxf(top, __shfl_xor(top, i));
+  if (lane == 0) tops[wave] = top;
+  __syncthreads();
+  if (threadIdx.x) return;
+  for (uint32_t i = 1; i < kPickThreads / 64; ++i) top = fmaxf(top, tops[i]);
+  int e = 0;
+  if (a.weights && top > 0.0f && top < INFINITY) {
+    frexpf(top, &e);                                    // top < 2^e
+    e = e < -100 ? -100 : e > 100 ? 100 : e;
+  }
+  head->count = before;
+  head->held = ldexpf(1.0f, kGradBits - e);
+  head->unit = ldexpf(c, e - kGradBits);
+}
+
+// Brings a piece's tokens together: those at places [first, first + most) among the ones
+// with a loss.  The first piece also clears the others' loss and dx.  A wave a token.
+__global__ __launch_bounds__(256) void loss_rows_kernel(VocabLaunch a, const uint32_t* slots,
+                                                        uint64_t first, uint64_t most,
+                                                        uint16_t* to, uint64_t lead) {
+  const uint64_t t = static_cast<uint64_t>(blockIdx.x) * 4 + threadIdx.x / 64;
+  if (t >= a.rows) return;
+  const uint32_t slot = __builtin_amdgcn_readfirstlane(slots[t]);
+  const uint64_t c0 = threadIdx.x % 64 * kChunk;
+  if (slot == UINT32_MAX) {
+    if (first) return;
+    if (threadIdx.x % 64 == 0) a.loss[t] = 0.0f;
+    if (a.dx.p)
+      for (uint64_t c = c0; c < a.cols; c += 512)
+        store8<false>(a.dx.p + t * a.dx.stride, c, a.cols, u32x4{0, 0, 0, 0});
+    return;
+  }
+  if (slot < first || slot >= first + most) return;
+  const uint16_t* from = a.x.p + t * a.x.stride;
+  for (uint64_t c = c0; c < lead; c += 512)
+    *reinterpret_cast<u32x4*>(to + (slot - first) * lead + c) =
+        c < a.cols ? load8(from, c, a.cols) : u32x4{0, 0, 0, 0};
+}
+
+// A piece's logits, scaled; those past the vocabulary are -infinity up to the row's end.
+struct Logits {
+  static constexpr bool kPairs = false, kJoins = false;
+  float* z;
+  uint64_t lead, vocab;
+  float scale;
+
+  template <typename T>
+  __device__ __forceinline__ void put(uint32_t, uint64_t m, uint64_t n, uint64_t m_all,
+                                      float (&x)[8]) const {
+    if (m >= m_all || n >= lead) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = n + i < vocab ? x[i] * scale : -INFINITY;
+    f32x4* p = reinterpret_cast<f32x4*>(z + m * lead + n);
+    p[0] = f32x4{x[0], x[1], x[2], x[3]};
+    p[1] = f32x4{x[4], x[5], x[6], x[7]};
+  }
+};
+
+__device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
+
+// The sum of v over the workgroup, in every thread; the order is fixed.
+__device__ __forceinline__ float group_sum(float v, float* room) {
+  v = wave_sum(v);
+  __syncthreads();
+  if (threadIdx.x % 64 == 0) room[threadIdx.x / 64] = v;
+  __syncthreads();
+  float s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kRowThreads / 64; ++i) s += room[i];
+  return s;
+}
+
+__device__ __forceinline__ float group_max(float v, float* room) {
+  for (int i = 1; i < 64; i *= 2) v = fmaxf(v, __shfl_xor(v, i));
+  __syncthreads();
+  if (threadIdx.x % 64 == 0) room[threadIdx.x / 64] = v;
+  __syncthreads();
+  float s = room[0];
+#pragma unroll
+  for (int i = 1; i < kRowThreads / 64; ++i) s = fmaxf(s, room[i]);
+  return s;
+}
+
+__device__ __forceinline__ float teacher_at(const VocabLaunch& a, uint64_t t, uint32_t j) {
+  const uint64_t i = t * a.logits_stride + j;
+  if (a.logits_dtype == kF32) return static_cast<const float*>(a.logits)[i];
+  const uint16_t w = static_cast<const uint16_t*>(a.logits)[i];
+  return a.logits_dtype == kF16 ? lo16<F16>(w) : lo16<Bf16>(w);
+}
+
+// One row a workgroup: its maximum and sum, its loss, and (GRAD) g in place of its
+// logits, 16 bits from the row's begin on.
+template <typename T, bool GRAD>
+__global__ __launch_bounds__(kRowThreads) void loss_row_kernel(VocabLaunch a, const Head* head,
+                                                               const uint32_t* rows, uint64_t first,
+                                                               float* z_all, uint64_t lead) {
+  __shared__ float room[kRowThreads / 64];
+  __shared__ int32_t ids[kMaxTop];
+  __shared__ float shares[kMaxTop];
+  const uint64_t slot = first + blockIdx.x;
+  if (slot >= head->count) return;
+  const uint32_t t = rows[slot];
+  float* z = z_all + blockIdx.x * lead;
+  const uint32_t tid = threadIdx.x;
+
+  // the maximum m and the sum s of exp(z - m)
+  float m = kLowest, s = 0.0f;
+  for (uint64_t c = tid * 4; c < lead; c += kRowThreads * 4) {
+    const f32x4 v = *reinterpret_cast<const f32x4*>(z + c);
+    const float top = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+    if (top > m) {
+      s *= exp_of(m - top);
+      m = top;
+    }
+    s += (exp_of(v[0] - m) + exp_of(v[1] - m)) + (exp_of(v[2] - m) + exp_of(v[3] - m));
+  }
+  const float all = group_max(m, room);
+  s = group_sum(s * exp_of(m - all), room);
+  m = all;
+  const float log_s = logf(s);
+
+  float w = a.weights ? a.weights[t] : 1.0f;
+  // the entries: their shares q, and the loss
+  constexpr int kEach = kMaxTop / kRowThreads;
+  float target[kEach];
+  float loss;
+  bool lost = false;                                    // an id past the vocabulary
+  if (a.top == 0) {
+    const int64_t id = id_at(a, t, 0);
+    lost = id >= static_cast<int64_t>(a.vocab);
+    target[0] = lost ? 0.0f : z[id];
+    if (tid == 0) {
+      ids[0] = static_cast<int32_t>(id);
+      shares[0] = 1.0f;
+    }
+    loss = w * ((m - target[0]) + log_s);
+  } else {
+    float e[kEach], at[kEach], most = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const uint32_t j = tid + i * kRowThreads;
+      int64_t id = j < a.top ? id_at(a, t, j) : -1;
+      at[i] = target[i] = 0.0f;
+      e[i] = -INFINITY;
+      if (id >= 0) {
+        e[i] = teacher_at(a, t, j) / a.tau;
+        most = fmaxf(most, e[i]);
+        if (id >= static_cast<int64_t>(a.vocab)) {
+          lost = true;
+          id = -1;
+        } else {
+          target[i] = z[id];
+        }
+        at[i] = 1.0f;
+      }
+      if (j < a.top) ids[j] = static_cast<int32_t>(id);
+    }
+    most = group_max(most, room);
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      e[i] = at[i] != 0.0f ? e[i] - most : 0.0f;        // log of the share, before the sum
+      at[i] = at[i] != 0.0f ? exp_of(e[i]) : 0.0f;
+      sum += at[i];
+    }
+    sum = group_sum(sum, room);
+    const float log_sum = logf(sum);
+    float part = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const uint32_t j = tid + i * kRowThreads;
+      const float q = at[i] / sum;
+      if (j < a.top) shares[j] = q;
+      // a share of 0 adds nothing, however far its logarithm is
+      if (q != 0.0f) part += q * ((e[i] - log_sum) - ((target[i] - m) - log_s));
+    }
+    loss = group_sum(part, room) * (w * (a.tau * a.tau));
+    lost = group_max(lost ? 1.0f : 0.0f, room) != 0.0f;
+  }
+  if (lost) loss = w = __builtin_nanf("");
+  if (tid == 0) a.loss[t] = loss;
+  if constexpr (GRAD) {
+    const float each = w * head->held / s, held = w * head->held;
+    uint16_t* g = reinterpret_cast<uint16_t*>(z);
+    const uint32_t some = a.top ? a.top : 1;
+    // the entries' own values of g, from fp32 logits: an id that stands there twice
+    // takes the shares of both
+    float own[kEach];
+    __syncthreads();                                    // ids and shares
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const uint32_t j = tid + i * kRowThreads;
+      own[i] = 0.0f;
+      if (j < some && ids[j] >= 0) {
+        float q = 0.0f;
+        for (uint32_t l = 0; l < some; ++l)
+          if (ids[l] == ids[j]) q += shares[l];
+        own[i] = (exp_of(target[i] - m) / s - q) * held;
+      }
+      forget(own[i]);
+    }
+    // Chunk i of g goes over logits of chunk i / 2: a barrier at every power of two
+    // keeps all threads' loads of those before it.
+    constexpr uint64_t kStep = kRowThreads * kChunk;
+    uint64_t chunk = 0;
+    for (uint64_t c0 = 0; c0 < lead; c0 += kStep, ++chunk) {
+      const uint64_t c = c0 + tid * kChunk;
+      f32x4 u = {0.f, 0.f, 0.f, 0.f}, v = u;
+      if (c < lead) {
+        u = *reinterpret_cast<const f32x4*>(z + c);
+        v = *reinterpret_cast<const f32x4*>(z + c + 4);
+      }
+      forget(u);
+      forget(v);
+      if ((chunk & (chunk - 1)) == 0) __syncthreads();
+      float x[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[i] = exp_of(u[i] - m) * each;
+        x[4 + i] = exp_of(v[i] - m) * each;
+      }
+      if (c < lead) *reinterpret_cast<u32x4*>(g + c) = pack8<T>(x);
+    }
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const uint32_t j = tid + i * kRowThreads;
+      if (j < some && ids[j] >= 0 && ids[j] < static_cast<int64_t>(a.vocab))
+        g[ids[j]] = static_cast<uint16_t>(pack16<T>(own[i], 0.0f));
+    }
+  }
+}
+
+template <typename T>
+hipError_t run_loss(const VocabLaunch& a, hipStream_t stream) {
+  const bool dx = a.dx.p != nullptr, dw = a.dw != nullptr;
+  const Room r = room_of(a.rows, a.cols, a.vocab, dx, dw);
+  uint8_t* ws = a.workspace;
+  Head* head = reinterpret_cast<Head*>(ws);
+  uint32_t* rows = reinterpret_cast<uint32_t*>(ws + r.rows);
+  uint32_t* slots = reinterpret_cast<uint32_t*>(ws + r.slots);
+  uint16_t* x = reinterpret_cast<uint16_t*>(ws + r.x);
+  float* z = reinterpret_cast<float*>(ws + r.z);
+  float* partial = reinterpret_cast<float*>(ws + r.partial);
+  const uint32_t waves = static_cast<uint32_t>((a.rows + 3) / 4);
+  hipError_t e = hipSuccess;
+  if (a.rows) {
+    if (a.top) {
+      loss_flags_kernel<<<waves, 256, 0, stream>>>(a, ws + r.flags);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    loss_pick_kernel<<<1, kPickThreads, 0, stream>>>(a, ws + r.flags, rows, slots, head,
+                                                     static_cast<float>(a.scale * a.tau));
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  for (uint64_t p = 0; p < r.pieces; ++p) {
+    const uint64_t first = p * r.piece;
+    const uint64_t most = a.rows - first < r.piece ? a.rows - first : r.piece;
+    const Operand xs = {x, r.lead_x, most};
+    const Operand w_rows = {a.w.p, a.w.stride, a.vocab}, w_cols = {a.w.p, a.w.stride, a.cols};
+    const uint64_t lead_g = 2 * r.lead_z;
+    const uint16_t* g = reinterpret_cast<const uint16_t*>(z);
+    if (a.rows) {
+      loss_rows_kernel<<<waves, 256, 0, stream>>>(a, slots, first, most, x, r.lead_x);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+      const Extents ex = {most, a.vocab, a.cols, 1, &head->count, first, 0};
+      const Logits logits = {z, r.lead_z, a.vocab, 1.0f / a.tau};
+      e = run_product<T, true, true>(plan_of(r.logits, most, a.vocab), xs, w_rows, ex, logits,
+                                     stream);
+      if (e != hipSuccess) return e;
+      const uint32_t grid = static_cast<uint32_t>(most);
+      if (dx || dw)
+        loss_row_kernel<T, true><<<grid, kRowThreads, 0, stream>>>(a, head, rows, first, z,
+                                                                   r.lead_z);
+      else
+        loss_row_kernel<T, false><<<grid, kRowThreads, 0, stream>>>(a, head, rows, first, z,
+                                                                    r.lead_z);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    if (dx && a.rows) {
+      const Operand d = {g, lead_g, most};
+      const Extents ex = {most, a.cols, a.vocab, 1, &head->count, first, 0};
+      Sink s = {};
+      s.out = a.dx.p;
+      s.stride = a.dx.stride;
+      s.dtype = T::kType;
+      s.cols = a.cols;
+      s.rows = rows + first;
+      s.factor = &head->unit;
+      s.lead = r.lead_w;
+      if (r.dx.splits > 1) {
+        s.partial = partial;
+        s.split_size = most * r.lead_w;
+      }
+      e = run_product<T, true, false>(plan_of(r.dx, most, a.cols), d, w_cols, ex, s, stream);
+      if (e != hipSuccess) return e;
+    }
+    if (dw) {
+      const Operand d = {g, lead_g, a.vocab}, xc = {x, r.lead_x, a.cols};
+      const Extents ex = {a.vocab, a.cols, most, 1, a.rows ? &head->count : nullptr, first, 1};
+      Sink s = {};
+      s.out = a.dw;
+      s.stride = a.dw_stride;
+      s.dtype = a.dw_dtype;
+      s.accumulate = a.accumulate;
+      s.cols = a.cols;
+      s.factor = a.rows ? &head->unit : nullptr;
+      s.lead = r.lead_w;
+      if (r.dw.splits > 1) {
+        s.partial = partial;
+        s.split_size = a.vocab * r.lead_w;
+      }
+      s.last = 1;
+      if (r.pieces > 1) {
+        s.sums = reinterpret_cast<float*>(ws + r.sums);
+        s.add = p > 0;
+        s.last = p + 1 == r.pieces;
+      }
+      e = run_product<T, false, false>(r.dw, d, xc, ex, s, stream);
+      if (e != hipSuccess) return e;
+    }
+  }
+  return hipSuccess;
+}
+
+}  // namespace
+
+uint64_t vocab_workspace(uint64_t rows, uint64_t cols, uint64_t vocab, bool dx, bool dw) {
+  return room_of(rows, cols, vocab, dx, dw).bytes;
+}
+
+bool vocab_fits(uint64_t rows, uint64_t cols, uint64_t vocab, bool dx, bool dw) {
+  const Room r = room_of(rows, cols, vocab, dx, dw);
+  return product_fits(r.logits, 0, 0) && (!dx || product_fits(r.dx, r.piece, cols)) &&
+         (!dw || product_fits(r.dw, vocab, cols));
+}
+
+hipError_t launch_vocab_loss(const VocabLaunch& a, hipStream_t stream) {
+  return a.dtype == kF16 ? run_loss<F16>(a, stream) : run_loss<Bf16>(a, stream);
+}
+
+}  // namespace act
+}  // namespace zero

@@ -19,10 +19,12 @@ and "Gradient lifecycle"):
   flat vector (16 Psi / Nd bytes in all).  Each layer's parameters are gathered
   from the rank shards just in time (gather_layer) and released after use.
 
-In backward a rank makes the local gradients that the reduce takes: linear_grad
-and norm_grad write the gradients of a layer's tensors to their flat places in
-the local gradient (stage 1) or in the bucket that is being filled (stages 2 and
-3), from activations kept in 8 bits (checkpoint; the guide's residual states).
+In backward a rank makes the local gradients that the reduce takes: linear_grad,
+norm_grad and gated_grad write the gradients of a layer's tensors to their flat
+places in the local gradient (stage 1) or in the bucket that is being filled
+(stages 2 and 3), from activations kept in 8 bits (checkpoint; the guide's residual
+states); loss_grad and distill_grad begin the backward with the gradient of the
+projection onto the vocabulary.
 
 This module allocates with torch and calls the library; no arithmetic of the
 path happens here.
@@ -33,8 +35,9 @@ from typing import Optional
 
 import torch
 
-from . import (CKPT_INT8, Ckpt, adam_step_shard, block_norm_grad, ckpt_empty, ckpt_weight_grad,
-               gather_params, memory_model, reduce_shard, shard_geometry)
+from . import (ACT_SILU, CKPT_INT8, Ckpt, adam_step_shard, block_norm_grad, ckpt_empty,
+               ckpt_weight_grad, distill_loss, gated_ffn_grad, gather_params, memory_model,
+               reduce_shard, shard_geometry, vocab_loss)
 
 STAGE_OS = 1
 STAGE_OS_G = 2
@@ -174,3 +177,25 @@ class RankState:
         slots = {name: self.grad_slot(lo, first.shape[1], bucket, bucket_offset)
                  for name, lo in places.items()}
         block_norm_grad(dout, dz, ckpt_out, ckpt_block, stats, **slots, **call)
+
+    def gated_grad(self, flat_lo: int, dout, ckpt_gate: Ckpt, ckpt_up: Ckpt, ckpt_x: Ckpt, w,
+                   act: int = ACT_SILU, dx=None, bucket=None, bucket_offset: int = 0,
+                   **call) -> None:
+        """gated_ffn_grad with the gradient of the block's stacked weight (2 dout.shape[1]
+        x ckpt_x.cols, at flat index flat_lo) in the local gradient."""
+        n, k = 2 * dout.shape[1], ckpt_x.cols
+        dw = self.grad_slot(flat_lo, n * k, bucket, bucket_offset).view(n, k)
+        gated_ffn_grad(dout, ckpt_gate, ckpt_up, w, act, dx=dx, ckpt_x=ckpt_x, dw=dw, **call)
+
+    def loss_grad(self, flat_lo: int, x, w, targets, loss, dx=None, bucket=None,
+                  bucket_offset: int = 0, **call) -> None:
+        """vocab_loss with the gradient of the projection onto the vocabulary (w's shape,
+        at flat index flat_lo) in the local gradient."""
+        dw = self.grad_slot(flat_lo, w.numel(), bucket, bucket_offset).view(w.shape)
+        vocab_loss(x, w, targets, loss, dx=dx, dw=dw, **call)
+
+    def distill_grad(self, flat_lo: int, x, w, ids, logits, loss, dx=None, bucket=None,
+                     bucket_offset: int = 0, **call) -> None:
+        """distill_loss, likewise."""
+        dw = self.grad_slot(flat_lo, w.numel(), bucket, bucket_offset).view(w.shape)
+        distill_loss(x, w, ids, logits, loss, dx=dx, dw=dw, **call)
