@@ -593,10 +593,11 @@ typedef struct zero_loss {
   uint64_t workspace_bytes;
 } zero_loss_t;
 
-/* Bytes of workspace of either loss at these sizes; with_dx, with_dw: whether that
- * gradient is wanted (0: sizes that the losses refuse). */
-uint64_t zero_loss_workspace(uint64_t rows, uint64_t cols, uint64_t vocab, int with_dx,
-                             int with_dw);
+/* Bytes of workspace of a loss at these sizes; top: the teacher's entries of a row, 0 for
+ * zero_vocab_loss; with_dx, with_dw: whether that gradient is wanted (0: sizes that the
+ * losses refuse). */
+uint64_t zero_loss_workspace(uint64_t rows, uint64_t cols, uint64_t vocab, uint32_t top,
+                             int with_dx, int with_dw);
 
 /*
  * Softmax cross entropy over the vocabulary, from the last hidden states, with its
@@ -604,9 +605,10 @@ uint64_t zero_loss_workspace(uint64_t rows, uint64_t cols, uint64_t vocab, int w
  *   loss[t] = weights[t] (log(sum over v of exp z[t][v]) - z[t][y]),  y = targets[t]
  *   d[t][v] = weights[t] (softmax(z[t])[v] - (v == y))       (rounded to dtype)
  *   dx = scale d w;  dw = scale d^T x                        (fp32 sums, one rounding)
- * The logits are never kept: the workspace holds those of a piece of the tokens, 4
- * bytes each and 2 GiB at most (or 256 tokens), a copy of their x and, if there are
- * several pieces, fp32 sums of dw.  Before its rounding d
+ * The logits are never kept: for the loss alone they are not stored at all, and for
+ * gradients the workspace holds those of a piece of the tokens, 4 bytes each and about 2
+ * GiB at most (or 256 tokens); besides, a copy of a piece's x and, if there are several
+ * pieces, fp32 sums of dw.  Before its rounding d
  * is divided by the weights' largest power of two and multiplied by 2^14, which fp16's
  * range asks for, and the products multiplied back.
  * A row whose target is negative or whose weight is 0 is left out: its loss and dx are

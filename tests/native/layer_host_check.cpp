@@ -44,7 +44,7 @@ hipError_t launch_gated_ffn(const GatedLaunch& a, hipStream_t) { return keep(g_g
 hipError_t launch_gated_ffn_grad(const GatedGradLaunch& a, hipStream_t) { return keep(g_grad, a); }
 hipError_t launch_vocab_loss(const VocabLaunch& a, hipStream_t) { return keep(g_loss, a); }
 uint64_t gated_grad_workspace(uint64_t, uint64_t, uint64_t) { return 4096; }
-uint64_t vocab_workspace(uint64_t, uint64_t, uint64_t, bool dx, bool dw) {
+uint64_t vocab_workspace(uint64_t, uint64_t, uint64_t, uint32_t, bool dx, bool dw) {
   return 4096 + (dx ? 1024 : 0) + (dw ? 2048 : 0);
 }
 bool gated_fits(uint64_t, uint64_t, uint64_t, bool) { return g_fits; }

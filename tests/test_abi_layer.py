@@ -157,11 +157,15 @@ def test_bad_top_logits(top, want):
 
 
 def test_loss_workspace_and_empty_calls():
-    full, no_dw = Z.loss_workspace(8192, 4096, 131072), Z.loss_workspace(8192, 4096, 131072, True,
-                                                                        False)
+    full = Z.loss_workspace(8192, 4096, 131072)
+    no_dw = Z.loss_workspace(8192, 4096, 131072, 0, True, False)
     # the logits and x of a piece, and the running sums of dw, however many tokens
     assert 2 ** 31 < no_dw < 2 ** 31 + 2 ** 28 and full - no_dw >= 131072 * 4096 * 4
-    assert Z.loss_workspace(1 << 20, 4096, 131072, True, False) < no_dw + 2 ** 24
+    assert Z.loss_workspace(1 << 20, 4096, 131072, 0, True, False) < no_dw + 2 ** 24
+    # cross entropy alone stores no logits
+    assert Z.loss_workspace(8192, 4096, 131072, 0, False, False) < 2 ** 28
+    assert Z.loss_workspace(8192, 4096, 131072, 64, False, False) > 2 ** 31
+    assert Z.loss_workspace(8192, 4096, 131072, 1025) == 0
     for bad in ((1 << 26, 70, 1000), (4, 0, 1000), (4, 70, 0), (4, 70, 1 << 25)):
         assert Z.loss_workspace(*bad) == 0
     nothing = dict(rows=0, x=None, w=None, dx=None, loss=None, workspace=None)

@@ -258,7 +258,7 @@ def _load() -> ctypes.CDLL:
     lib.zero_gated_ffn_grad_workspace.restype = u64
     lib.zero_gated_ffn_grad.argtypes = [ctypes.POINTER(_GatedFfnGradArg), vp]
     lib.zero_gated_ffn_grad.restype = ci
-    lib.zero_loss_workspace.argtypes = [u64, u64, u64, ci, ci]
+    lib.zero_loss_workspace.argtypes = [u64, u64, u64, u32, ci, ci]
     lib.zero_loss_workspace.restype = u64
     lib.zero_vocab_loss.argtypes = [ctypes.POINTER(_LossArg), vp, ci, vp]
     lib.zero_vocab_loss.restype = ci
@@ -865,13 +865,13 @@ def gated_ffn_grad(dout, ckpt_gate: Ckpt, ckpt_up: Ckpt, w, act: int = ACT_SILU,
 _IDS = {torch.int32: 4, torch.int64: 8}
 
 
-def loss_workspace(rows: int, cols: int, vocab: int, with_dx: bool = True,
+def loss_workspace(rows: int, cols: int, vocab: int, top: int = 0, with_dx: bool = True,
                    with_dw: bool = True) -> int:
-    """Bytes of workspace of vocab_loss and distill_loss at these sizes."""
-    return lib.zero_loss_workspace(rows, cols, vocab, int(bool(with_dx)), int(bool(with_dw)))
+    """Bytes of workspace of vocab_loss (top 0) or distill_loss at these sizes."""
+    return lib.zero_loss_workspace(rows, cols, vocab, top, int(bool(with_dx)), int(bool(with_dw)))
 
 
-def _loss_arg(x, w, loss, weights, scale, dx, dw, accumulate, workspace, stream, tensors):
+def _loss_arg(x, w, loss, weights, scale, dx, dw, accumulate, workspace, stream, tensors, top=0):
     """(argument, device index, workspace tensor) of a loss; tensors: its other ones."""
     p_x, s_x = _matrix(x, "x", _F16_BF16)
     (rows, cols), own = x.shape, (x.dtype,)
@@ -889,7 +889,7 @@ def _loss_arg(x, w, loss, weights, scale, dx, dw, accumulate, workspace, stream,
     p_dw, s_dw = _optional(dw, "dw", own + (torch.float32,), (vocab, cols), tensors)
     dev = _index(tensors, stream)
     ws, ws_bytes, held = _workspace(
-        workspace, lib.zero_loss_workspace(rows, cols, vocab, dx is not None, dw is not None),
+        workspace, lib.zero_loss_workspace(rows, cols, vocab, top, dx is not None, dw is not None),
         dev, stream)
     a = _LossArg(_CODE[x.dtype], rows, cols, vocab, p_x, s_x, p_w, s_w, p_weights, p_loss, scale,
                  p_dx, s_dx, p_dw, s_dw, _CODE[x.dtype if dw is None else dw.dtype],
@@ -936,7 +936,7 @@ def distill_loss(x, w, ids, logits, loss, temperature: float = 1.0, weights=None
         raise ValueError(f"ids has {shape[0]} rows, x {x.shape[0]}")
     p_top, s_top = _matrix(logits, "logits", _FLOATS, shape)
     a, dev, held = _loss_arg(x, w, loss, weights, scale, dx, dw, accumulate, workspace, stream,
-                             [ids, logits])
+                             [ids, logits], shape[1])
     t = _TopLogitsArg(shape[1], p_ids, s_ids, _IDS[ids.dtype], p_top, s_top, _CODE[logits.dtype],
                       temperature)
     _call(dev, stream, lib.zero_distill_loss, ctypes.byref(a), ctypes.byref(t))

@@ -62,7 +62,8 @@ struct VocabLaunch {
   uint8_t* workspace;           // vocab_workspace bytes
 };
 
-uint64_t vocab_workspace(uint64_t rows, uint64_t cols, uint64_t vocab, bool dx, bool dw);
+uint64_t vocab_workspace(uint64_t rows, uint64_t cols, uint64_t vocab, uint32_t top, bool dx,
+                         bool dw);
 bool vocab_fits(uint64_t rows, uint64_t cols, uint64_t vocab, bool dx, bool dw);
 hipError_t launch_vocab_loss(const VocabLaunch& a, hipStream_t stream);
 

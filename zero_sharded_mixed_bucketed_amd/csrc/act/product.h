@@ -40,6 +40,7 @@ constexpr int kMulDepth = 64;     // k of a turn
 struct Operand {
   const uint16_t* p;
   uint64_t stride, extent;
+  bool padded;   // its fast axis is followed by zeros up to a whole chunk
 };
 
 // The sizes of a product.  A count in device memory, where there is one, says how
@@ -202,12 +203,94 @@ __device__ __forceinline__ Spot spot_of(uint32_t wg, uint32_t wgs, uint32_t tile
   return {split, row0 + rest % rows, rest / rows};
 }
 
-// WM x WN waves.  An epilogue E holds what it writes and
-//   put<T>(split, m, n, rows, x):  eight neighbouring sums x of row m, from column n on
-//     (a multiple of eight; rows from `rows` on and columns past the edge among them),
-//     or, with E::kPairs, put<T>(split, m, n, rows, x, y) of the same columns of both
-//     stacked matrices.
-// All lanes of a wave call it together.
+// A wave's sums, FM x FN fragments from row m0 and column n0 on, to an epilogue.  b's
+// fragment is the matrix instructions' first operand, so the sums' rows are the lanes'
+// (l % 32), and a lane has four neighbouring columns of a row at a time.  Through shared
+// memory (`piece`, 32 rows of 64 columns), it gets eight; the 16-byte pieces are permuted
+// by row, so that sixteen neighbouring rows of one lie in different banks.
+//
+// An epilogue E holds what it writes.  put<T>(split, m, n, rows, x) takes eight
+// neighbouring sums x of row m, from column n on (a multiple of eight; rows from `rows`
+// on and columns past the edge among them); with E::kPairs, put<T>(split, m, n, rows, x,
+// y) those of the same columns of both stacked matrices.  All lanes of a wave call it
+// together.  With E::kRows, columns(row, x, m, n, rows) sees each lane's sums x of row m
+// first, half of the columns at a time, the others in lane ^ 32, with a Row of its own to
+// keep, which finish(row, m, piece, rows) gets in the end, `piece` being which of the
+// row's 32 FN columns these were.  stores() says whether there is anything to store.
+// simple() says whether a whole
+// tile needs none of put's checks: now(split, m0, factor) then gives what stores it,
+// factor what load_factor() gave at the kernel's begin; row_of(i, line, m) is the row at
+// which it stores row m, line `line` of the wave's i-th 32.
+template <typename T, bool UNROLL, int FM, int FN, typename E, typename P>
+__device__ __forceinline__ void wave_store(const f32x16 (&acc)[FM][FN], float* piece, const E& e,
+                                           const P& to, uint32_t split, uint64_t m0, uint64_t n0,
+                                           uint64_t m_all) {
+  constexpr int kWide = !E::kPairs && FN > 1 ? 2 : 1;       // fragments of c beside each other
+  constexpr uint32_t kLanes = kWide * 4, kLines = 64 / kLanes, kPass = 32 / kLines;
+  constexpr int kUnroll = UNROLL ? kPass : 1;
+  constexpr int kTurns = E::kPairs ? FN / 2 : FN / kWide;
+  constexpr int kHeld = E::kPairs ? 2 : kWide;              // fragments a turn
+  const uint32_t lane = threadIdx.x % 64, c = lane % kLanes;
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    [[maybe_unused]] typename E::Row row;
+#pragma unroll
+    for (int h = 0; h < kTurns; ++h) {
+#pragma unroll
+      for (int j = 0; j < kHeld; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const f32x16& v = acc[i][E::kPairs ? h + kTurns * j : kWide * h + j];
+          const uint32_t line = lane % 32, q = j * 8 + r * 2 + lane / 32;
+          *reinterpret_cast<f32x4*>(piece + line * 64 + ((q ^ (line % 16)) * 4)) =
+              f32x4{v[4 * r], v[4 * r + 1], v[4 * r + 2], v[4 * r + 3]};
+        }
+      wave_fence();
+      if constexpr (E::kRows) {
+        constexpr int kHalf = kWide * kMulFrag / 2;
+        float x[kHalf];
+#pragma unroll
+        for (int t = 0; t < kHalf / 4; ++t) {
+          const uint32_t line = lane % 32, q = lane / 32 * (kHalf / 4) + t;
+          const f32x4 v = *reinterpret_cast<const f32x4*>(piece + line * 64 +
+                                                          ((q ^ (line % 16)) * 4));
+#pragma unroll
+          for (int d = 0; d < 4; ++d) x[4 * t + d] = v[d];
+        }
+        e.columns(row, x, m0 + i * kMulFrag + lane % 32,
+                  n0 + h * (kWide * kMulFrag) + lane / 32 * kHalf, m_all);
+        if (h + 1 == kTurns)
+          e.finish(row, m0 + i * kMulFrag + lane % 32, n0 / (FN * kMulFrag), m_all);
+      }
+      if (!e.stores()) {
+        wave_fence();
+        continue;
+      }
+#pragma unroll kUnroll
+      for (uint32_t r = 0; r < kPass; ++r) {
+        const uint32_t line = r * kLines + lane / kLanes;
+        const uint64_t m = to.row_of(i, line, m0 + i * kMulFrag + line);
+        const uint64_t n = n0 + h * (kWide * kMulFrag) + c * kChunk;
+        const float* p = piece + line * 64;
+        const uint32_t turn = line % 16;
+        const f32x4 u = *reinterpret_cast<const f32x4*>(p + ((2 * c) ^ turn) * 4);
+        const f32x4 v = *reinterpret_cast<const f32x4*>(p + ((2 * c + 1) ^ turn) * 4);
+        float y[8] = {u[0], u[1], u[2], u[3], v[0], v[1], v[2], v[3]};
+        if constexpr (E::kPairs) {
+          const f32x4 u2 = *reinterpret_cast<const f32x4*>(p + ((8 + 2 * c) ^ turn) * 4);
+          const f32x4 v2 = *reinterpret_cast<const f32x4*>(p + ((9 + 2 * c) ^ turn) * 4);
+          float y2[8] = {u2[0], u2[1], u2[2], u2[3], v2[0], v2[1], v2[2], v2[3]};
+          to.template put<T>(split, m, n, m_all, y, y2);
+        } else {
+          to.template put<T>(split, m, n, m_all, y);
+        }
+      }
+      wave_fence();                                           // before the next turn's writes
+    }
+  }
+}
+
+// Operands of any alignment, WM x WN waves.
 template <typename T, bool AF, bool BF, int TM, int TN, int WM, int WN, typename E>
 __global__ __launch_bounds__(kMulThreads) void product_kernel(Operand a, Operand b, Extents x,
                                                               uint64_t safe, E epilogue) {
@@ -216,9 +299,9 @@ __global__ __launch_bounds__(kMulThreads) void product_kernel(Operand a, Operand
   typedef Side<BF, TN, E::kPairs ? TN / WN / 2 : 0> B;
   constexpr int kFm = TM / WM / kMulFrag, kFn = TN / WN / kMulFrag;
   constexpr int kSub = kMulDepth / kMulStep, kMul = kFm * kFn;
-  constexpr uint32_t kCols = TN / WN, kPitch = kCols + 8;
+  constexpr uint32_t kCols = TN / WN, kPiece = kMulFrag * 64;
   constexpr uint32_t kTiles = A::kElems + B::kElems;        // 32-bit words of two buffers
-  constexpr uint32_t kOut = 4 * kMulFrag * kPitch;
+  constexpr uint32_t kOut = 4 * kPiece;
   __shared__ __attribute__((aligned(16))) float lds[kTiles > kOut ? kTiles : kOut];
   uint16_t* la = reinterpret_cast<uint16_t*>(lds);
   uint16_t* lb = la + 2 * A::kElems;
@@ -325,7 +408,7 @@ __global__ __launch_bounds__(kMulThreads) void product_kernel(Operand a, Operand
 #pragma unroll
       for (int w = 0; w < kMul; ++w) {
         const int i = w / kFn, j = w % kFn;
-        acc[i][j] = mul<T>(fa[s & 1][i], fb[s & 1][j], acc[i][j]);
+        acc[i][j] = mul<T>(fb[s & 1][j], fa[s & 1][i], acc[i][j]);
 #pragma unroll
         for (int d = 0; d < kReadsEach; ++d) {
           const int q = w * kReads / kMul + d;
@@ -354,53 +437,348 @@ __global__ __launch_bounds__(kMulThreads) void product_kernel(Operand a, Operand
   }
   __syncthreads();
 
-  // Through shared memory, so that a lane has eight neighbouring columns: each wave
-  // turns 32 rows at a time in a piece of its own, whose rows lie kPitch words apart
-  // (4 kPitch = 32 mod 64: the two halves of a wave, four rows apart, meet different
-  // banks).
-  const uint32_t lane = tid % 64;
-  static_assert((4 * kPitch) % 64 == 32, "");
-  float* piece = lds + wave * kMulFrag * kPitch;
+  wave_store<T, false>(acc, lds + wave * kPiece, epilogue, epilogue, at.split, m0 + wm,
+                       n0 + (E::kPairs ? wn / 2 : wn), m_all);
+}
+
+// ------------------------------------------------------------ whole chunks
+
+// The same product where every 16-byte chunk of both operands is whole and aligned
+// (ring_takes): 256 x 256 tiles and stages of 64 k that go from memory straight to
+// shared memory, one under way while the other is worked on, and workgroups that stay
+// for several tiles, so that the next tile's first stage is read while this one's sums
+// are stored.  Without registers between, a stage's loads are issued with little else,
+// right behind the barrier that frees its place.
+//
+// Loads past an operand's end are out of their descriptor's range: they give 0 and
+// touch no memory.  Places in shared memory are those of Side.  A wave's load is 1 KiB
+// of a stage: eight rows of 64 k (k fast) or two of 256 columns (k slow); in either case
+// whole 128-byte lines, which the caches hand out twice as fast as halves (stages of 32
+// k, four of them, took 1266 where this takes 1391 TFLOP/s with k fast in both operands,
+// 4096 x 4096 over 65536).
+constexpr int kRingTile = 256;
+constexpr uint32_t kRingSide = kRingTile * kMulDepth * 2;    // bytes of an operand's stage
+constexpr uint32_t kRingStage = 2 * kRingSide;
+constexpr int kRingLoads = 8;                                // of a thread, an operand's stage
+constexpr uint32_t kRingOut = 8192;                          // of a wave: 32 rows of 64 sums
+constexpr uint32_t kRingWgs = 256;                           // one a compute unit
+
+// One operand's loads, PAIR as Side's.
+template <bool FAST, int PAIR = 0>
+struct RingSide {
+  static constexpr int kReads = FAST ? 1 : 2;                // shared loads a fragment
+  static constexpr uint32_t kNone = 0x80000000u, kAll = 0x7FFFFFF0u;
+  static constexpr uint32_t kLanes = FAST ? kMulDepth / kChunk : kRingTile / kChunk;
+  static constexpr uint32_t kRows = 64 / kLanes;             // of memory, a wave's load
+  u32x4 srd;                  // the descriptor of the stage to load next
+  uint64_t stride;            // bytes
+  uint32_t off[kRingLoads];   // of this lane's chunk in each of its loads, or kNone
+
+  // The chunk of a row that this lane loads, by the place it has in shared memory.
+  static __device__ __forceinline__ uint32_t chunk_of(uint32_t wave) {
+    const uint32_t lane = threadIdx.x % 64;
+    if constexpr (FAST) return lane % 8 ^ (wave % 2 * 4 + lane / 16);
+    return ((lane % 32 / 4) ^ ((wave * 2 + lane / 32) & 3)) * 4 + lane % 4;
+  }
+
+  __device__ __forceinline__ void go_to(uint64_t base) {
+    srd[0] = static_cast<uint32_t>(base);
+    srd[1] = static_cast<uint32_t>(base >> 32);              // addresses have 48 bits
+  }
+
+  __device__ __forceinline__ void begin(const Operand& o, uint64_t first, uint64_t k,
+                                        uint32_t wave) {
+    stride = o.stride * 2;
+    srd[2] = kAll;
+    srd[3] = 0x00027000u;
+    const uint64_t p = reinterpret_cast<uint64_t>(o.p);
+    go_to(FAST ? p + first * stride + k * 2 : p + k * stride);
+    const uint32_t chunk = chunk_of(wave);
 #pragma unroll
-  for (int i = 0; i < kFm; ++i) {
-#pragma unroll
-    for (int j = 0; j < kFn; ++j)
-#pragma unroll
-      for (int r = 0; r < 16; ++r)
-        piece[(r / 4 * 8 + lane / 32 * 4 + r % 4) * kPitch + j * kMulFrag + lane % 32] =
-            acc[i][j][r];
-    wave_fence();
-    constexpr uint32_t kWide = E::kPairs ? kCols / 2 : kCols;  // columns of c a wave
-    constexpr uint32_t kLanes = kWide / kChunk;             // lanes of a row
-    constexpr int kRows = kMulFrag * kLanes / 64;           // passes over the 32 rows
-    const uint32_t q = lane / kLanes, c = lane % kLanes * kChunk;
-#pragma unroll 2
-    for (int r = 0; r < kRows; ++r) {
-      const uint32_t line = q + r * (64 / kLanes);
-      const float* p = piece + line * kPitch + c;
-      const uint64_t m = m0 + wm + i * kMulFrag + line;
-      const uint64_t n = n0 + (E::kPairs ? wn / 2 : wn) + c;
-      const f32x4 u = *reinterpret_cast<const f32x4*>(p);
-      const f32x4 v = *reinterpret_cast<const f32x4*>(p + 4);
-      float s[8] = {u[0], u[1], u[2], u[3], v[0], v[1], v[2], v[3]};
-      if constexpr (E::kPairs) {
-        const f32x4 u2 = *reinterpret_cast<const f32x4*>(p + kWide);
-        const f32x4 v2 = *reinterpret_cast<const f32x4*>(p + kWide + 4);
-        float s2[8] = {u2[0], u2[1], u2[2], u2[3], v2[0], v2[1], v2[2], v2[3]};
-        epilogue.template put<T>(at.split, m, n, m_all, s, s2);
+    for (int i = 0; i < kRingLoads; ++i) {
+      const uint32_t r = (i * 4 + wave) * kRows + threadIdx.x % 64 / kLanes;
+      if constexpr (!FAST) {
+        const uint64_t c = first + chunk * kChunk;
+        off[i] = c < o.extent ? static_cast<uint32_t>(r * stride + c * 2) : kNone;
+      } else if constexpr (PAIR != 0) {
+        const uint32_t c = r / (2 * PAIR) * PAIR + r % PAIR;
+        const uint64_t row = c + (r / PAIR % 2 ? o.extent : 0);
+        off[i] = first + c < o.extent ? static_cast<uint32_t>(row * stride) + chunk * 16 : kNone;
       } else {
-        epilogue.template put<T>(at.split, m, n, m_all, s);
+        off[i] = first + r < o.extent ? static_cast<uint32_t>(r * stride) + chunk * 16 : kNone;
       }
     }
-    wave_fence();
   }
+
+  // The stage to load next has `left` < 64 k: the rest is out of range.
+  __device__ __forceinline__ void cut(uint32_t left, uint32_t wave) {
+    if constexpr (FAST) {
+      const bool in = chunk_of(wave) * kChunk < left;
+#pragma unroll
+      for (int i = 0; i < kRingLoads; ++i) off[i] = in ? off[i] : kNone;
+    } else {
+      srd[2] = static_cast<uint32_t>(left * stride);
+    }
+  }
+
+  // One load, to shared memory from `to` + TO on (a scalar).  It writes no register; the
+  // loop's own waits are what orders it.
+  template <int TO>
+  __device__ __forceinline__ void load(uint32_t to, uint32_t from) const {
+    asm volatile("s_add_u32 m0, %0, %3\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :
+                 : "s"(to), "v"(from), "s"(srd), "i"(TO)
+                 : "memory", "scc", "m0");
+  }
+
+  __device__ __forceinline__ void next() {
+    go_to((static_cast<uint64_t>(srd[1]) << 32 | srd[0]) +
+          (FAST ? kMulDepth * 2 : kMulDepth * stride));
+  }
+
+  // This lane's place, in bytes from an operand's stage on, of part q of the fragment at
+  // rows [at, at + 32) and 16 k from step * 16 on.
+  static __device__ __forceinline__ uint32_t place(int step, uint32_t at, int q) {
+    const uint32_t lane = threadIdx.x % 64;
+    if constexpr (FAST) {
+      // chunks 2 step and 2 step + 1, before their permutation
+      const uint32_t r = at + lane % 32;
+      return ((r * kMulDepth + ((lane / 32) ^ (r / 2 % 8)) * kChunk) * 2) ^ (step * 32);
+    } else {
+      const uint32_t r = step * kMulStep + (lane / 32) * 8 + (lane % 16) / 4 + q * 4;
+      const uint32_t c = at + (lane / 16 % 2) * 16 + lane % 4 * 4;
+      return (r * kRingTile + ((((c >> 5) ^ (r & 3)) << 5) | (c & 31))) * 2;
+    }
+  }
+
+  static __device__ __forceinline__ void read(uint32_t at, int q, u32x4& to) {
+    typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
+    typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+    if constexpr (FAST) {
+      to = *reinterpret_cast<lds_u32x4*>(at);
+    } else {
+      const u32x2 v = __builtin_bit_cast(
+          u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_s16x4*>(at)));
+      to[2 * q] = v[0];
+      to[2 * q + 1] = v[1];
+    }
+  }
+};
+
+// Load `which` of a stage's 16: a's eight, then b's.
+template <int I, typename A, typename B>
+__device__ __forceinline__ void ring_load(const A& a, const B& b, uint32_t to, int which) {
+  if (which == I) {
+    if constexpr (I < kRingLoads)
+      a.template load<I * 4096>(to, a.off[I]);
+    else
+      b.template load<I * 4096>(to, b.off[I - kRingLoads]);
+  } else if constexpr (I + 1 < 2 * kRingLoads) {
+    ring_load<I + 1>(a, b, to, which);
+  }
+}
+
+template <typename T, bool AF, bool BF, typename E>
+__global__ __launch_bounds__(kMulThreads, 1) void ring_kernel(Operand a, Operand b, Extents x,
+                                                              E epilogue) {
+  typedef RingSide<AF> A;
+  typedef RingSide<BF, E::kPairs ? 64 : 0> B;
+  constexpr int kF = 4, kMul = kF * kF, kReads = kF * (A::kReads + B::kReads);
+  constexpr int kSteps = kMulDepth / kMulStep;
+  static_assert(kRingSide == kRingLoads * 4096, "a workgroup's load is 4 KiB");
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kRingStage + 4 * kRingOut];
+  const uint32_t lds0 = static_cast<uint32_t>(
+      reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)lds));
+
+  const float by = epilogue.load_factor();
+  uint64_t m_all = x.m, k_all = x.k;
+  if (x.count) {
+    const uint64_t c = *x.count;
+    const uint64_t left = c > x.first ? c - x.first : 0;
+    uint64_t& of = x.count_k ? k_all : m_all;
+    of = left < of ? left : of;
+  }
+  constexpr int kOutN = E::kPairs ? kRingTile / 2 : kRingTile;
+  const uint32_t tiles_m = static_cast<uint32_t>((m_all + kRingTile - 1) / kRingTile);
+  const uint32_t tiles_n = static_cast<uint32_t>((x.n + kOutN - 1) / kOutN);
+  const uint32_t wgs = tiles_m * tiles_n * x.splits;
+  if (blockIdx.x >= wgs) return;
+  const uint64_t per = ((k_all + x.splits - 1) / x.splits + kMulDepth - 1) / kMulDepth * kMulDepth;
+  const uint32_t lane = threadIdx.x % 64;
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const uint32_t wm = wave / 2 * 128, wn = wave % 2 * 128;
+
+  // The loads' side: which tile it is at, the k left of it, and where a stage goes.
+  A sa;
+  B sb;
+  uint32_t id = blockIdx.x;
+  int64_t left = 0, rest = 0;
+  uint64_t load_m = 0, load_n = 0, load_k = 0;
+  const uint32_t fill0 = lds0 + wave * 1024;
+  uint32_t fill = fill0;
+  const auto enter = [&]() __attribute__((always_inline)) {
+    const Spot at = spot_of(id, wgs, tiles_m, tiles_n);
+    const uint64_t lo = at.split * per < k_all ? at.split * per : k_all;
+    const uint64_t hi = lo + per < k_all ? lo + per : k_all;
+    // Neighbouring tiles begin up to seven stages further on and end with what they
+    // left out: rows whose stride is a power of two begin in the same channels of the
+    // caches, which all tiles would ask together (4096 x 131072 over 4096: 1264 -> 1335
+    // TFLOP/s with k fast, 1279 -> 1287 with k slow).
+    const uint32_t stages = static_cast<uint32_t>((hi - lo + kMulDepth - 1) / kMulDepth);
+    rest = stages ? static_cast<int64_t>((at.m + at.n) % 8 % stages) * kMulDepth : 0;
+    left = static_cast<int64_t>(hi - lo) - rest;
+    load_m = static_cast<uint64_t>(at.m) * kRingTile;
+    load_n = static_cast<uint64_t>(at.n) * kOutN;
+    load_k = lo;
+    sa.begin(a, load_m, lo + rest, wave);
+    sb.begin(b, load_n, lo + rest, wave);
+  };
+  // The stage to load next is the range's last, or past it: on to the part that was left
+  // out, to the next tile, or to nothing.
+  const auto turn = [&]() __attribute__((always_inline)) {
+    while (left <= 0 && id < wgs) {
+      if (rest > 0) {
+        left = rest;
+        rest = 0;
+        sa.begin(a, load_m, load_k, wave);
+        sb.begin(b, load_n, load_k, wave);
+      } else {
+        id += gridDim.x;
+        if (id < wgs) enter();
+      }
+    }
+    if (left < kMulDepth) {
+      const uint32_t some = left > 0 ? static_cast<uint32_t>(left) : 0;
+      sa.cut(some, wave);
+      sb.cut(some, wave);
+    }
+  };
+  const auto stage_done = [&]() __attribute__((always_inline)) {
+    fill = fill == fill0 ? fill0 + kRingStage : fill0;
+    sa.next();
+    sb.next();
+    left -= kMulDepth;
+    if (left < kMulDepth) turn();
+  };
+
+  // Fragments of a step in the order of their use: a0, b0 .. b3, a1 .. a3.
+  u32x4 fa[2][kF], fb[2][kF];
+  f32x16 acc[kF][kF];
+  uint32_t ring = lds0;     // the stage that is worked on
+  const uint32_t pa = A::place(0, wm, 0), pb = B::place(0, wn, 0);
+  const auto read = [&](uint32_t stage, int s, int to, int q) __attribute__((always_inline)) {
+    constexpr uint32_t kNext = kMulFrag * kMulDepth * 2;   // bytes to a next fragment, k fast
+    const bool of_b = q >= A::kReads && q < A::kReads + kF * B::kReads;
+    if (of_b) {
+      const int i = (q - A::kReads) / B::kReads, h = (q - A::kReads) % B::kReads;
+      const uint32_t at = BF ? (pb ^ s * 32) + i * kNext : B::place(s, wn + i * kMulFrag, h);
+      B::read(stage + kRingSide + at, h, fb[to][i]);
+    } else {
+      const int w = q < A::kReads ? q : q - kF * B::kReads, i = w / A::kReads, h = w % A::kReads;
+      const uint32_t at = AF ? (pa ^ s * 32) + i * kNext : A::place(s, wm + i * kMulFrag, h);
+      A::read(stage + at, h, fa[to][i]);
+    }
+  };
+
+  enter();
+  turn();
+  // The first kFirst loads of a stage go between the matrix instructions of the step
+  // behind the barrier, the others evenly into the two steps after it, so that the last
+  // has a step left to arrive (8, 12 and 16 first: 1302, 1391 and 1318 TFLOP/s).
+  constexpr int kLoads = 2 * kRingLoads, kFirst = 12;
+  constexpr int kRest = (kLoads - kFirst + kSteps - 2) / (kSteps - 1);
+#pragma unroll
+  for (int q = 0; q < kLoads; ++q) ring_load<0>(sa, sb, fill, q);
+  stage_done();
+#pragma unroll
+  for (int q = 0; q < kFirst; ++q) ring_load<0>(sa, sb, fill, q);
+  asm volatile("s_waitcnt vmcnt(%0)" ::"i"(kFirst) : "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+#pragma unroll
+  for (int q = 0; q < kReads; ++q) read(ring, 0, 0, q);
+
+#pragma unroll 1
+  for (uint32_t tile = blockIdx.x; tile < wgs; tile += gridDim.x) {
+    const Spot at = spot_of(tile, wgs, tiles_m, tiles_n);
+    const uint64_t lo = at.split * per < k_all ? at.split * per : k_all;
+    const uint64_t hi = lo + per < k_all ? lo + per : k_all;
+    const uint32_t stages = static_cast<uint32_t>((hi - lo + kMulDepth - 1) / kMulDepth);
+#pragma unroll
+    for (int i = 0; i < kF; ++i)
+#pragma unroll
+      for (int j = 0; j < kF; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+    constexpr int kOver = kMul - 3;       // a step's reads end three instructions early
+#pragma unroll 1
+    for (uint32_t s = 0; s < stages; ++s) {
+      const uint32_t then = ring == lds0 ? lds0 + kRingStage : lds0;
+      // step p beside the reads of step p + 1; the last one's are the next stage's
+#pragma unroll
+      for (int p = 0; p < kSteps; ++p) {
+        const bool last = p + 1 == kSteps;
+        const int l0 = last ? 0 : kFirst + p * kRest;
+        const int l1 = last ? kFirst : l0 + kRest < kLoads ? l0 + kRest : kLoads;
+        if (last) {
+          stage_done();
+          // this wave has read all of this stage, and its loads of the next one are
+          // there: so have and are, behind the barrier, all waves'
+          asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+          __builtin_amdgcn_s_barrier();
+          asm volatile("" ::: "memory");
+        }
+#pragma unroll
+        for (int w = 0; w < kMul; ++w) {
+          acc[w / kF][w % kF] = mul<T>(fb[p & 1][w % kF], fa[p & 1][w / kF], acc[w / kF][w % kF]);
+#pragma unroll
+          for (int d = 0; d < (kReads + kOver - 1) / kOver; ++d) {
+            const int q = w * kReads / kOver + d;
+            if (q < (w + 1) * kReads / kOver && q < kReads)
+              read(last ? then : ring, last ? 0 : p + 1, (p + 1) & 1, q);
+          }
+          const int n = l1 - l0;
+          if (n > 0 && (w + 1) * n / kMul > w * n / kMul)
+            ring_load<0>(sa, sb, fill, l0 + w * n / kMul);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+      ring = then;
+    }
+
+    const uint64_t m0 = static_cast<uint64_t>(at.m) * kRingTile + wm;
+    const uint64_t n0 = static_cast<uint64_t>(at.n) * kOutN + (E::kPairs ? wn / 2 : wn);
+    float* piece = reinterpret_cast<float*>(lds + 2 * kRingStage + wave * kRingOut);
+    const bool whole = static_cast<uint64_t>(at.m + 1) * kRingTile <= m_all &&
+                       static_cast<uint64_t>(at.n + 1) * kOutN <= x.n;
+    if (whole && epilogue.simple())
+      wave_store<T, !E::kPairs>(acc, piece, epilogue, epilogue.now(at.split, m0, by), at.split,
+                                m0, n0, m_all);
+    else
+      wave_store<T, false>(acc, piece, epilogue, epilogue, at.split, m0, n0, m_all);
+    // vmcnt(0), seen by the compiler: it would wait for the epilogue's loads in every
+    // turn of the next tile otherwise, and with them for the stage under way
+    if (!(whole && epilogue.simple())) __builtin_amdgcn_s_waitcnt(0x0F70);
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // nothing lands in shared memory later
+}
+
+// Whether the ring takes an operand: whole, aligned chunks, and a tile's (k fast) or a
+// stage's (k slow) offsets within 31 bits.
+inline bool ring_takes(const Operand& o, bool fast, uint64_t k, bool pairs = false) {
+  constexpr uint64_t kFar = 1ull << 30;
+  if (reinterpret_cast<uintptr_t>(o.p) % 16 || o.stride % kChunk) return false;
+  if (o.stride >= kFar / 512) return false;
+  if (!o.padded && (fast ? k : o.extent) % kChunk) return false;
+  return fast ? ((pairs ? o.extent : 0) + 256) * o.stride < kFar
+              : o.stride * kMulDepth + o.extent < kFar;
 }
 
 // Where sums go: partial sums of splits (fp32, `lead` apart, joined afterwards by
 // join_kernel), running sums over several products, or the result itself, scaled and
 // rounded once.
 struct Sink {
-  static constexpr bool kPairs = false, kJoins = true;
+  static constexpr bool kPairs = false, kRows = false, kJoins = true;
   void* out;
   uint64_t stride;
   int dtype, accumulate;   // kF16, kBf16 or kF32
@@ -463,6 +841,65 @@ struct Sink {
       for (int i = 0; i < 8; ++i) x[i] += old[i];
     }
     store8<false>(o, n, cols, pack8<T>(x));
+  }
+
+  struct Row {};
+
+  __device__ __forceinline__ bool stores() const { return true; }
+  __device__ __forceinline__ uint64_t row_of(int, uint32_t, uint64_t m) const { return m; }
+
+  // Whole tiles: partial or running sums that are stored, or a 16-bit result that is.
+  __device__ __forceinline__ bool simple() const {
+    return partial || (sums ? !add && !last : dtype != kF32 && !accumulate);
+  }
+
+  struct Now {
+    float* to;              // sums' place, or nullptr
+    uint64_t lead;
+    uint16_t* out;
+    uint64_t stride;
+    float factor;
+    bool mapped;
+    uint32_t rows[4];       // mapped: the rows of lane % 32 in each 32 of the wave's
+
+    __device__ __forceinline__ uint64_t row_of(int i, uint32_t line, uint64_t m) const {
+      if (!mapped) return m;
+      return static_cast<uint32_t>(__builtin_amdgcn_ds_bpermute(static_cast<int>(line * 4),
+                                                                static_cast<int>(rows[i])));
+    }
+
+    template <typename T>
+    __device__ __forceinline__ void put(uint32_t, uint64_t m, uint64_t n, uint64_t,
+                                        float (&x)[8]) const {
+      if (to) {
+        f32x4* p = reinterpret_cast<f32x4*>(to + m * lead + n);
+        p[0] = f32x4{x[0], x[1], x[2], x[3]};
+        p[1] = f32x4{x[4], x[5], x[6], x[7]};
+        return;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] *= factor;
+      *reinterpret_cast<u32x4_at2*>(out + m * stride + n) = pack8<T>(x);
+    }
+  };
+
+  // In a scalar register, so that no load is under way when the products begin.
+  __device__ __forceinline__ float load_factor() const {
+    return factor ? __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(
+                                                  __builtin_bit_cast(int, *factor)))
+                  : 1.0f;
+  }
+
+  __device__ __forceinline__ Now now(uint32_t split, uint64_t m0, float by) const {
+    Now n = {partial ? partial + split * split_size : sums, lead, static_cast<uint16_t*>(out),
+             stride, by, rows && !partial && !sums, {0, 0, 0, 0}};
+    if (n.mapped) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) n.rows[i] = rows[m0 + i * 32 + threadIdx.x % 32];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) forget(n.rows[i]);
+    }
+    return n;
   }
 
   template <typename T>
@@ -552,6 +989,14 @@ inline MulPlan plan_of(MulPlan p, uint64_t m, uint64_t n) {
 
 inline uint64_t chunks_up(uint64_t n, uint64_t to) { return (n + to - 1) / to * to; }
 
+// Elements between 16-bit rows of a workspace: whole 128-byte lines, and not a multiple of
+// 4 KiB, whose rows begin in the same channels of the caches (4096 x 4096 over 131072, k
+// fast in a: 1311 -> 1395 TFLOP/s).
+inline uint64_t row_lead(uint64_t n) {
+  const uint64_t lead = chunks_up(n, 64);
+  return lead % 2048 ? lead : lead + 64;
+}
+
 // Whether a product, and the join of its splits, is one launch each.
 inline bool product_fits(const MulPlan& p, uint64_t m, uint64_t n) {
   constexpr uint64_t kMost = most_workgroups(kMulThreads);
@@ -570,7 +1015,10 @@ hipError_t run_product(const MulPlan& p, const Operand& a, const Operand& b, Ext
   const uint64_t sa = safe_k(a, AF, x.k), sb = safe_k(b, BF, x.k, E::kPairs);
   const uint64_t safe = sa < sb ? sa : sb;
   const uint32_t grid = static_cast<uint32_t>(wgs);
-  if (p.tile == 256)
+  if (p.tile == 256 && ring_takes(a, AF, x.k) && ring_takes(b, BF, x.k, E::kPairs))
+    ring_kernel<T, AF, BF, E><<<grid < kRingWgs ? grid : kRingWgs, kMulThreads, 0, stream>>>(
+        a, b, x, e);
+  else if (p.tile == 256)
     product_kernel<T, AF, BF, 256, 256, 2, 2, E>
         <<<grid, kMulThreads, 0, stream>>>(a, b, x, safe, e);
   else if (p.tile == 128)

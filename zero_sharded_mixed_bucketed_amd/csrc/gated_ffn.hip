@@ -21,47 +21,76 @@ __device__ __forceinline__ float sigmoid(float g) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * g));
 }
 
-// The share p of g that passes, act(g) = g p, and its slope dp/dg.  Powers that
-// overflow give p = 0 or 1; the slope's product with g is then 0.
-__device__ __forceinline__ float passed(float g, int act, float* slope) {
-  if (act == kSilu) {
+// The share p of g that passes, act(g) = g p, and its slope dp/dg.
+template <int ACT>
+__device__ __forceinline__ float passed(float g, float* slope) {
+  if constexpr (ACT == kSilu) {
     const float p = sigmoid(g);
     *slope = p * (1.0f - p);
     return p;
-  }
-  if (act == kGelu) {
+  } else if constexpr (ACT == kGelu) {
     *slope = 0.398942280401432678f * __builtin_amdgcn_exp2f(-0.5f * kLog2e * g * g);
     return 0.5f * erfcf(-0.707106781186547524f * g);
+  } else {
+    // (1 + tanh(y)) / 2 = sigmoid(2 y)
+    const float y2 = 1.59576912160573071f * (g + 0.044715f * g * g * g);
+    const float p = sigmoid(y2);
+    *slope = p * (1.0f - p) * (1.59576912160573071f + 0.214069822634528751f * g * g);
+    return p;
   }
-  // (1 + tanh(y)) / 2 = sigmoid(2 y)
-  const float y2 = 1.59576912160573071f * (g + 0.044715f * g * g * g);
-  const float p = sigmoid(y2);
-  *slope = p * (1.0f - p) * (1.59576912160573071f + 0.214069822634528751f * g * g);
-  return p;
 }
 
-// act(g), and act'(g).  A slope of 0 stays 0 beside an infinite factor (g or g^2
-// past fp32's range) only where p has reached its end, so it is kept there.
-__device__ __forceinline__ float activate(float g, int act) {
-  float slope;
-  const float p = passed(g, act, &slope);
-  return p == 0.0f ? (g != g ? g : -0.0f) : g * p;
+// act(g) of eight gates.  Where p has reached 0, g may be anything, -infinity too.
+template <int ACT>
+__device__ __forceinline__ void activate8(const float (&g)[8], float (&a)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float slope;
+    const float p = passed<ACT>(g[i], &slope);
+    a[i] = p == 0.0f ? -0.0f : g[i] * p;
+  }
 }
 
-__device__ __forceinline__ float activate(float g, int act, float* derivative) {
-  float slope;
-  const float p = passed(g, act, &slope);
-  *derivative = p == 0.0f || p == 1.0f ? p : p + g * slope;
-  return p == 0.0f ? -0.0f : g * p;
+__device__ __forceinline__ void activate8(int act, const float (&g)[8], float (&a)[8]) {
+  if (act == kSilu) activate8<kSilu>(g, a);
+  else if (act == kGelu) activate8<kGelu>(g, a);
+  else activate8<kGeluTanh>(g, a);
+}
+
+// act(g) and act'(g).  Where p has reached an end, the slope is 0 whatever g is.
+template <int ACT>
+__device__ __forceinline__ void slopes8(const float (&g)[8], float (&a)[8], float (&d)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float slope;
+    const float p = passed<ACT>(g[i], &slope);
+    d[i] = p == 0.0f || p == 1.0f ? p : p + g[i] * slope;
+    a[i] = p == 0.0f ? -0.0f : g[i] * p;
+  }
+}
+
+__device__ __forceinline__ void slopes8(int act, const float (&g)[8], float (&a)[8],
+                                        float (&d)[8]) {
+  if (act == kSilu) slopes8<kSilu>(g, a, d);
+  else if (act == kGelu) slopes8<kGelu>(g, a, d);
+  else slopes8<kGeluTanh>(g, a, d);
 }
 
 // The forward's epilogue: both sums of a column to a, and their checkpoints.
 struct Gated {
-  static constexpr bool kPairs = true, kJoins = false;
+  static constexpr bool kPairs = true, kRows = false, kJoins = false;
   Rows out;
   Ckpt c_gate, c_up, c_out;
   uint64_t cols;
   int act, format;
+
+  struct Row {};
+
+  __device__ __forceinline__ bool stores() const { return true; }
+  __device__ __forceinline__ bool simple() const { return false; }
+  __device__ __forceinline__ float load_factor() const { return 1.0f; }
+  __device__ __forceinline__ uint64_t row_of(int, uint32_t, uint64_t m) const { return m; }
+  __device__ __forceinline__ const Gated& now(uint32_t, uint64_t, float) const { return *this; }
 
   template <typename T>
   __device__ __forceinline__ void keep(const Ckpt& c, uint64_t m, uint64_t n, bool in,
@@ -79,13 +108,14 @@ struct Gated {
   __device__ __forceinline__ void put(uint32_t, uint64_t m, uint64_t n, uint64_t m_all,
                                       float (&g)[8], float (&u)[8]) const {
     const bool in = m < m_all && n < cols;
-    float a[8];
+    if (n + kChunk > cols)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      // columns past the edge hold another row's sums: 0 in their block's scale
-      if (n + i >= cols) g[i] = u[i] = 0.0f;
-      a[i] = activate(g[i], act) * u[i];
-    }
+      for (int i = 0; i < 8; ++i)       // not in their block's scale
+        if (n + i >= cols) g[i] = u[i] = 0.0f;
+    float a[8];
+    activate8(act, g, a);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a[i] *= u[i];
     const u32x4 held = pack8<T>(a);
     if (in && out.p) store8(out.p + m * out.stride, n, cols, held);
     keep<T>(c_gate, m, n, in, pack8<T>(g));
@@ -97,7 +127,7 @@ struct Gated {
 template <typename T>
 hipError_t forward(const GatedLaunch& a, hipStream_t stream) {
   const MulPlan p = plan_product(a.rows, 2 * a.width, a.cols, false, true);
-  const Operand x = {a.x.p, a.x.stride, a.rows}, w = {a.w.p, a.w.stride, a.width};
+  const Operand x = {a.x.p, a.x.stride, a.rows, false}, w = {a.w.p, a.w.stride, a.width, false};
   const Extents e = {a.rows, a.width, a.cols, 1, nullptr, 0, 0};
   const Gated g = {a.out, a.c_gate, a.c_up, a.c_out, a.width, a.act, a.format};
   return run_product<T, true, true>(p, x, w, e, g, stream);
@@ -125,12 +155,12 @@ __global__ __launch_bounds__(kMulThreads) void gated_slopes_kernel(GatedGradLaun
   unpack8<T>(w, d);
   decode8<FMT>(kg, scale_of(bg), g);
   decode8<FMT>(ku, scale_of(bu), u);
+  float held[8], slope[8];
+  slopes8(a.act, g, held, slope);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    float slope;
-    const float held = activate(g[i], a.act, &slope);
-    dg[i] = d[i] * u[i] * slope;
-    du[i] = d[i] * held;
+    dg[i] = d[i] * u[i] * slope[i];
+    du[i] = d[i] * held[i];
   }
   uint16_t* o = to + row * lead;
   store8<false>(o, c, a.width, pack8<T>(dg));
@@ -139,19 +169,30 @@ __global__ __launch_bounds__(kMulThreads) void gated_slopes_kernel(GatedGradLaun
 
 struct GradRoom {
   uint64_t lead;            // of [dg du], in elements
-  MulPlan plan;             // of dx
-  uint64_t slopes, bytes;
+  MulPlan plan, weight;     // of dx, and of dw if held
+  bool held;                // dw from x^ in 16 bits
+  uint64_t lead_x, slopes, x, bytes;
 };
 
+// dw takes x^ in 16 bits first where its product fills the chip with whole 256 x 256 tiles:
+// 8192 tokens, 4096 -> 2 x 16384 takes 1.70 + 0.04 ms where the product straight from the
+// 8-bit codes, beside their arithmetic, takes 2.20; with fewer tiles, or columns that are
+// not in whole chunks, the latter's splits and edges are better.
 GradRoom grad_room(uint64_t rows, uint64_t cols, uint64_t width) {
   GradRoom r;
-  r.lead = chunks_up(2 * width, 64);
+  r.lead = row_lead(2 * width);
+  r.lead_x = row_lead(cols);
   r.plan = plan_product(rows, cols, 2 * width, true, true);
+  r.weight = plan_product(2 * width, cols, rows, true, false);
+  r.held = r.weight.tile == 256 && rows && (2 * width) % kChunk == 0 && cols % kChunk == 0;
   r.slopes = chunks_up(rows * r.lead * 2, 256);
-  const uint64_t partial =
-      r.plan.splits > 1 ? r.plan.splits * rows * chunks_up(cols, kChunk) * 4 : 0;
-  const uint64_t weight = weight_grad_workspace(rows, cols, 2 * width);
-  r.bytes = r.slopes + (partial > weight ? partial : weight);
+  r.x = r.held ? chunks_up(rows * r.lead_x * 2, 256) : 0;
+  const uint64_t lead_out = chunks_up(cols, kChunk) * 4;
+  uint64_t rest = r.plan.splits > 1 ? r.plan.splits * rows * lead_out : 0;
+  const uint64_t weight = !r.held ? weight_grad_workspace(rows, cols, 2 * width)
+                          : r.weight.splits > 1 ? r.weight.splits * 2 * width * lead_out : 0;
+  if (weight > rest) rest = weight;
+  r.bytes = r.slopes + r.x + rest;
   return r;
 }
 
@@ -159,7 +200,8 @@ template <typename T>
 hipError_t backward(const GatedGradLaunch& a, hipStream_t stream) {
   const GradRoom room = grad_room(a.rows, a.cols, a.width);
   uint16_t* slopes = reinterpret_cast<uint16_t*>(a.workspace);
-  float* rest = reinterpret_cast<float*>(a.workspace + room.slopes);
+  uint16_t* held = reinterpret_cast<uint16_t*>(a.workspace + room.slopes);
+  float* rest = reinterpret_cast<float*>(a.workspace + room.slopes + room.x);
   if (a.rows) {
     const uint64_t segments = (a.width + 511) / 512, units = a.rows * segments;
     constexpr uint64_t kMost = most_workgroups(kMulThreads);
@@ -177,7 +219,7 @@ hipError_t backward(const GatedGradLaunch& a, hipStream_t stream) {
     }
   }
   if (a.dx.p && a.rows) {
-    const Operand d = {slopes, room.lead, a.rows}, w = {a.w.p, a.w.stride, a.cols};
+    const Operand d = {slopes, room.lead, a.rows, false}, w = {a.w.p, a.w.stride, a.cols, false};
     const Extents x = {a.rows, a.cols, 2 * a.width, 1, nullptr, 0, 0};
     Sink s = {};
     s.out = a.dx.p;
@@ -193,6 +235,32 @@ hipError_t backward(const GatedGradLaunch& a, hipStream_t stream) {
     if (e != hipSuccess) return e;
   }
   if (!a.dw) return hipSuccess;
+  if (room.held) {
+    StoreLaunch read;
+    read.c = a.c_x;
+    read.x = held;
+    read.x_stride = room.lead_x;
+    read.dtype = T::kType;
+    read.rows = a.rows;
+    read.cols = a.cols;
+    const hipError_t e = launch_ckpt_read(read, stream);
+    if (e != hipSuccess) return e;
+    const Operand d = {slopes, room.lead, 2 * a.width, false};
+    const Operand x = {held, room.lead_x, a.cols, false};
+    const Extents by = {2 * a.width, a.cols, a.rows, 1, nullptr, 0, 0};
+    Sink s = {};
+    s.out = a.dw;
+    s.stride = a.dw_stride;
+    s.dtype = a.dw_dtype;
+    s.accumulate = a.accumulate;
+    s.cols = a.cols;
+    s.lead = chunks_up(a.cols, kChunk);
+    if (room.weight.splits > 1) {
+      s.partial = rest;
+      s.split_size = 2 * a.width * s.lead;
+    }
+    return run_product<T, false, false>(room.weight, d, x, by, s, stream);
+  }
   WeightGradLaunch L;
   L.x = a.c_x;
   L.rows = a.rows;
@@ -216,7 +284,10 @@ uint64_t gated_grad_workspace(uint64_t rows, uint64_t cols, uint64_t width) {
 }
 
 bool gated_fits(uint64_t rows, uint64_t cols, uint64_t width, bool dx) {
-  if (dx) return product_fits(grad_room(rows, cols, width).plan, rows, cols);
+  if (dx) {
+    const GradRoom r = grad_room(rows, cols, width);
+    return product_fits(r.plan, rows, cols) && (!r.held || product_fits(r.weight, 2 * width, cols));
+  }
   return product_fits(plan_product(rows, 2 * width, cols, false, true), 0, 0);
 }
 

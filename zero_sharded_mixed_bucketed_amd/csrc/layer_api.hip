@@ -135,7 +135,7 @@ int check_ids(const char* name, const void* ids, int id_bytes, uint64_t rows) {
 int run_loss(const zero_loss_t* a, VocabLaunch& L, void* hip_stream, const char* what) {
   if (a->rows == 0 && (!a->dw || a->accumulate)) return ok();
   const uint64_t need =
-      vocab_workspace(a->rows, a->cols, a->vocab, a->dx != nullptr, a->dw != nullptr);
+      vocab_workspace(a->rows, a->cols, a->vocab, L.top, a->dx != nullptr, a->dw != nullptr);
   const int rc = check_workspace(a->workspace, a->workspace_bytes, need);
   if (rc) return rc;
   L.dtype = a->dtype;
@@ -244,10 +244,10 @@ int zero_gated_ffn_grad(const zero_gated_ffn_grad_t* a, void* hip_stream) {
                 "gated block gradient");
 }
 
-uint64_t zero_loss_workspace(uint64_t rows, uint64_t cols, uint64_t vocab, int with_dx,
-                             int with_dw) {
-  if (!loss_sizes(rows, cols, vocab)) return 0;
-  return vocab_workspace(rows, cols, vocab, with_dx != 0, with_dw != 0);
+uint64_t zero_loss_workspace(uint64_t rows, uint64_t cols, uint64_t vocab, uint32_t top,
+                             int with_dx, int with_dw) {
+  if (!loss_sizes(rows, cols, vocab) || top > ZERO_DISTILL_MAX_TOP) return 0;
+  return vocab_workspace(rows, cols, vocab, top, with_dx != 0, with_dw != 0);
 }
 
 int zero_vocab_loss(const zero_loss_t* a, const void* targets, int id_bytes, void* hip_stream) {

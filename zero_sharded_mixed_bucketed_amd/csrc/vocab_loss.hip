@@ -47,25 +47,28 @@ struct Head {
 struct Room {
   uint64_t piece, pieces;   // tokens of a piece
   uint64_t lead_x, lead_z, lead_w;
-  uint64_t rows, slots, flags, x, z, sums, partial, bytes;
+  uint64_t wide;            // columns of a row of logits: whole chunks, and -infinity
+  uint64_t entries;         // of a row: maxima and sums of parts of it
+  uint64_t rows, slots, flags, x, z, stats, ids, sums, partial, bytes;
   MulPlan logits, dx, dw;
 };
 
-// Bytes of a piece's logits, at most (a piece has 256 tokens at least).  Larger pieces
+// Bytes of a piece's logits, about (a piece has 256 tokens at least).  Larger pieces
 // add to dW's running sums less often.
 constexpr uint64_t kPieceBytes = 1ull << 31;
 constexpr uint64_t kMostRows = 1ull << 22;  // of a piece: a workgroup a row in one launch
 
-Room room_of(uint64_t rows, uint64_t cols, uint64_t vocab, bool dx, bool dw) {
+Room room_of(uint64_t rows, uint64_t cols, uint64_t vocab, uint32_t top, bool dx, bool dw) {
   Room r = {};
-  r.lead_x = chunks_up(cols, 64);
-  r.lead_z = chunks_up(vocab, 128);  // whole tiles of the logits' product
+  r.lead_x = row_lead(cols);
+  r.wide = chunks_up(vocab, 128);    // whole tiles of the logits' product
+  r.lead_z = row_lead(2 * r.wide) / 2;
   r.lead_w = chunks_up(cols, kChunk);
-  uint64_t most = kPieceBytes / (4 * r.lead_z) / 256 * 256;
+  uint64_t most = kPieceBytes / (4 * r.wide) / 256 * 256;
   if (most < 256) most = 256;
   if (most > kMostRows) most = kMostRows;
-  r.piece = rows < most ? rows : most;
-  r.pieces = rows ? (rows + r.piece - 1) / r.piece : 1;
+  r.pieces = rows ? (rows + most - 1) / most : 1;
+  r.piece = r.pieces > 1 ? chunks_up((rows + r.pieces - 1) / r.pieces, 256) : rows;
   uint64_t at = 256;
   const auto take = [&](uint64_t bytes) {
     const uint64_t from = at;
@@ -76,8 +79,14 @@ Room room_of(uint64_t rows, uint64_t cols, uint64_t vocab, bool dx, bool dw) {
   r.slots = take(rows * 4);
   r.flags = take(rows);
   r.x = take(r.piece * r.lead_x * 2);
-  r.z = take(r.piece * r.lead_z * 4);
   r.logits = plan_product(r.piece, vocab, cols, false, true);
+  const uint64_t tiles = (vocab + (r.logits.tile == 256 ? 255 : 127)) /
+                         (r.logits.tile == 256 ? 256 : 128);
+  r.entries = tiles * (r.logits.tile == 32 ? 4 : 2);          // one a wave's columns
+  r.stats = take(r.piece * r.entries * 8);
+  // cross entropy alone needs the target's logit of each row, not the row
+  if (dx || dw || top) r.z = take(r.piece * r.lead_z * 4);
+  else r.ids = take(r.piece * 8);
   uint64_t partial = 0;
   if (dx) {
     r.dx = plan_product(r.piece, cols, vocab, true, true);
@@ -159,7 +168,8 @@ __global__ __launch_bounds__(kPickThreads) void loss_pick_kernel(VocabLaunch a,
 // with a loss.  The first piece also clears the others' loss and dx.  A wave a token.
 __global__ __launch_bounds__(256) void loss_rows_kernel(VocabLaunch a, const uint32_t* slots,
                                                         uint64_t first, uint64_t most,
-                                                        uint16_t* to, uint64_t lead) {
+                                                        uint16_t* to, uint64_t lead,
+                                                        int32_t* ids) {
   const uint64_t t = static_cast<uint64_t>(blockIdx.x) * 4 + threadIdx.x / 64;
   if (t >= a.rows) return;
   const uint32_t slot = __builtin_amdgcn_readfirstlane(slots[t]);
@@ -173,23 +183,105 @@ __global__ __launch_bounds__(256) void loss_rows_kernel(VocabLaunch a, const uin
     return;
   }
   if (slot < first || slot >= first + most) return;
+  if (ids && threadIdx.x % 64 == 0) {
+    const int64_t id = id_at(a, t, 0);
+    ids[slot - first] = id < static_cast<int64_t>(a.vocab) ? static_cast<int32_t>(id) : -1;
+  }
   const uint16_t* from = a.x.p + t * a.x.stride;
   for (uint64_t c = c0; c < lead; c += 512)
     *reinterpret_cast<u32x4*>(to + (slot - first) * lead + c) =
         c < a.cols ? load8(from, c, a.cols) : u32x4{0, 0, 0, 0};
 }
 
-// A piece's logits, scaled; those past the vocabulary are -infinity up to the row's end.
+__device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
+
+struct Part {
+  float top, sum;           // of a part of a row: the maximum m, and the sum of exp(z - m)
+};
+
+// A piece's logits, scaled: the maximum and sum of each wave's columns of a row, from the
+// fp32 sums where they are (a row is then read once less: 4096 x 131072 words, 1060 ->
+// 590 us), and what is wanted of the logits themselves: all (those past the vocabulary
+// are -infinity up to `wide`), or each row's target's.
 struct Logits {
-  static constexpr bool kPairs = false, kJoins = false;
-  float* z;
-  uint64_t lead, vocab;
+  static constexpr bool kPairs = false, kRows = true, kJoins = false;
+  float* z;                 // or nullptr
+  uint64_t lead, wide, vocab;
   float scale;
+  Part* parts;              // [rows][entries]
+  uint64_t entries;
+  const int32_t* ids;       // of the targets, without z
+  float* caught;
+
+  __device__ __forceinline__ bool stores() const { return z != nullptr; }
+  __device__ __forceinline__ float load_factor() const { return 1.0f; }
+  __device__ __forceinline__ uint64_t row_of(int, uint32_t, uint64_t m) const { return m; }
+
+  struct Row {
+    float top = kLowest, sum = 0.0f;
+  };
+
+  template <int N>
+  __device__ __forceinline__ void columns(Row& row, float (&x)[N], uint64_t m, uint64_t n,
+                                          uint64_t m_all) const {
+    if (n + N > vocab) {
+      const int exist = static_cast<int>(static_cast<int64_t>(vocab) - static_cast<int64_t>(n));
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (i >= exist) x[i] = -INFINITY;
+    }
+    float top = row.top;
+#pragma unroll
+    for (int i = 0; i < N; ++i) top = fmaxf(top, x[i]);
+    const float c = scale * kLog2e;
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) sum += __builtin_amdgcn_exp2f((x[i] - top) * c);
+    row.sum = row.sum * __builtin_amdgcn_exp2f((row.top - top) * c) + sum;
+    row.top = top;
+    if (!ids) return;
+    const int64_t from = (m < m_all ? ids[m] : -1) - static_cast<int64_t>(n);
+    const int mine = from >= 0 && from < N ? static_cast<int>(from) : -1;
+    if (__builtin_amdgcn_ballot_w64(mine >= 0) == 0) return;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (mine == i) caught[m] = x[i] * scale;
+  }
+
+  __device__ __forceinline__ void finish(const Row& row, uint64_t m, uint64_t piece,
+                                         uint64_t m_all) const {
+    const float c = scale * kLog2e, top = fmaxf(row.top, __shfl_xor(row.top, 32));
+    float sum = row.sum * __builtin_amdgcn_exp2f((row.top - top) * c);
+    sum += __shfl_xor(sum, 32);
+    if (threadIdx.x % 64 < 32 && m < m_all) parts[m * entries + piece] = {top * scale, sum};
+  }
+
+  __device__ __forceinline__ bool simple() const { return true; }
+
+  struct Now {
+    float* z;
+    uint64_t lead;
+    float scale;
+
+    __device__ __forceinline__ uint64_t row_of(int, uint32_t, uint64_t m) const { return m; }
+
+    template <typename T>
+    __device__ __forceinline__ void put(uint32_t, uint64_t m, uint64_t n, uint64_t,
+                                        float (&x)[8]) const {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] *= scale;
+      f32x4* p = reinterpret_cast<f32x4*>(z + m * lead + n);
+      p[0] = f32x4{x[0], x[1], x[2], x[3]};
+      p[1] = f32x4{x[4], x[5], x[6], x[7]};
+    }
+  };
+
+  __device__ __forceinline__ Now now(uint32_t, uint64_t, float) const { return {z, lead, scale}; }
 
   template <typename T>
   __device__ __forceinline__ void put(uint32_t, uint64_t m, uint64_t n, uint64_t m_all,
                                       float (&x)[8]) const {
-    if (m >= m_all || n >= lead) return;
+    if (m >= m_all || n >= wide) return;
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = n + i < vocab ? x[i] * scale : -INFINITY;
     f32x4* p = reinterpret_cast<f32x4*>(z + m * lead + n);
@@ -197,8 +289,6 @@ struct Logits {
     p[1] = f32x4{x[4], x[5], x[6], x[7]};
   }
 };
-
-__device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
 
 // The sum of v over the workgroup, in every thread; the order is fixed.
 __device__ __forceinline__ float group_sum(float v, float* room) {
@@ -230,12 +320,12 @@ __device__ __forceinline__ float teacher_at(const VocabLaunch& a, uint64_t t, ui
   return a.logits_dtype == kF16 ? lo16<F16>(w) : lo16<Bf16>(w);
 }
 
-// One row a workgroup: its maximum and sum, its loss, and (GRAD) g in place of its
-// logits, 16 bits from the row's begin on.
+// One row a workgroup: its maximum and sum from its parts, its loss, and (GRAD) g in place
+// of its logits, 16 bits from the row's begin on.
 template <typename T, bool GRAD>
-__global__ __launch_bounds__(kRowThreads) void loss_row_kernel(VocabLaunch a, const Head* head,
-                                                               const uint32_t* rows, uint64_t first,
-                                                               float* z_all, uint64_t lead) {
+__global__ __launch_bounds__(kRowThreads) void loss_row_kernel(
+    VocabLaunch a, const Head* head, const uint32_t* rows, uint64_t first, const Part* parts,
+    uint64_t entries, const float* caught, float* z_all, uint64_t lead, uint64_t wide) {
   __shared__ float room[kRowThreads / 64];
   __shared__ int32_t ids[kMaxTop];
   __shared__ float shares[kMaxTop];
@@ -247,14 +337,12 @@ __global__ __launch_bounds__(kRowThreads) void loss_row_kernel(VocabLaunch a, co
 
   // the maximum m and the sum s of exp(z - m)
   float m = kLowest, s = 0.0f;
-  for (uint64_t c = tid * 4; c < lead; c += kRowThreads * 4) {
-    const f32x4 v = *reinterpret_cast<const f32x4*>(z + c);
-    const float top = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
-    if (top > m) {
-      s *= exp_of(m - top);
-      m = top;
-    }
-    s += (exp_of(v[0] - m) + exp_of(v[1] - m)) + (exp_of(v[2] - m) + exp_of(v[3] - m));
+  const Part* own_parts = parts + blockIdx.x * entries;
+  for (uint64_t e = tid; e < entries; e += kRowThreads) {
+    const Part p = own_parts[e];
+    const float top = fmaxf(m, p.top);
+    s = s * exp_of(m - top) + p.sum * exp_of(p.top - top);
+    m = top;
   }
   const float all = group_max(m, room);
   s = group_sum(s * exp_of(m - all), room);
@@ -270,7 +358,7 @@ __global__ __launch_bounds__(kRowThreads) void loss_row_kernel(VocabLaunch a, co
   if (a.top == 0) {
     const int64_t id = id_at(a, t, 0);
     lost = id >= static_cast<int64_t>(a.vocab);
-    target[0] = lost ? 0.0f : z[id];
+    target[0] = lost ? 0.0f : caught ? caught[blockIdx.x] : z[id];
     if (tid == 0) {
       ids[0] = static_cast<int32_t>(id);
       shares[0] = 1.0f;
@@ -345,10 +433,10 @@ __global__ __launch_bounds__(kRowThreads) void loss_row_kernel(VocabLaunch a, co
     // keeps all threads' loads of those before it.
     constexpr uint64_t kStep = kRowThreads * kChunk;
     uint64_t chunk = 0;
-    for (uint64_t c0 = 0; c0 < lead; c0 += kStep, ++chunk) {
+    for (uint64_t c0 = 0; c0 < wide; c0 += kStep, ++chunk) {
       const uint64_t c = c0 + tid * kChunk;
       f32x4 u = {0.f, 0.f, 0.f, 0.f}, v = u;
-      if (c < lead) {
+      if (c < wide) {
         u = *reinterpret_cast<const f32x4*>(z + c);
         v = *reinterpret_cast<const f32x4*>(z + c + 4);
       }
@@ -361,7 +449,7 @@ __global__ __launch_bounds__(kRowThreads) void loss_row_kernel(VocabLaunch a, co
         x[i] = exp_of(u[i] - m) * each;
         x[4 + i] = exp_of(v[i] - m) * each;
       }
-      if (c < lead) *reinterpret_cast<u32x4*>(g + c) = pack8<T>(x);
+      if (c < wide) *reinterpret_cast<u32x4*>(g + c) = pack8<T>(x);
     }
     __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();
@@ -377,13 +465,16 @@ __global__ __launch_bounds__(kRowThreads) void loss_row_kernel(VocabLaunch a, co
 template <typename T>
 hipError_t run_loss(const VocabLaunch& a, hipStream_t stream) {
   const bool dx = a.dx.p != nullptr, dw = a.dw != nullptr;
-  const Room r = room_of(a.rows, a.cols, a.vocab, dx, dw);
+  const Room r = room_of(a.rows, a.cols, a.vocab, a.top, dx, dw);
   uint8_t* ws = a.workspace;
   Head* head = reinterpret_cast<Head*>(ws);
   uint32_t* rows = reinterpret_cast<uint32_t*>(ws + r.rows);
   uint32_t* slots = reinterpret_cast<uint32_t*>(ws + r.slots);
   uint16_t* x = reinterpret_cast<uint16_t*>(ws + r.x);
-  float* z = reinterpret_cast<float*>(ws + r.z);
+  float* z = r.z ? reinterpret_cast<float*>(ws + r.z) : nullptr;
+  Part* parts = reinterpret_cast<Part*>(ws + r.stats);
+  int32_t* ids = r.ids ? reinterpret_cast<int32_t*>(ws + r.ids) : nullptr;
+  float* caught = r.ids ? reinterpret_cast<float*>(ws + r.ids + 4 * r.piece) : nullptr;
   float* partial = reinterpret_cast<float*>(ws + r.partial);
   const uint32_t waves = static_cast<uint32_t>((a.rows + 3) / 4);
   hipError_t e = hipSuccess;
@@ -399,29 +490,31 @@ hipError_t run_loss(const VocabLaunch& a, hipStream_t stream) {
   for (uint64_t p = 0; p < r.pieces; ++p) {
     const uint64_t first = p * r.piece;
     const uint64_t most = a.rows - first < r.piece ? a.rows - first : r.piece;
-    const Operand xs = {x, r.lead_x, most};
-    const Operand w_rows = {a.w.p, a.w.stride, a.vocab}, w_cols = {a.w.p, a.w.stride, a.cols};
+    const Operand xs = {x, r.lead_x, most, true};
+    const Operand w_rows = {a.w.p, a.w.stride, a.vocab, false};
+    const Operand w_cols = {a.w.p, a.w.stride, a.cols, false};
     const uint64_t lead_g = 2 * r.lead_z;
     const uint16_t* g = reinterpret_cast<const uint16_t*>(z);
     if (a.rows) {
-      loss_rows_kernel<<<waves, 256, 0, stream>>>(a, slots, first, most, x, r.lead_x);
+      loss_rows_kernel<<<waves, 256, 0, stream>>>(a, slots, first, most, x, r.lead_x, ids);
       if ((e = hipGetLastError()) != hipSuccess) return e;
       const Extents ex = {most, a.vocab, a.cols, 1, &head->count, first, 0};
-      const Logits logits = {z, r.lead_z, a.vocab, 1.0f / a.tau};
+      const Logits logits = {z, r.lead_z, r.wide, a.vocab, 1.0f / a.tau, parts, r.entries, ids,
+                             caught};
       e = run_product<T, true, true>(plan_of(r.logits, most, a.vocab), xs, w_rows, ex, logits,
                                      stream);
       if (e != hipSuccess) return e;
       const uint32_t grid = static_cast<uint32_t>(most);
       if (dx || dw)
-        loss_row_kernel<T, true><<<grid, kRowThreads, 0, stream>>>(a, head, rows, first, z,
-                                                                   r.lead_z);
+        loss_row_kernel<T, true><<<grid, kRowThreads, 0, stream>>>(
+            a, head, rows, first, parts, r.entries, caught, z, r.lead_z, r.wide);
       else
-        loss_row_kernel<T, false><<<grid, kRowThreads, 0, stream>>>(a, head, rows, first, z,
-                                                                    r.lead_z);
+        loss_row_kernel<T, false><<<grid, kRowThreads, 0, stream>>>(
+            a, head, rows, first, parts, r.entries, caught, z, r.lead_z, r.wide);
       if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     if (dx && a.rows) {
-      const Operand d = {g, lead_g, most};
+      const Operand d = {g, lead_g, most, true};
       const Extents ex = {most, a.cols, a.vocab, 1, &head->count, first, 0};
       Sink s = {};
       s.out = a.dx.p;
@@ -439,7 +532,7 @@ hipError_t run_loss(const VocabLaunch& a, hipStream_t stream) {
       if (e != hipSuccess) return e;
     }
     if (dw) {
-      const Operand d = {g, lead_g, a.vocab}, xc = {x, r.lead_x, a.cols};
+      const Operand d = {g, lead_g, a.vocab, true}, xc = {x, r.lead_x, a.cols, true};
       const Extents ex = {a.vocab, a.cols, most, 1, a.rows ? &head->count : nullptr, first, 1};
       Sink s = {};
       s.out = a.dw;
@@ -468,12 +561,13 @@ hipError_t run_loss(const VocabLaunch& a, hipStream_t stream) {
 
 }  // namespace
 
-uint64_t vocab_workspace(uint64_t rows, uint64_t cols, uint64_t vocab, bool dx, bool dw) {
-  return room_of(rows, cols, vocab, dx, dw).bytes;
+uint64_t vocab_workspace(uint64_t rows, uint64_t cols, uint64_t vocab, uint32_t top, bool dx,
+                         bool dw) {
+  return room_of(rows, cols, vocab, top, dx, dw).bytes;
 }
 
 bool vocab_fits(uint64_t rows, uint64_t cols, uint64_t vocab, bool dx, bool dw) {
-  const Room r = room_of(rows, cols, vocab, dx, dw);
+  const Room r = room_of(rows, cols, vocab, 0, dx, dw);
   return product_fits(r.logits, 0, 0) && (!dx || product_fits(r.dx, r.piece, cols)) &&
          (!dw || product_fits(r.dw, vocab, cols));
 }
