@@ -49,10 +49,21 @@ struct Operand {
 struct Extents {
   uint64_t m, n, k;
   uint32_t splits;          // of k, each a range of whole turns
+  uint32_t most, fill;      // see splits_of
   const uint32_t* count;
   uint64_t first;
   int count_k;
 };
+
+// The splits of a product whose rows are counted on the device: as planned for the most
+// rows, or with fewer tiles than that what fills the chip, `fill` workgroups, but not over
+// `most`.  (1200 of 3001 tokens with a loss, 50001 words at 2050: dx 510 -> 330 us.)
+__host__ __device__ inline uint32_t splits_of(uint32_t splits, uint32_t most, uint32_t fill,
+                                              uint32_t tiles) {
+  if (most <= splits || tiles == 0) return splits;
+  const uint32_t s = fill / tiles;
+  return s <= splits ? splits : s < most ? s : most;
+}
 
 template <typename T>
 __device__ __forceinline__ f32x16 mul(u32x4 a, u32x4 b, f32x16 c) {
@@ -221,21 +232,39 @@ __device__ __forceinline__ Spot spot_of(uint32_t wg, uint32_t wgs, uint32_t tile
 // tile needs none of put's checks: now(split, m0, factor) then gives what stores it,
 // factor what load_factor() gave at the kernel's begin; row_of(i, line, m) is the row at
 // which it stores row m, line `line` of the wave's i-th 32.
-template <typename T, bool UNROLL, int FM, int FN, typename E, typename P>
+template <typename T, bool WHOLE, int FM, int FN, typename E, typename P>
 __device__ __forceinline__ void wave_store(const f32x16 (&acc)[FM][FN], float* piece, const E& e,
                                            const P& to, uint32_t split, uint64_t m0, uint64_t n0,
                                            uint64_t m_all) {
   constexpr int kWide = !E::kPairs && FN > 1 ? 2 : 1;       // fragments of c beside each other
   constexpr uint32_t kLanes = kWide * 4, kLines = 64 / kLanes, kPass = 32 / kLines;
-  constexpr int kUnroll = UNROLL ? kPass : 1;
+  constexpr int kUnroll = WHOLE && !E::kPairs ? kPass : 1;
   constexpr int kTurns = E::kPairs ? FN / 2 : FN / kWide;
   constexpr int kHeld = E::kPairs ? 2 : kWide;              // fragments a turn
+  constexpr bool kOld = WHOLE && P::kOld;
   const uint32_t lane = threadIdx.x % 64, c = lane % kLanes;
+  const auto column = [&](int step) __attribute__((always_inline)) {
+    return n0 + step % kTurns * (kWide * kMulFrag) + c * kChunk;
+  };
+  // What is added, read before the turn through shared memory where it fits.
+  constexpr uint32_t kAhead = kPass / 2;
+  [[maybe_unused]] typename P::Old old[kAhead];
+  [[maybe_unused]] const auto fetch = [&](int step, uint32_t r0) __attribute__((always_inline)) {
+    if constexpr (kOld) {
+      if (!to.adds()) return;
+#pragma unroll
+      for (uint32_t r = r0; r < r0 + kAhead; ++r)
+        old[r % kAhead] = to.fetch(m0 + step / kTurns * kMulFrag + r * kLines + lane / kLanes,
+                            column(step));
+    }
+  };
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
     [[maybe_unused]] typename E::Row row;
 #pragma unroll
     for (int h = 0; h < kTurns; ++h) {
+      const int step = i * kTurns + h;
+      fetch(step, 0);
 #pragma unroll
       for (int j = 0; j < kHeld; ++j)
 #pragma unroll
@@ -268,9 +297,9 @@ __device__ __forceinline__ void wave_store(const f32x16 (&acc)[FM][FN], float* p
       }
 #pragma unroll kUnroll
       for (uint32_t r = 0; r < kPass; ++r) {
+        if (r == kAhead) fetch(step, kAhead);
         const uint32_t line = r * kLines + lane / kLanes;
-        const uint64_t m = to.row_of(i, line, m0 + i * kMulFrag + line);
-        const uint64_t n = n0 + h * (kWide * kMulFrag) + c * kChunk;
+        const uint64_t m = to.row_of(i, line, m0 + i * kMulFrag + line), n = column(step);
         const float* p = piece + line * 64;
         const uint32_t turn = line % 16;
         const f32x4 u = *reinterpret_cast<const f32x4*>(p + ((2 * c) ^ turn) * 4);
@@ -281,6 +310,8 @@ __device__ __forceinline__ void wave_store(const f32x16 (&acc)[FM][FN], float* p
           const f32x4 v2 = *reinterpret_cast<const f32x4*>(p + ((9 + 2 * c) ^ turn) * 4);
           float y2[8] = {u2[0], u2[1], u2[2], u2[3], v2[0], v2[1], v2[2], v2[3]};
           to.template put<T>(split, m, n, m_all, y, y2);
+        } else if constexpr (kOld) {
+          to.template put<T>(m, n, y, old[r % kAhead]);
         } else {
           to.template put<T>(split, m, n, m_all, y);
         }
@@ -316,11 +347,13 @@ __global__ __launch_bounds__(kMulThreads) void product_kernel(Operand a, Operand
   const uint32_t tiles_m = static_cast<uint32_t>((m_all + TM - 1) / TM);
   constexpr int kOutN = E::kPairs ? TN / 2 : TN;            // columns of c a tile
   const uint32_t tiles_n = static_cast<uint32_t>((x.n + kOutN - 1) / kOutN);
-  const uint32_t wgs = tiles_m * tiles_n * x.splits;
+  const uint32_t splits = splits_of(x.splits, x.most, x.fill, tiles_m * tiles_n);
+  const uint32_t wgs = tiles_m * tiles_n * splits;
   if (blockIdx.x >= wgs) return;
+  epilogue.cut(splits, m_all);
   const Spot at = spot_of(blockIdx.x, wgs, tiles_m, tiles_n);
   const uint64_t m0 = static_cast<uint64_t>(at.m) * TM, n0 = static_cast<uint64_t>(at.n) * kOutN;
-  const uint64_t per = ((k_all + x.splits - 1) / x.splits + kMulDepth - 1) / kMulDepth * kMulDepth;
+  const uint64_t per = ((k_all + splits - 1) / splits + kMulDepth - 1) / kMulDepth * kMulDepth;
   const uint64_t k_lo = at.split * per < k_all ? at.split * per : k_all;
   const uint64_t k_hi = k_lo + per < k_all ? k_lo + per : k_all;
   const uint32_t tid = threadIdx.x, wave = tid / 64;
@@ -601,9 +634,11 @@ __global__ __launch_bounds__(kMulThreads, 1) void ring_kernel(Operand a, Operand
   constexpr int kOutN = E::kPairs ? kRingTile / 2 : kRingTile;
   const uint32_t tiles_m = static_cast<uint32_t>((m_all + kRingTile - 1) / kRingTile);
   const uint32_t tiles_n = static_cast<uint32_t>((x.n + kOutN - 1) / kOutN);
-  const uint32_t wgs = tiles_m * tiles_n * x.splits;
+  const uint32_t splits = splits_of(x.splits, x.most, x.fill, tiles_m * tiles_n);
+  const uint32_t wgs = tiles_m * tiles_n * splits;
   if (blockIdx.x >= wgs) return;
-  const uint64_t per = ((k_all + x.splits - 1) / x.splits + kMulDepth - 1) / kMulDepth * kMulDepth;
+  epilogue.cut(splits, m_all);
+  const uint64_t per = ((k_all + splits - 1) / splits + kMulDepth - 1) / kMulDepth * kMulDepth;
   const uint32_t lane = threadIdx.x % 64;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const uint32_t wm = wave / 2 * 128, wn = wave % 2 * 128;
@@ -695,11 +730,12 @@ __global__ __launch_bounds__(kMulThreads, 1) void ring_kernel(Operand a, Operand
   asm volatile("s_waitcnt vmcnt(%0)" ::"i"(kFirst) : "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
-#pragma unroll
-  for (int q = 0; q < kReads; ++q) read(ring, 0, 0, q);
 
 #pragma unroll 1
   for (uint32_t tile = blockIdx.x; tile < wgs; tile += gridDim.x) {
+    // again for a next tile, whose first stage is there: registers that the stores need
+#pragma unroll
+    for (int q = 0; q < kReads; ++q) read(ring, 0, 0, q);
     const Spot at = spot_of(tile, wgs, tiles_m, tiles_n);
     const uint64_t lo = at.split * per < k_all ? at.split * per : k_all;
     const uint64_t hi = lo + per < k_all ? lo + per : k_all;
@@ -752,7 +788,7 @@ __global__ __launch_bounds__(kMulThreads, 1) void ring_kernel(Operand a, Operand
     const bool whole = static_cast<uint64_t>(at.m + 1) * kRingTile <= m_all &&
                        static_cast<uint64_t>(at.n + 1) * kOutN <= x.n;
     if (whole && epilogue.simple())
-      wave_store<T, !E::kPairs>(acc, piece, epilogue, epilogue.now(at.split, m0, by), at.split,
+      wave_store<T, true>(acc, piece, epilogue, epilogue.now(at.split, m0, by), at.split,
                                 m0, n0, m_all);
     else
       wave_store<T, false>(acc, piece, epilogue, epilogue, at.split, m0, n0, m_all);
@@ -785,8 +821,8 @@ struct Sink {
   uint64_t cols;
   const uint32_t* rows;    // the result's row of row m, or nullptr: m
   const float* factor;     // in device memory, or nullptr
-  float* partial;          // [splits][most rows][lead], or nullptr: one split
-  uint64_t split_size;
+  float* partial;          // [splits][rows][lead], or nullptr: one split
+  uint64_t split_size;     // elements: rows * lead
   float* sums;             // [rows][lead] running sums, or nullptr
   int add, last;           // add what `sums` holds; the result is final
   uint64_t lead;           // cols, rounded up to a chunk
@@ -843,21 +879,33 @@ struct Sink {
     store8<false>(o, n, cols, pack8<T>(x));
   }
 
+  static constexpr bool kOld = false;
   struct Row {};
+  struct Old {};
+
+  __device__ __forceinline__ void cut(uint32_t splits, uint64_t m_all) {
+    if (splits == 1) partial = nullptr;
+    split_size = m_all * lead;
+  }
 
   __device__ __forceinline__ bool stores() const { return true; }
   __device__ __forceinline__ uint64_t row_of(int, uint32_t, uint64_t m) const { return m; }
 
-  // Whole tiles: partial or running sums that are stored, or a 16-bit result that is.
-  __device__ __forceinline__ bool simple() const {
-    return partial || (sums ? !add && !last : dtype != kF32 && !accumulate);
-  }
+  // Whole tiles: all but the last running sums on top of an old result.
+  __device__ __forceinline__ bool simple() const { return !(sums && add && last && accumulate); }
 
+  // What is stored, and what is added to it: old running sums before the factor, or an old
+  // result after it.
   struct Now {
-    float* to;              // sums' place, or nullptr
-    uint64_t lead;
-    uint16_t* out;
-    uint64_t stride;
+    static constexpr bool kOld = true;
+    struct Old {
+      u32x4 a, b;
+    };
+    uint8_t* out;
+    uint64_t stride;        // bytes, as all here
+    const uint8_t* old;     // or nullptr
+    uint64_t old_stride;
+    bool wide, old_wide, old_first;   // fp32
     float factor;
     bool mapped;
     uint32_t rows[4];       // mapped: the rows of lane % 32 in each 32 of the wave's
@@ -868,18 +916,44 @@ struct Sink {
                                                                 static_cast<int>(rows[i])));
     }
 
+    __device__ __forceinline__ bool adds() const { return old != nullptr; }
+
+    __device__ __forceinline__ Old fetch(uint64_t m, uint64_t n) const {
+      const uint8_t* p = old + m * old_stride + n * (old_wide ? 4 : 2);
+      Old o;
+      o.a = *reinterpret_cast<const u32x4_at2*>(p);
+      o.b = *reinterpret_cast<const u32x4_at2*>(p + (old_wide ? 16 : 0));
+      return o;
+    }
+
     template <typename T>
-    __device__ __forceinline__ void put(uint32_t, uint64_t m, uint64_t n, uint64_t,
-                                        float (&x)[8]) const {
-      if (to) {
-        f32x4* p = reinterpret_cast<f32x4*>(to + m * lead + n);
-        p[0] = f32x4{x[0], x[1], x[2], x[3]};
-        p[1] = f32x4{x[4], x[5], x[6], x[7]};
-        return;
-      }
+    __device__ __forceinline__ void put(uint64_t m, uint64_t n, float (&x)[8], Old o) const {
+      float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (old) {
+        if (old_wide) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] *= factor;
-      *reinterpret_cast<u32x4_at2*>(out + m * stride + n) = pack8<T>(x);
+          for (int i = 0; i < 4; ++i) {
+            y[i] = __builtin_bit_cast(float, o.a[i]);
+            y[4 + i] = __builtin_bit_cast(float, o.b[i]);
+          }
+        } else {
+          unpack8<T>(o.a, y);
+        }
+      }
+      if (old_first) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = (y[i] + x[i]) * factor;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = x[i] * factor + y[i];
+      }
+      if (wide) {
+        f32x4_at4* w = reinterpret_cast<f32x4_at4*>(out + m * stride + n * 4);
+        w[0] = f32x4{x[0], x[1], x[2], x[3]};
+        w[1] = f32x4{x[4], x[5], x[6], x[7]};
+      } else {
+        *reinterpret_cast<u32x4_at2*>(out + m * stride + n * 2) = pack8<T>(x);
+      }
     }
   };
 
@@ -891,8 +965,28 @@ struct Sink {
   }
 
   __device__ __forceinline__ Now now(uint32_t split, uint64_t m0, float by) const {
-    Now n = {partial ? partial + split * split_size : sums, lead, static_cast<uint16_t*>(out),
-             stride, by, rows && !partial && !sums, {0, 0, 0, 0}};
+    Now n = {};
+    if (partial || (sums && !last)) {
+      n.out = reinterpret_cast<uint8_t*>(partial ? partial + split * split_size : sums);
+      n.stride = lead * 4;
+      n.wide = true;
+      n.factor = 1.0f;
+    } else {
+      n.out = static_cast<uint8_t*>(out);
+      n.wide = dtype == kF32;
+      n.stride = stride * (n.wide ? 4 : 2);
+      n.factor = by;
+      n.mapped = rows != nullptr;
+    }
+    if (!partial && sums && add) {
+      n.old = reinterpret_cast<const uint8_t*>(sums);
+      n.old_stride = lead * 4;
+      n.old_wide = n.old_first = true;
+    } else if (!partial && !sums && accumulate) {
+      n.old = n.out;
+      n.old_stride = n.stride;
+      n.old_wide = n.wide;
+    }
     if (n.mapped) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) n.rows[i] = rows[m0 + i * 32 + threadIdx.x % 32];
@@ -918,13 +1012,18 @@ struct Sink {
 
 // Adds the splits' partial sums in their order, eight neighbouring columns a thread.
 template <typename T>
-__global__ __launch_bounds__(kMulThreads) void join_kernel(Sink s, Extents x) {
+__global__ __launch_bounds__(kMulThreads) void join_kernel(Sink s, Extents x, uint32_t tile_m,
+                                                           uint32_t tiles_n) {
   uint64_t m_all = x.m;
   if (x.count && !x.count_k) {
     const uint64_t c = *x.count;
     const uint64_t left = c > x.first ? c - x.first : 0;
     m_all = left < m_all ? left : m_all;
   }
+  const uint32_t tiles = static_cast<uint32_t>((m_all + tile_m - 1) / tile_m) * tiles_n;
+  const uint32_t splits = splits_of(x.splits, x.most, x.fill, tiles);
+  if (splits == 1) return;
+  s.cut(splits, m_all);
   const uint64_t per_row = s.lead / kChunk;
   const uint64_t id = static_cast<uint64_t>(blockIdx.x) * kMulThreads + threadIdx.x;
   const uint64_t m = id / per_row, n = id % per_row * kChunk;
@@ -932,7 +1031,7 @@ __global__ __launch_bounds__(kMulThreads) void join_kernel(Sink s, Extents x) {
   f32x4 u = {0.f, 0.f, 0.f, 0.f}, v = u;
   const float* p = s.partial + m * s.lead + n;
 #pragma unroll 8
-  for (uint32_t i = 0; i < x.splits; ++i, p += s.split_size) {
+  for (uint32_t i = 0; i < splits; ++i, p += s.split_size) {
     u += *reinterpret_cast<const f32x4*>(p);
     v += *reinterpret_cast<const f32x4*>(p + 4);
   }
@@ -940,51 +1039,84 @@ __global__ __launch_bounds__(kMulThreads) void join_kernel(Sink s, Extents x) {
   s.finish<T>(m, n, sum);
 }
 
-// How a product is cut: the tile of c (256 x 256, 128 x 128, or 32 rows x 128) and the
-// splits of k.
+// How a product is cut: the tile of c (256 x 256, 128 x 128, or 32 rows x 128; of pairs 32
+// rows x 2 x 128), the splits of k, and their most where rows are counted on the device.
 struct MulPlan {
   int tile;
-  uint32_t splits;
-  uint64_t tiles;
+  uint32_t splits, most, fill;
+  uint64_t tiles, tiles_n;
 };
 
-// The cut with the least estimated time, in microseconds as measured on MI355X: a
-// workgroup of 256 x 256 has a compute unit to itself and takes 14 us and 0.028 a k;
-// one of 128 x 128 takes 7 us and 0.015 a k alone on its unit, 0.021 beside a second
-// one; a join costs a launch, and its partial sums' way out and back.  n counts
-// columns of b's tile; few_rows: tiles of 32 rows are built (k fast in a).
-inline MulPlan plan_product(uint64_t m, uint64_t n, uint64_t k, bool may_split, bool few_rows) {
+// What may be: splits at all; tiles of 32 rows (k fast in a); rows that are counted on
+// the device; pairs; operands of whole chunks (ring_takes).
+struct MulWays {
+  bool split, few_rows, counted, pairs, whole;
+};
+
+inline uint64_t tile_columns(int tile, bool pairs) {
+  return tile == 256 || (tile == 32 && pairs) ? 256 : 128;
+}
+
+// The same cut over m rows of c and n columns of b.
+inline MulPlan plan_of(MulPlan p, uint64_t m, uint64_t n, bool pairs = false) {
+  const uint64_t tn = tile_columns(p.tile, pairs);
+  p.tiles_n = (n + tn - 1) / tn;
+  p.tiles = (m + p.tile - 1) / p.tile * p.tiles_n;
+  return p;
+}
+
+// The cut with the least estimated time.  Microseconds of a round of workgroups that the
+// chip holds together, as measured on MI355X: a fixed part, and one for each k, which is
+// less where fewer workgroups share a compute unit.  256 x 256: 7 + 0.026 k (14 + 0.0285 k
+// where the operands are not whole chunks); 128 x 128, two a unit: 6.7 + 0.0141 k, one:
+// 0.0075 k; 32 x 128, four a unit: 4.3 + 0.0123 k, two: 0.0075 k, one: 0.0056 k.  A join
+// costs a launch, and its partial sums' way out and back.  (4096 x 4096 over 1024, k slow:
+// 43, 55 us in 256, 128; 200 x 4096 over 1024, k fast: 35, 18, 11 us in 256, 128, 32.)
+inline MulPlan plan_product(uint64_t m, uint64_t n, uint64_t k, const MulWays& may) {
   constexpr uint64_t kUnits = 256;
-  MulPlan best = {128, 1, 0};
+  MulPlan best = {};
   double least = 0;
   for (const int tile : {256, 128, 32}) {
-    if (tile == 32 && (m > 32 || !few_rows)) continue;
-    const uint64_t tn = tile == 256 ? 256 : 128;
-    const uint64_t tiles = ((m + tile - 1) / tile) * ((n + tn - 1) / tn);
+    if (tile == 32 && !may.few_rows) continue;
+    MulPlan p = {tile, 1, 1, 0, 0, 0};
+    p = plan_of(p, m, n, may.pairs);
+    const bool wide = tile == 32 && may.pairs;
+    const uint64_t at_once = tile == 256 ? kUnits : tile == 128 || wide ? 2 * kUnits : 4 * kUnits;
+    p.fill = static_cast<uint32_t>(at_once);
     for (const uint32_t s : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
-      if (s > 1 && (!may_split || k < 256 * s)) break;
-      const uint64_t per = ((k + s - 1) / s + 63) / 64 * 64, wgs = tiles * s;
-      const uint64_t at_once = tile == 256 ? kUnits : tile == 128 ? 2 * kUnits : 4 * kUnits;
+      if (s > 1 && (!may.split || k < 256 * s)) break;
+      p.splits = s;
+      p.most = s;
+      const uint64_t per = ((k + s - 1) / s + 63) / 64 * 64, wgs = p.tiles * s;
       const double rounds = static_cast<double>((wgs + at_once - 1) / at_once);
-      const double each = tile == 256 ? 0.028 : tile == 128 ? (wgs > kUnits ? 0.021 : 0.015)
-                                                            : (wgs > 2 * kUnits ? 0.02 : 0.01);
-      const double fix = tile == 256 ? 14.0 : tile == 128 ? 7.0 : 4.0;
+      const double each = tile == 256 ? (may.whole ? 0.026 : 0.0285)
+                          : tile == 128 ? (wgs > kUnits ? 0.0141 : 0.0075)
+                          : wide ? (wgs > kUnits ? 0.0123 : 0.0075)
+                                 : (wgs > 2 * kUnits ? 0.0123 : wgs > kUnits ? 0.0075 : 0.0056);
+      const double fix = tile == 256 ? (may.whole ? 7.0 : 14.0) : tile == 128 ? 6.7 : 4.3;
       double us = rounds * (fix + each * static_cast<double>(per));
-      if (s > 1) us += 3.0 + s * static_cast<double>(m) * static_cast<double>(n) * 8 / 6e6;
+      if (s > 1) us += 4.0 + s * static_cast<double>(m) * static_cast<double>(n) * 8 / 5e6;
       if (best.tiles == 0 || us < least) {
         least = us;
-        best = {tile, s, tiles};
+        best = p;
       }
     }
+  }
+  if (may.counted && may.split) {
+    const uint64_t most = k / 256 < 32 ? k / 256 : 32;
+    if (most > best.most) best.most = static_cast<uint32_t>(most);
   }
   return best;
 }
 
-// The same cut over fewer rows of c.
-inline MulPlan plan_of(MulPlan p, uint64_t m, uint64_t n) {
-  const uint64_t tn = p.tile == 256 ? 256 : 128;
-  p.tiles = ((m + p.tile - 1) / p.tile) * ((n + tn - 1) / tn);
-  return p;
+// Rows of partial sums that the cut's splits of m rows may need: with fewer rows there may
+// be more splits, but no more than fill the chip.
+inline uint64_t partial_rows(const MulPlan& p, uint64_t m) {
+  if (p.most <= 1) return 0;
+  const uint64_t planned = p.splits > 1 ? p.splits * m : 0;
+  if (p.most == p.splits) return planned;
+  const uint64_t filled = p.fill / p.tiles_n * p.tile;
+  return filled > planned ? filled : planned;
 }
 
 inline uint64_t chunks_up(uint64_t n, uint64_t to) { return (n + to - 1) / to * to; }
@@ -1000,7 +1132,7 @@ inline uint64_t row_lead(uint64_t n) {
 // Whether a product, and the join of its splits, is one launch each.
 inline bool product_fits(const MulPlan& p, uint64_t m, uint64_t n) {
   constexpr uint64_t kMost = most_workgroups(kMulThreads);
-  const uint64_t joins = p.splits > 1 ? (m * (chunks_up(n, kChunk) / kChunk)) / kMulThreads + 1 : 0;
+  const uint64_t joins = p.most > 1 ? (m * (chunks_up(n, kChunk) / kChunk)) / kMulThreads + 1 : 0;
   return p.tiles <= kMost / p.splits && joins <= kMost;
 }
 
@@ -1010,7 +1142,10 @@ template <typename T, bool AF, bool BF, typename E>
 hipError_t run_product(const MulPlan& p, const Operand& a, const Operand& b, Extents x, const E& e,
                        hipStream_t stream) {
   x.splits = p.splits;
-  const uint64_t wgs = p.tiles * p.splits;
+  x.most = p.most;
+  x.fill = p.fill;
+  uint64_t wgs = p.tiles * p.splits;
+  if (p.most > p.splits && wgs < p.fill) wgs = p.fill;
   if (!product_fits(p, x.m, x.n)) return hipErrorInvalidConfiguration;
   const uint64_t sa = safe_k(a, AF, x.k), sb = safe_k(b, BF, x.k, E::kPairs);
   const uint64_t safe = sa < sb ? sa : sb;
@@ -1032,9 +1167,10 @@ hipError_t run_product(const MulPlan& p, const Operand& a, const Operand& b, Ext
         <<<grid, kMulThreads, 0, stream>>>(a, b, x, safe, e);
   hipError_t err = hipGetLastError();
   if constexpr (!E::kPairs && E::kJoins) {
-    if (err != hipSuccess || p.splits == 1) return err;
+    if (err != hipSuccess || p.most == 1) return err;
     const uint64_t joins = (x.m * (e.lead / kChunk) + kMulThreads - 1) / kMulThreads;
-    join_kernel<T><<<static_cast<uint32_t>(joins), kMulThreads, 0, stream>>>(e, x);
+    join_kernel<T><<<static_cast<uint32_t>(joins), kMulThreads, 0, stream>>>(
+        e, x, static_cast<uint32_t>(p.tile), static_cast<uint32_t>(p.tiles_n));
     err = hipGetLastError();
   }
   return err;

@@ -84,8 +84,11 @@ struct Gated {
   uint64_t cols;
   int act, format;
 
+  static constexpr bool kOld = false;
   struct Row {};
+  struct Old {};
 
+  __device__ __forceinline__ void cut(uint32_t, uint64_t) {}
   __device__ __forceinline__ bool stores() const { return true; }
   __device__ __forceinline__ bool simple() const { return false; }
   __device__ __forceinline__ float load_factor() const { return 1.0f; }
@@ -124,11 +127,13 @@ struct Gated {
   }
 };
 
+MulWays forward_ways(uint64_t cols) { return {false, true, false, true, cols % kChunk == 0}; }
+
 template <typename T>
 hipError_t forward(const GatedLaunch& a, hipStream_t stream) {
-  const MulPlan p = plan_product(a.rows, 2 * a.width, a.cols, false, true);
+  const MulPlan p = plan_product(a.rows, 2 * a.width, a.cols, forward_ways(a.cols));
   const Operand x = {a.x.p, a.x.stride, a.rows, false}, w = {a.w.p, a.w.stride, a.width, false};
-  const Extents e = {a.rows, a.width, a.cols, 1, nullptr, 0, 0};
+  const Extents e = {a.rows, a.width, a.cols, 1, 1, 0, nullptr, 0, 0};
   const Gated g = {a.out, a.c_gate, a.c_up, a.c_out, a.width, a.act, a.format};
   return run_product<T, true, true>(p, x, w, e, g, stream);
 }
@@ -182,15 +187,16 @@ GradRoom grad_room(uint64_t rows, uint64_t cols, uint64_t width) {
   GradRoom r;
   r.lead = row_lead(2 * width);
   r.lead_x = row_lead(cols);
-  r.plan = plan_product(rows, cols, 2 * width, true, true);
-  r.weight = plan_product(2 * width, cols, rows, true, false);
-  r.held = r.weight.tile == 256 && rows && (2 * width) % kChunk == 0 && cols % kChunk == 0;
+  const bool whole = (2 * width) % kChunk == 0 && cols % kChunk == 0;
+  r.plan = plan_product(rows, cols, 2 * width, {true, true, false, false, whole});
+  r.weight = plan_product(2 * width, cols, rows, {true, false, false, false, whole});
+  r.held = r.weight.tile == 256 && rows && whole;
   r.slopes = chunks_up(rows * r.lead * 2, 256);
   r.x = r.held ? chunks_up(rows * r.lead_x * 2, 256) : 0;
   const uint64_t lead_out = chunks_up(cols, kChunk) * 4;
-  uint64_t rest = r.plan.splits > 1 ? r.plan.splits * rows * lead_out : 0;
+  uint64_t rest = partial_rows(r.plan, rows) * lead_out;
   const uint64_t weight = !r.held ? weight_grad_workspace(rows, cols, 2 * width)
-                          : r.weight.splits > 1 ? r.weight.splits * 2 * width * lead_out : 0;
+                          : partial_rows(r.weight, 2 * width) * lead_out;
   if (weight > rest) rest = weight;
   r.bytes = r.slopes + r.x + rest;
   return r;
@@ -220,17 +226,14 @@ hipError_t backward(const GatedGradLaunch& a, hipStream_t stream) {
   }
   if (a.dx.p && a.rows) {
     const Operand d = {slopes, room.lead, a.rows, false}, w = {a.w.p, a.w.stride, a.cols, false};
-    const Extents x = {a.rows, a.cols, 2 * a.width, 1, nullptr, 0, 0};
+    const Extents x = {a.rows, a.cols, 2 * a.width, 1, 1, 0, nullptr, 0, 0};
     Sink s = {};
     s.out = a.dx.p;
     s.stride = a.dx.stride;
     s.dtype = T::kType;
     s.cols = a.cols;
     s.lead = chunks_up(a.cols, kChunk);
-    if (room.plan.splits > 1) {
-      s.partial = rest;
-      s.split_size = a.rows * s.lead;
-    }
+    s.partial = rest;
     const hipError_t e = run_product<T, true, false>(room.plan, d, w, x, s, stream);
     if (e != hipSuccess) return e;
   }
@@ -247,7 +250,7 @@ hipError_t backward(const GatedGradLaunch& a, hipStream_t stream) {
     if (e != hipSuccess) return e;
     const Operand d = {slopes, room.lead, 2 * a.width, false};
     const Operand x = {held, room.lead_x, a.cols, false};
-    const Extents by = {2 * a.width, a.cols, a.rows, 1, nullptr, 0, 0};
+    const Extents by = {2 * a.width, a.cols, a.rows, 1, 1, 0, nullptr, 0, 0};
     Sink s = {};
     s.out = a.dw;
     s.stride = a.dw_stride;
@@ -255,10 +258,7 @@ hipError_t backward(const GatedGradLaunch& a, hipStream_t stream) {
     s.accumulate = a.accumulate;
     s.cols = a.cols;
     s.lead = chunks_up(a.cols, kChunk);
-    if (room.weight.splits > 1) {
-      s.partial = rest;
-      s.split_size = 2 * a.width * s.lead;
-    }
+    s.partial = rest;
     return run_product<T, false, false>(room.weight, d, x, by, s, stream);
   }
   WeightGradLaunch L;
@@ -288,7 +288,7 @@ bool gated_fits(uint64_t rows, uint64_t cols, uint64_t width, bool dx) {
     const GradRoom r = grad_room(rows, cols, width);
     return product_fits(r.plan, rows, cols) && (!r.held || product_fits(r.weight, 2 * width, cols));
   }
-  return product_fits(plan_product(rows, 2 * width, cols, false, true), 0, 0);
+  return product_fits(plan_product(rows, 2 * width, cols, forward_ways(cols)), 0, 0);
 }
 
 hipError_t launch_gated_ffn(const GatedLaunch& a, hipStream_t stream) {

@@ -79,7 +79,8 @@ Room room_of(uint64_t rows, uint64_t cols, uint64_t vocab, uint32_t top, bool dx
   r.slots = take(rows * 4);
   r.flags = take(rows);
   r.x = take(r.piece * r.lead_x * 2);
-  r.logits = plan_product(r.piece, vocab, cols, false, true);
+  const bool whole = cols % kChunk == 0;
+  r.logits = plan_product(r.piece, vocab, cols, {false, true, true, false, whole});
   const uint64_t tiles = (vocab + (r.logits.tile == 256 ? 255 : 127)) /
                          (r.logits.tile == 256 ? 256 : 128);
   r.entries = tiles * (r.logits.tile == 32 ? 4 : 2);          // one a wave's columns
@@ -89,12 +90,12 @@ Room room_of(uint64_t rows, uint64_t cols, uint64_t vocab, uint32_t top, bool dx
   else r.ids = take(r.piece * 8);
   uint64_t partial = 0;
   if (dx) {
-    r.dx = plan_product(r.piece, cols, vocab, true, true);
-    if (r.dx.splits > 1) partial = r.dx.splits * r.piece * r.lead_w * 4;
+    r.dx = plan_product(r.piece, cols, vocab, {true, true, true, false, whole});
+    partial = partial_rows(r.dx, r.piece) * r.lead_w * 4;
   }
   if (dw) {
-    r.dw = plan_product(vocab, cols, r.piece, true, false);
-    const uint64_t more = r.dw.splits > 1 ? r.dw.splits * vocab * r.lead_w * 4 : 0;
+    r.dw = plan_product(vocab, cols, r.piece, {true, false, false, false, true});
+    const uint64_t more = partial_rows(r.dw, vocab) * r.lead_w * 4;
     if (more > partial) partial = more;
     if (r.pieces > 1) r.sums = take(vocab * r.lead_w * 4);
   }
@@ -204,7 +205,8 @@ struct Part {
 // 590 us), and what is wanted of the logits themselves: all (those past the vocabulary
 // are -infinity up to `wide`), or each row's target's.
 struct Logits {
-  static constexpr bool kPairs = false, kRows = true, kJoins = false;
+  static constexpr bool kPairs = false, kRows = true, kJoins = false, kOld = false;
+  struct Old {};
   float* z;                 // or nullptr
   uint64_t lead, wide, vocab;
   float scale;
@@ -213,6 +215,7 @@ struct Logits {
   const int32_t* ids;       // of the targets, without z
   float* caught;
 
+  __device__ __forceinline__ void cut(uint32_t, uint64_t) {}
   __device__ __forceinline__ bool stores() const { return z != nullptr; }
   __device__ __forceinline__ float load_factor() const { return 1.0f; }
   __device__ __forceinline__ uint64_t row_of(int, uint32_t, uint64_t m) const { return m; }
@@ -259,6 +262,8 @@ struct Logits {
   __device__ __forceinline__ bool simple() const { return true; }
 
   struct Now {
+    static constexpr bool kOld = false;
+    struct Old {};
     float* z;
     uint64_t lead;
     float scale;
@@ -498,7 +503,7 @@ hipError_t run_loss(const VocabLaunch& a, hipStream_t stream) {
     if (a.rows) {
       loss_rows_kernel<<<waves, 256, 0, stream>>>(a, slots, first, most, x, r.lead_x, ids);
       if ((e = hipGetLastError()) != hipSuccess) return e;
-      const Extents ex = {most, a.vocab, a.cols, 1, &head->count, first, 0};
+      const Extents ex = {most, a.vocab, a.cols, 1, 1, 0, &head->count, first, 0};
       const Logits logits = {z, r.lead_z, r.wide, a.vocab, 1.0f / a.tau, parts, r.entries, ids,
                              caught};
       e = run_product<T, true, true>(plan_of(r.logits, most, a.vocab), xs, w_rows, ex, logits,
@@ -515,7 +520,7 @@ hipError_t run_loss(const VocabLaunch& a, hipStream_t stream) {
     }
     if (dx && a.rows) {
       const Operand d = {g, lead_g, most, true};
-      const Extents ex = {most, a.cols, a.vocab, 1, &head->count, first, 0};
+      const Extents ex = {most, a.cols, a.vocab, 1, 1, 0, &head->count, first, 0};
       Sink s = {};
       s.out = a.dx.p;
       s.stride = a.dx.stride;
@@ -524,16 +529,13 @@ hipError_t run_loss(const VocabLaunch& a, hipStream_t stream) {
       s.rows = rows + first;
       s.factor = &head->unit;
       s.lead = r.lead_w;
-      if (r.dx.splits > 1) {
-        s.partial = partial;
-        s.split_size = most * r.lead_w;
-      }
+      s.partial = partial;
       e = run_product<T, true, false>(plan_of(r.dx, most, a.cols), d, w_cols, ex, s, stream);
       if (e != hipSuccess) return e;
     }
     if (dw) {
       const Operand d = {g, lead_g, a.vocab, true}, xc = {x, r.lead_x, a.cols, true};
-      const Extents ex = {a.vocab, a.cols, most, 1, a.rows ? &head->count : nullptr, first, 1};
+      const Extents ex = {a.vocab, a.cols, most, 1, 1, 0, a.rows ? &head->count : nullptr, first, 1};
       Sink s = {};
       s.out = a.dw;
       s.stride = a.dw_stride;
@@ -542,10 +544,7 @@ hipError_t run_loss(const VocabLaunch& a, hipStream_t stream) {
       s.cols = a.cols;
       s.factor = a.rows ? &head->unit : nullptr;
       s.lead = r.lead_w;
-      if (r.dw.splits > 1) {
-        s.partial = partial;
-        s.split_size = a.vocab * r.lead_w;
-      }
+      s.partial = partial;
       s.last = 1;
       if (r.pieces > 1) {
         s.sums = reinterpret_cast<float*>(ws + r.sums);
