@@ -321,13 +321,43 @@ __device__ __forceinline__ void wave_store(const f32x16 (&acc)[FM][FN], float* p
   }
 }
 
+// The same of two waves that have a fragment each, of the same columns of the two stacked
+// matrices: `which` is this wave's.  They share `piece`, and store half of its rows each.
+// All of a workgroup's waves call it together.
+template <typename T, typename E>
+__device__ __forceinline__ void pair_store(const f32x16& v, float* piece, const E& e,
+                                           uint32_t which, uint64_t m0, uint64_t n0,
+                                           uint64_t m_all) {
+  const uint32_t lane = threadIdx.x % 64, c = lane % 4;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const uint32_t line = lane % 32, q = which * 8 + r * 2 + lane / 32;
+    *reinterpret_cast<f32x4*>(piece + line * 64 + ((q ^ (line % 16)) * 4)) =
+        f32x4{v[4 * r], v[4 * r + 1], v[4 * r + 2], v[4 * r + 3]};
+  }
+  __syncthreads();
+  const uint32_t line = which * 16 + lane / 4;
+  const float* p = piece + line * 64;
+  float x[2][8];
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const f32x4 u = *reinterpret_cast<const f32x4*>(p + ((j * 8 + 2 * c + h) ^ (line % 16)) * 4);
+#pragma unroll
+      for (int d = 0; d < 4; ++d) x[j][4 * h + d] = u[d];
+    }
+  e.template put<T>(0, m0 + line, n0 + c * kChunk, m_all, x[0], x[1]);
+}
+
 // Operands of any alignment, WM x WN waves.
 template <typename T, bool AF, bool BF, int TM, int TN, int WM, int WN, typename E>
 __global__ __launch_bounds__(kMulThreads) void product_kernel(Operand a, Operand b, Extents x,
                                                               uint64_t safe, E epilogue) {
   static_assert(WM * WN == 4, "four waves");
   typedef Side<AF, TM> A;
-  typedef Side<BF, TN, E::kPairs ? TN / WN / 2 : 0> B;
+  constexpr bool kShared = E::kPairs && TN / WN == kMulFrag;   // pair_store
+  typedef Side<BF, TN, kShared ? kMulFrag : E::kPairs ? TN / WN / 2 : 0> B;
   constexpr int kFm = TM / WM / kMulFrag, kFn = TN / WN / kMulFrag;
   constexpr int kSub = kMulDepth / kMulStep, kMul = kFm * kFn;
   constexpr uint32_t kCols = TN / WN, kPiece = kMulFrag * 64;
@@ -470,8 +500,12 @@ __global__ __launch_bounds__(kMulThreads) void product_kernel(Operand a, Operand
   }
   __syncthreads();
 
-  wave_store<T, false>(acc, lds + wave * kPiece, epilogue, epilogue, at.split, m0 + wm,
-                       n0 + (E::kPairs ? wn / 2 : wn), m_all);
+  if constexpr (kShared)
+    pair_store<T>(acc[0][0], lds + wave / 2 * kPiece, epilogue, wave % 2, m0,
+                  n0 + wave / 2 * kMulFrag, m_all);
+  else
+    wave_store<T, false>(acc, lds + wave * kPiece, epilogue, epilogue, at.split, m0 + wm,
+                         n0 + (E::kPairs ? wn / 2 : wn), m_all);
 }
 
 // ------------------------------------------------------------ whole chunks
@@ -492,26 +526,30 @@ __global__ __launch_bounds__(kMulThreads) void product_kernel(Operand a, Operand
 constexpr int kRingTile = 256;
 constexpr uint32_t kRingSide = kRingTile * kMulDepth * 2;    // bytes of an operand's stage
 constexpr uint32_t kRingStage = 2 * kRingSide;
-constexpr int kRingLoads = 8;                                // of a thread, an operand's stage
 constexpr uint32_t kRingOut = 8192;                          // of a wave: 32 rows of 64 sums
 constexpr uint32_t kRingWgs = 256;                           // one a compute unit
+constexpr int kSlimCols = 128, kSlimStages = 4;
+constexpr uint32_t kSlimRows = kMulFrag * kMulDepth * 2;     // bytes of a's stage
+constexpr uint32_t kSlimStage = kSlimRows + kSlimCols * kMulDepth * 2;
 
-// One operand's loads, PAIR as Side's.
-template <bool FAST, int PAIR = 0>
+// One operand's loads, TILE and PAIR as Side's.
+template <bool FAST, int TILE, int PAIR = 0>
 struct RingSide {
+  static constexpr int kLoads = TILE / 32;                   // of a thread, a stage
   static constexpr int kReads = FAST ? 1 : 2;                // shared loads a fragment
   static constexpr uint32_t kNone = 0x80000000u, kAll = 0x7FFFFFF0u;
-  static constexpr uint32_t kLanes = FAST ? kMulDepth / kChunk : kRingTile / kChunk;
+  static constexpr uint32_t kLanes = FAST ? kMulDepth / kChunk : TILE / kChunk;
   static constexpr uint32_t kRows = 64 / kLanes;             // of memory, a wave's load
   u32x4 srd;                  // the descriptor of the stage to load next
   uint64_t stride;            // bytes
-  uint32_t off[kRingLoads];   // of this lane's chunk in each of its loads, or kNone
+  uint32_t off[kLoads];   // of this lane's chunk in each of its loads, or kNone
 
   // The chunk of a row that this lane loads, by the place it has in shared memory.
   static __device__ __forceinline__ uint32_t chunk_of(uint32_t wave) {
     const uint32_t lane = threadIdx.x % 64;
     if constexpr (FAST) return lane % 8 ^ (wave % 2 * 4 + lane / 16);
-    return ((lane % 32 / 4) ^ ((wave * 2 + lane / 32) & 3)) * 4 + lane % 4;
+    const uint32_t row = wave * kRows + lane / kLanes;
+    return ((lane % kLanes / 4) ^ (row & 3)) * 4 + lane % 4;
   }
 
   __device__ __forceinline__ void go_to(uint64_t base) {
@@ -528,7 +566,7 @@ struct RingSide {
     go_to(FAST ? p + first * stride + k * 2 : p + k * stride);
     const uint32_t chunk = chunk_of(wave);
 #pragma unroll
-    for (int i = 0; i < kRingLoads; ++i) {
+    for (int i = 0; i < kLoads; ++i) {
       const uint32_t r = (i * 4 + wave) * kRows + threadIdx.x % 64 / kLanes;
       if constexpr (!FAST) {
         const uint64_t c = first + chunk * kChunk;
@@ -548,7 +586,7 @@ struct RingSide {
     if constexpr (FAST) {
       const bool in = chunk_of(wave) * kChunk < left;
 #pragma unroll
-      for (int i = 0; i < kRingLoads; ++i) off[i] = in ? off[i] : kNone;
+      for (int i = 0; i < kLoads; ++i) off[i] = in ? off[i] : kNone;
     } else {
       srd[2] = static_cast<uint32_t>(left * stride);
     }
@@ -580,7 +618,7 @@ struct RingSide {
     } else {
       const uint32_t r = step * kMulStep + (lane / 32) * 8 + (lane % 16) / 4 + q * 4;
       const uint32_t c = at + (lane / 16 % 2) * 16 + lane % 4 * 4;
-      return (r * kRingTile + ((((c >> 5) ^ (r & 3)) << 5) | (c & 31))) * 2;
+      return (r * TILE + ((((c >> 5) ^ (r & 3)) << 5) | (c & 31))) * 2;
     }
   }
 
@@ -598,15 +636,15 @@ struct RingSide {
   }
 };
 
-// Load `which` of a stage's 16: a's eight, then b's.
+// Load `which` of a stage: a's, then b's.
 template <int I, typename A, typename B>
 __device__ __forceinline__ void ring_load(const A& a, const B& b, uint32_t to, int which) {
   if (which == I) {
-    if constexpr (I < kRingLoads)
+    if constexpr (I < A::kLoads)
       a.template load<I * 4096>(to, a.off[I]);
     else
-      b.template load<I * 4096>(to, b.off[I - kRingLoads]);
-  } else if constexpr (I + 1 < 2 * kRingLoads) {
+      b.template load<I * 4096>(to, b.off[I - A::kLoads]);
+  } else if constexpr (I + 1 < A::kLoads + B::kLoads) {
     ring_load<I + 1>(a, b, to, which);
   }
 }
@@ -614,11 +652,11 @@ __device__ __forceinline__ void ring_load(const A& a, const B& b, uint32_t to, i
 template <typename T, bool AF, bool BF, typename E>
 __global__ __launch_bounds__(kMulThreads, 1) void ring_kernel(Operand a, Operand b, Extents x,
                                                               E epilogue) {
-  typedef RingSide<AF> A;
-  typedef RingSide<BF, E::kPairs ? 64 : 0> B;
+  typedef RingSide<AF, kRingTile> A;
+  typedef RingSide<BF, kRingTile, E::kPairs ? 64 : 0> B;
   constexpr int kF = 4, kMul = kF * kF, kReads = kF * (A::kReads + B::kReads);
   constexpr int kSteps = kMulDepth / kMulStep;
-  static_assert(kRingSide == kRingLoads * 4096, "a workgroup's load is 4 KiB");
+  static_assert(kRingSide == A::kLoads * 4096, "a workgroup's load is 4 KiB");
   __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kRingStage + 4 * kRingOut];
   const uint32_t lds0 = static_cast<uint32_t>(
       reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)lds));
@@ -720,7 +758,7 @@ __global__ __launch_bounds__(kMulThreads, 1) void ring_kernel(Operand a, Operand
   // The first kFirst loads of a stage go between the matrix instructions of the step
   // behind the barrier, the others evenly into the two steps after it, so that the last
   // has a step left to arrive (8, 12 and 16 first: 1302, 1391 and 1318 TFLOP/s).
-  constexpr int kLoads = 2 * kRingLoads, kFirst = 12;
+  constexpr int kLoads = A::kLoads + B::kLoads, kFirst = 12;
   constexpr int kRest = (kLoads - kFirst + kSteps - 2) / (kSteps - 1);
 #pragma unroll
   for (int q = 0; q < kLoads; ++q) ring_load<0>(sa, sb, fill, q);
@@ -797,6 +835,115 @@ __global__ __launch_bounds__(kMulThreads, 1) void ring_kernel(Operand a, Operand
     if (!(whole && epilogue.simple())) __builtin_amdgcn_s_waitcnt(0x0F70);
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // nothing lands in shared memory later
+}
+
+// 32 rows of c, whole chunks: bound by how fast b comes from memory, so what counts is how
+// much of it is under way.  Tiles of 32 x 128, STAGES stages of 64 k (20 KiB), all but one
+// of them under way while that one is worked on.
+template <typename T, bool BF, int STAGES, typename E>
+__global__ __launch_bounds__(kMulThreads) void slim_kernel(Operand a, Operand b, Extents x,
+                                                           E epilogue) {
+  typedef RingSide<true, kMulFrag> A;
+  typedef RingSide<BF, kSlimCols, E::kPairs ? kMulFrag : 0> B;
+  constexpr int kSteps = kMulDepth / kMulStep, kLoads = A::kLoads + B::kLoads;
+  constexpr uint32_t kPiece = kMulFrag * 64;
+  static_assert(STAGES * kSlimStage >= 4 * kPiece * 4, "the epilogue's pieces");
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[STAGES * kSlimStage];
+  const uint32_t lds0 = static_cast<uint32_t>(
+      reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)lds));
+
+  uint64_t m_all = x.m;
+  if (x.count) {
+    const uint64_t c = *x.count;
+    const uint64_t left = c > x.first ? c - x.first : 0;
+    m_all = left < m_all ? left : m_all;
+  }
+  constexpr int kOutN = E::kPairs ? kSlimCols / 2 : kSlimCols;
+  const uint32_t tiles_m = static_cast<uint32_t>((m_all + kMulFrag - 1) / kMulFrag);
+  const uint32_t tiles_n = static_cast<uint32_t>((x.n + kOutN - 1) / kOutN);
+  const uint32_t splits = splits_of(x.splits, x.most, x.fill, tiles_m * tiles_n);
+  const uint32_t wgs = tiles_m * tiles_n * splits;
+  if (blockIdx.x >= wgs) return;
+  epilogue.cut(splits, m_all);
+  const Spot at = spot_of(blockIdx.x, wgs, tiles_m, tiles_n);
+  const uint64_t m0 = static_cast<uint64_t>(at.m) * kMulFrag;
+  const uint64_t n0 = static_cast<uint64_t>(at.n) * kOutN;
+  const uint64_t per = ((x.k + splits - 1) / splits + kMulDepth - 1) / kMulDepth * kMulDepth;
+  const uint64_t lo = at.split * per < x.k ? at.split * per : x.k;
+  const uint64_t hi = lo + per < x.k ? lo + per : x.k;
+  const uint32_t stages = static_cast<uint32_t>((hi - lo + kMulDepth - 1) / kMulDepth);
+  const uint32_t lane = threadIdx.x % 64;
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+
+  // Neighbouring tiles begin at different stages, as in the ring.
+  A sa;
+  B sb;
+  uint32_t turn = stages ? at.n % stages : 0, loaded = 0, fill = lds0 + wave * 1024;
+  const auto begin = [&]() __attribute__((always_inline)) {
+    sa.begin(a, m0, lo + turn * static_cast<uint64_t>(kMulDepth), wave);
+    sb.begin(b, n0, lo + turn * static_cast<uint64_t>(kMulDepth), wave);
+  };
+  const auto load = [&]() __attribute__((always_inline)) {
+    if (loaded >= stages) {                                  // nothing is left
+      sa.cut(0, wave);
+      sb.cut(0, wave);
+    } else if (turn + 1 == stages) {
+      const uint64_t left = hi - lo - turn * static_cast<uint64_t>(kMulDepth);
+      if (left < kMulDepth) {
+        sa.cut(static_cast<uint32_t>(left), wave);
+        sb.cut(static_cast<uint32_t>(left), wave);
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < kLoads; ++q) ring_load<0>(sa, sb, fill, q);
+    fill = fill + kSlimStage < lds0 + STAGES * kSlimStage ? fill + kSlimStage
+                                                          : lds0 + wave * 1024;
+    sa.next();
+    sb.next();
+    ++loaded;
+    if (++turn >= stages) {
+      turn = 0;
+      begin();
+    }
+  };
+  begin();
+#pragma unroll 1
+  for (int s = 0; s + 1 < STAGES; ++s) load();
+
+  f32x16 acc[1][1];
+#pragma unroll
+  for (int r = 0; r < 16; ++r) acc[0][0][r] = 0.f;
+  uint32_t stage = lds0;
+#pragma unroll 1
+  for (uint32_t s = 0; s < stages; ++s) {
+    // this wave's loads of the stage are there, and it has read the one before: so are
+    // and have, behind the barrier, all waves'
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"i"(kLoads * (STAGES - 2)) : "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    load();
+#pragma unroll
+    for (int p = 0; p < kSteps; ++p) {
+      u32x4 fa, fb;
+      A::read(stage + A::place(p, 0, 0), 0, fa);
+#pragma unroll
+      for (int h = 0; h < B::kReads; ++h)
+        B::read(stage + kSlimRows + B::place(p, wave * kMulFrag, h), h, fb);
+      acc[0][0] = mul<T>(fb, fa, acc[0][0]);
+    }
+    stage = stage + kSlimStage < lds0 + STAGES * kSlimStage ? stage + kSlimStage : lds0;
+  }
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");   // nothing lands later
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+
+  float* pieces = reinterpret_cast<float*>(lds);
+  if constexpr (E::kPairs)
+    pair_store<T>(acc[0][0], pieces + wave / 2 * kPiece, epilogue, wave % 2, m0,
+                  n0 + wave / 2 * kMulFrag, m_all);
+  else
+    wave_store<T, false>(acc, pieces + wave * kPiece, epilogue, epilogue, at.split, m0,
+                         n0 + wave * kMulFrag, m_all);
 }
 
 // Whether the ring takes an operand: whole, aligned chunks, and a tile's (k fast) or a
@@ -1039,8 +1186,8 @@ __global__ __launch_bounds__(kMulThreads) void join_kernel(Sink s, Extents x, ui
   s.finish<T>(m, n, sum);
 }
 
-// How a product is cut: the tile of c (256 x 256, 128 x 128, or 32 rows x 128; of pairs 32
-// rows x 2 x 128), the splits of k, and their most where rows are counted on the device.
+// How a product is cut: the tile of c (256 x 256, 128 x 128, or 32 rows x 128), the splits
+// of k, and their most where rows are counted on the device.
 struct MulPlan {
   int tile;
   uint32_t splits, most, fill;
@@ -1048,18 +1195,14 @@ struct MulPlan {
 };
 
 // What may be: splits at all; tiles of 32 rows (k fast in a); rows that are counted on
-// the device; pairs; operands of whole chunks (ring_takes).
+// the device; operands of whole chunks (ring_takes).
 struct MulWays {
-  bool split, few_rows, counted, pairs, whole;
+  bool split, few_rows, counted, whole;
 };
 
-inline uint64_t tile_columns(int tile, bool pairs) {
-  return tile == 256 || (tile == 32 && pairs) ? 256 : 128;
-}
-
 // The same cut over m rows of c and n columns of b.
-inline MulPlan plan_of(MulPlan p, uint64_t m, uint64_t n, bool pairs = false) {
-  const uint64_t tn = tile_columns(p.tile, pairs);
+inline MulPlan plan_of(MulPlan p, uint64_t m, uint64_t n) {
+  const uint64_t tn = p.tile == 256 ? 256 : 128;
   p.tiles_n = (n + tn - 1) / tn;
   p.tiles = (m + p.tile - 1) / p.tile * p.tiles_n;
   return p;
@@ -1069,7 +1212,7 @@ inline MulPlan plan_of(MulPlan p, uint64_t m, uint64_t n, bool pairs = false) {
 // chip holds together, as measured on MI355X: a fixed part, and one for each k, which is
 // less where fewer workgroups share a compute unit.  256 x 256: 7 + 0.026 k (14 + 0.0285 k
 // where the operands are not whole chunks); 128 x 128, two a unit: 6.7 + 0.0141 k, one:
-// 0.0075 k; 32 x 128, four a unit: 4.3 + 0.0123 k, two: 0.0075 k, one: 0.0056 k.  A join
+// 0.0075 k; 32 x 128, four a unit (two of whole chunks): 4.3 + 0.0123 k, two: 0.0075 k, one: 0.0056 k.  A join
 // costs a launch, and its partial sums' way out and back.  (4096 x 4096 over 1024, k slow:
 // 43, 55 us in 256, 128; 200 x 4096 over 1024, k fast: 35, 18, 11 us in 256, 128, 32.)
 inline MulPlan plan_product(uint64_t m, uint64_t n, uint64_t k, const MulWays& may) {
@@ -1079,9 +1222,9 @@ inline MulPlan plan_product(uint64_t m, uint64_t n, uint64_t k, const MulWays& m
   for (const int tile : {256, 128, 32}) {
     if (tile == 32 && !may.few_rows) continue;
     MulPlan p = {tile, 1, 1, 0, 0, 0};
-    p = plan_of(p, m, n, may.pairs);
-    const bool wide = tile == 32 && may.pairs;
-    const uint64_t at_once = tile == 256 ? kUnits : tile == 128 || wide ? 2 * kUnits : 4 * kUnits;
+    p = plan_of(p, m, n);
+    const uint64_t at_once = tile == 256 ? kUnits
+                             : tile == 128 || may.whole ? 2 * kUnits : 4 * kUnits;
     p.fill = static_cast<uint32_t>(at_once);
     for (const uint32_t s : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
       if (s > 1 && (!may.split || k < 256 * s)) break;
@@ -1091,7 +1234,6 @@ inline MulPlan plan_product(uint64_t m, uint64_t n, uint64_t k, const MulWays& m
       const double rounds = static_cast<double>((wgs + at_once - 1) / at_once);
       const double each = tile == 256 ? (may.whole ? 0.026 : 0.0285)
                           : tile == 128 ? (wgs > kUnits ? 0.0141 : 0.0075)
-                          : wide ? (wgs > kUnits ? 0.0123 : 0.0075)
                                  : (wgs > 2 * kUnits ? 0.0123 : wgs > kUnits ? 0.0075 : 0.0056);
       const double fix = tile == 256 ? (may.whole ? 7.0 : 14.0) : tile == 128 ? 6.7 : 4.3;
       double us = rounds * (fix + each * static_cast<double>(per));
@@ -1150,7 +1292,8 @@ hipError_t run_product(const MulPlan& p, const Operand& a, const Operand& b, Ext
   const uint64_t sa = safe_k(a, AF, x.k), sb = safe_k(b, BF, x.k, E::kPairs);
   const uint64_t safe = sa < sb ? sa : sb;
   const uint32_t grid = static_cast<uint32_t>(wgs);
-  if (p.tile == 256 && ring_takes(a, AF, x.k) && ring_takes(b, BF, x.k, E::kPairs))
+  const bool whole = ring_takes(a, AF, x.k) && ring_takes(b, BF, x.k, E::kPairs);
+  if (p.tile == 256 && whole)
     ring_kernel<T, AF, BF, E><<<grid < kRingWgs ? grid : kRingWgs, kMulThreads, 0, stream>>>(
         a, b, x, e);
   else if (p.tile == 256)
@@ -1159,12 +1302,13 @@ hipError_t run_product(const MulPlan& p, const Operand& a, const Operand& b, Ext
   else if (p.tile == 128)
     product_kernel<T, AF, BF, 128, 128, 2, 2, E>
         <<<grid, kMulThreads, 0, stream>>>(a, b, x, safe, e);
-  else if constexpr (AF && E::kPairs)
-    product_kernel<T, AF, BF, 32, 256, 1, 4, E>
-        <<<grid, kMulThreads, 0, stream>>>(a, b, x, safe, e);
-  else if constexpr (AF)
-    product_kernel<T, AF, BF, 32, 128, 1, 4, E>
-        <<<grid, kMulThreads, 0, stream>>>(a, b, x, safe, e);
+  else if constexpr (AF) {
+    if (whole)
+      slim_kernel<T, BF, kSlimStages, E><<<grid, kMulThreads, 0, stream>>>(a, b, x, e);
+    else
+      product_kernel<T, AF, BF, 32, 128, 1, 4, E>
+          <<<grid, kMulThreads, 0, stream>>>(a, b, x, safe, e);
+  }
   hipError_t err = hipGetLastError();
   if constexpr (!E::kPairs && E::kJoins) {
     if (err != hipSuccess || p.most == 1) return err;

@@ -127,7 +127,7 @@ struct Gated {
   }
 };
 
-MulWays forward_ways(uint64_t cols) { return {false, true, false, true, cols % kChunk == 0}; }
+MulWays forward_ways(uint64_t cols) { return {false, true, false, cols % kChunk == 0}; }
 
 template <typename T>
 hipError_t forward(const GatedLaunch& a, hipStream_t stream) {
@@ -188,8 +188,8 @@ GradRoom grad_room(uint64_t rows, uint64_t cols, uint64_t width) {
   r.lead = row_lead(2 * width);
   r.lead_x = row_lead(cols);
   const bool whole = (2 * width) % kChunk == 0 && cols % kChunk == 0;
-  r.plan = plan_product(rows, cols, 2 * width, {true, true, false, false, whole});
-  r.weight = plan_product(2 * width, cols, rows, {true, false, false, false, whole});
+  r.plan = plan_product(rows, cols, 2 * width, {true, true, false, whole});
+  r.weight = plan_product(2 * width, cols, rows, {true, false, false, whole});
   r.held = r.weight.tile == 256 && rows && whole;
   r.slopes = chunks_up(rows * r.lead * 2, 256);
   r.x = r.held ? chunks_up(rows * r.lead_x * 2, 256) : 0;

@@ -80,7 +80,7 @@ Room room_of(uint64_t rows, uint64_t cols, uint64_t vocab, uint32_t top, bool dx
   r.flags = take(rows);
   r.x = take(r.piece * r.lead_x * 2);
   const bool whole = cols % kChunk == 0;
-  r.logits = plan_product(r.piece, vocab, cols, {false, true, true, false, whole});
+  r.logits = plan_product(r.piece, vocab, cols, {false, true, true, whole});
   const uint64_t tiles = (vocab + (r.logits.tile == 256 ? 255 : 127)) /
                          (r.logits.tile == 256 ? 256 : 128);
   r.entries = tiles * (r.logits.tile == 32 ? 4 : 2);          // one a wave's columns
@@ -90,11 +90,11 @@ Room room_of(uint64_t rows, uint64_t cols, uint64_t vocab, uint32_t top, bool dx
   else r.ids = take(r.piece * 8);
   uint64_t partial = 0;
   if (dx) {
-    r.dx = plan_product(r.piece, cols, vocab, {true, true, true, false, whole});
+    r.dx = plan_product(r.piece, cols, vocab, {true, true, true, whole});
     partial = partial_rows(r.dx, r.piece) * r.lead_w * 4;
   }
   if (dw) {
-    r.dw = plan_product(vocab, cols, r.piece, {true, false, false, false, true});
+    r.dw = plan_product(vocab, cols, r.piece, {true, false, false, true});
     const uint64_t more = partial_rows(r.dw, vocab) * r.lead_w * 4;
     if (more > partial) partial = more;
     if (r.pieces > 1) r.sums = take(vocab * r.lead_w * 4);
