@@ -606,7 +606,7 @@ uint64_t zero_loss_workspace(uint64_t rows, uint64_t cols, uint64_t vocab, uint3
  *   d[t][v] = weights[t] (softmax(z[t])[v] - (v == y))       (rounded to dtype)
  *   dx = scale d w;  dw = scale d^T x                        (fp32 sums, one rounding)
  * The logits are never kept: for the loss alone they are not stored at all, and for
- * gradients the workspace holds those of a piece of the tokens, 4 bytes each and about 2
+ * gradients the workspace holds those of a piece of the tokens, 4 bytes each and about 6
  * GiB at most (or 256 tokens); besides, a copy of a piece's x and, if there are several
  * pieces, fp32 sums of dw.  Before its rounding d
  * is divided by the weights' largest power of two and multiplied by 2^14, which fp16's

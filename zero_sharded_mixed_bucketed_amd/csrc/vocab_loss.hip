@@ -54,8 +54,9 @@ struct Room {
 };
 
 // Bytes of a piece's logits, about (a piece has 256 tokens at least).  Larger pieces
-// add to dW's running sums less often.
-constexpr uint64_t kPieceBytes = 1ull << 31;
+// add to dW's running sums less often: 8192 tokens x 131072 words at 4096 take PPP ms in
+// two pieces and PPQ ms in one, whose workspace is no larger, as it needs no such sums.
+constexpr uint64_t kPieceBytes = 6ull << 30;
 constexpr uint64_t kMostRows = 1ull << 22;  // of a piece: a workgroup a row in one launch
 
 Room room_of(uint64_t rows, uint64_t cols, uint64_t vocab, uint32_t top, bool dx, bool dw) {
