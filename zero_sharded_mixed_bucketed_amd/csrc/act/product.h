@@ -57,7 +57,7 @@ struct Extents {
 
 // The splits of a product whose rows are counted on the device: as planned for the most
 // rows, or with fewer tiles than that what fills the chip, `fill` workgroups, but not over
-// `most`.  (1200 of 3001 tokens with a loss, 50001 words at 2050: dx 510 -> 330 us.)
+// `most`.  (1200 of 3001 tokens with a loss, 50001 words at 2050: dx 510 -> 290 us with its join.)
 __host__ __device__ inline uint32_t splits_of(uint32_t splits, uint32_t most, uint32_t fill,
                                               uint32_t tiles) {
   if (most <= splits || tiles == 0) return splits;
@@ -229,8 +229,9 @@ __device__ __forceinline__ Spot spot_of(uint32_t wg, uint32_t wgs, uint32_t tile
 // keep, which finish(row, m, piece, rows) gets in the end, `piece` being which of the
 // row's 32 FN columns these were.  stores() says whether there is anything to store.
 // simple() says whether a whole
-// tile needs none of put's checks: now(split, m0, factor) then gives what stores it,
-// factor what load_factor() gave at the kernel's begin; row_of(i, line, m) is the row at
+// tile needs none of put's checks: now<false>(split, m0, factor) then gives what stores it
+// (now<true> with E::kAdds, if adds(): what it adds to is read ahead), factor what
+// load_factor() gave at the kernel's begin; row_of(i, line, m) is the row at
 // which it stores row m, line `line` of the wave's i-th 32.
 template <typename T, bool WHOLE, int FM, int FN, typename E, typename P>
 __device__ __forceinline__ void wave_store(const f32x16 (&acc)[FM][FN], float* piece, const E& e,
@@ -251,7 +252,6 @@ __device__ __forceinline__ void wave_store(const f32x16 (&acc)[FM][FN], float* p
   [[maybe_unused]] typename P::Old old[kAhead];
   [[maybe_unused]] const auto fetch = [&](int step, uint32_t r0) __attribute__((always_inline)) {
     if constexpr (kOld) {
-      if (!to.adds()) return;
 #pragma unroll
       for (uint32_t r = r0; r < r0 + kAhead; ++r)
         old[r % kAhead] = to.fetch(m0 + step / kTurns * kMulFrag + r * kLines + lane / kLanes,
@@ -825,10 +825,15 @@ __global__ __launch_bounds__(kMulThreads, 1) void ring_kernel(Operand a, Operand
     float* piece = reinterpret_cast<float*>(lds + 2 * kRingStage + wave * kRingOut);
     const bool whole = static_cast<uint64_t>(at.m + 1) * kRingTile <= m_all &&
                        static_cast<uint64_t>(at.n + 1) * kOutN <= x.n;
-    if (whole && epilogue.simple())
-      wave_store<T, true>(acc, piece, epilogue, epilogue.now(at.split, m0, by), at.split,
-                                m0, n0, m_all);
-    else
+    if (whole && epilogue.simple()) {
+      if (E::kAdds && epilogue.adds())
+        wave_store<T, true>(acc, piece, epilogue,
+                            epilogue.template now<E::kAdds>(at.split, m0, by), at.split, m0, n0,
+                            m_all);
+      else
+        wave_store<T, true>(acc, piece, epilogue, epilogue.template now<false>(at.split, m0, by),
+                            at.split, m0, n0, m_all);
+    } else
       wave_store<T, false>(acc, piece, epilogue, epilogue, at.split, m0, n0, m_all);
     // vmcnt(0), seen by the compiler: it would wait for the epilogue's loads in every
     // turn of the next tile otherwise, and with them for the stage under way
@@ -838,17 +843,21 @@ __global__ __launch_bounds__(kMulThreads, 1) void ring_kernel(Operand a, Operand
 }
 
 // 32 rows of c, whole chunks: bound by how fast b comes from memory, so what counts is how
-// much of it is under way.  Tiles of 32 x 128, STAGES stages of 64 k (20 KiB), all but one
-// of them under way while that one is worked on.
-template <typename T, bool BF, int STAGES, typename E>
+// much of it is under way, and that its rows are not all asked from the same channels.
+// Tiles of 32 x 128, stages of 64 k (20 KiB), all but one of them under way while that one
+// is worked on; two workgroups a unit.  1 or 32 x 32768 over 4096, b in memory: 46 us, 5.8
+// TB/s, where product_kernel takes 61 and reading b in order 47; six to eight stages, one
+// workgroup a unit, are no faster.  A counted x is rows (k is not slow in a).
+template <typename T, bool BF, typename E>
 __global__ __launch_bounds__(kMulThreads) void slim_kernel(Operand a, Operand b, Extents x,
                                                            E epilogue) {
   typedef RingSide<true, kMulFrag> A;
   typedef RingSide<BF, kSlimCols, E::kPairs ? kMulFrag : 0> B;
   constexpr int kSteps = kMulDepth / kMulStep, kLoads = A::kLoads + B::kLoads;
   constexpr uint32_t kPiece = kMulFrag * 64;
-  static_assert(STAGES * kSlimStage >= 4 * kPiece * 4, "the epilogue's pieces");
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[STAGES * kSlimStage];
+  constexpr uint32_t kLds = kSlimStages * kSlimStage;
+  static_assert(kLds >= 4 * kPiece * 4, "the epilogue's pieces");
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];
   const uint32_t lds0 = static_cast<uint32_t>(
       reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)lds));
 
@@ -896,8 +905,7 @@ __global__ __launch_bounds__(kMulThreads) void slim_kernel(Operand a, Operand b,
     }
 #pragma unroll
     for (int q = 0; q < kLoads; ++q) ring_load<0>(sa, sb, fill, q);
-    fill = fill + kSlimStage < lds0 + STAGES * kSlimStage ? fill + kSlimStage
-                                                          : lds0 + wave * 1024;
+    fill = fill + kSlimStage < lds0 + kLds ? fill + kSlimStage : lds0 + wave * 1024;
     sa.next();
     sb.next();
     ++loaded;
@@ -908,7 +916,7 @@ __global__ __launch_bounds__(kMulThreads) void slim_kernel(Operand a, Operand b,
   };
   begin();
 #pragma unroll 1
-  for (int s = 0; s + 1 < STAGES; ++s) load();
+  for (int s = 0; s + 1 < kSlimStages; ++s) load();
 
   f32x16 acc[1][1];
 #pragma unroll
@@ -918,7 +926,7 @@ __global__ __launch_bounds__(kMulThreads) void slim_kernel(Operand a, Operand b,
   for (uint32_t s = 0; s < stages; ++s) {
     // this wave's loads of the stage are there, and it has read the one before: so are
     // and have, behind the barrier, all waves'
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"i"(kLoads * (STAGES - 2)) : "memory");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"i"(kLoads * (kSlimStages - 2)) : "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
     load();
@@ -931,7 +939,7 @@ __global__ __launch_bounds__(kMulThreads) void slim_kernel(Operand a, Operand b,
         B::read(stage + kSlimRows + B::place(p, wave * kMulFrag, h), h, fb);
       acc[0][0] = mul<T>(fb, fa, acc[0][0]);
     }
-    stage = stage + kSlimStage < lds0 + STAGES * kSlimStage ? stage + kSlimStage : lds0;
+    stage = stage + kSlimStage < lds0 + kLds ? stage + kSlimStage : lds0;
   }
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");   // nothing lands later
   __builtin_amdgcn_s_barrier();
@@ -961,7 +969,7 @@ inline bool ring_takes(const Operand& o, bool fast, uint64_t k, bool pairs = fal
 // join_kernel), running sums over several products, or the result itself, scaled and
 // rounded once.
 struct Sink {
-  static constexpr bool kPairs = false, kRows = false, kJoins = true;
+  static constexpr bool kPairs = false, kRows = false, kJoins = true, kAdds = true;
   void* out;
   uint64_t stride;
   int dtype, accumulate;   // kF16, kBf16 or kF32
@@ -1043,14 +1051,15 @@ struct Sink {
 
   // What is stored, and what is added to it: old running sums before the factor, or an old
   // result after it.
+  template <bool OLD>
   struct Now {
-    static constexpr bool kOld = true;
+    static constexpr bool kOld = OLD;
     struct Old {
       u32x4 a, b;
     };
     uint8_t* out;
     uint64_t stride;        // bytes, as all here
-    const uint8_t* old;     // or nullptr
+    const uint8_t* old;
     uint64_t old_stride;
     bool wide, old_wide, old_first;   // fp32
     float factor;
@@ -1063,8 +1072,6 @@ struct Sink {
                                                                 static_cast<int>(rows[i])));
     }
 
-    __device__ __forceinline__ bool adds() const { return old != nullptr; }
-
     __device__ __forceinline__ Old fetch(uint64_t m, uint64_t n) const {
       const uint8_t* p = old + m * old_stride + n * (old_wide ? 4 : 2);
       Old o;
@@ -1075,17 +1082,17 @@ struct Sink {
 
     template <typename T>
     __device__ __forceinline__ void put(uint64_t m, uint64_t n, float (&x)[8], Old o) const {
-      float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (old) {
-        if (old_wide) {
+      float y[8];
+      forget(o.b);            // arrived in any case: no wait is left for the next tile
+      if (old_wide) {
+        const f32x4 u = __builtin_bit_cast(f32x4, o.a), v = __builtin_bit_cast(f32x4, o.b);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            y[i] = __builtin_bit_cast(float, o.a[i]);
-            y[4 + i] = __builtin_bit_cast(float, o.b[i]);
-          }
-        } else {
-          unpack8<T>(o.a, y);
+        for (int i = 0; i < 4; ++i) {
+          y[i] = u[i];
+          y[4 + i] = v[i];
         }
+      } else {
+        unpack8<T>(o.a, y);
       }
       if (old_first) {
 #pragma unroll
@@ -1094,6 +1101,19 @@ struct Sink {
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = x[i] * factor + y[i];
       }
+      store<T>(m, n, x);
+    }
+
+    template <typename T>
+    __device__ __forceinline__ void put(uint32_t, uint64_t m, uint64_t n, uint64_t,
+                                        float (&x)[8]) const {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] *= factor;
+      store<T>(m, n, x);
+    }
+
+    template <typename T>
+    __device__ __forceinline__ void store(uint64_t m, uint64_t n, const float (&x)[8]) const {
       if (wide) {
         f32x4_at4* w = reinterpret_cast<f32x4_at4*>(out + m * stride + n * 4);
         w[0] = f32x4{x[0], x[1], x[2], x[3]};
@@ -1111,8 +1131,13 @@ struct Sink {
                   : 1.0f;
   }
 
-  __device__ __forceinline__ Now now(uint32_t split, uint64_t m0, float by) const {
-    Now n = {};
+  __device__ __forceinline__ bool adds() const {
+    return !partial && (sums ? add != 0 : accumulate != 0);
+  }
+
+  template <bool OLD>
+  __device__ __forceinline__ Now<OLD> now(uint32_t split, uint64_t m0, float by) const {
+    Now<OLD> n = {};
     if (partial || (sums && !last)) {
       n.out = reinterpret_cast<uint8_t*>(partial ? partial + split * split_size : sums);
       n.stride = lead * 4;
@@ -1125,11 +1150,11 @@ struct Sink {
       n.factor = by;
       n.mapped = rows != nullptr;
     }
-    if (!partial && sums && add) {
+    if (OLD && sums) {
       n.old = reinterpret_cast<const uint8_t*>(sums);
       n.old_stride = lead * 4;
       n.old_wide = n.old_first = true;
-    } else if (!partial && !sums && accumulate) {
+    } else if (OLD) {
       n.old = n.out;
       n.old_stride = n.stride;
       n.old_wide = n.wide;
@@ -1304,7 +1329,7 @@ hipError_t run_product(const MulPlan& p, const Operand& a, const Operand& b, Ext
         <<<grid, kMulThreads, 0, stream>>>(a, b, x, safe, e);
   else if constexpr (AF) {
     if (whole)
-      slim_kernel<T, BF, kSlimStages, E><<<grid, kMulThreads, 0, stream>>>(a, b, x, e);
+      slim_kernel<T, BF, E><<<grid, kMulThreads, 0, stream>>>(a, b, x, e);
     else
       product_kernel<T, AF, BF, 32, 128, 1, 4, E>
           <<<grid, kMulThreads, 0, stream>>>(a, b, x, safe, e);

@@ -78,7 +78,7 @@ __device__ __forceinline__ void slopes8(int act, const float (&g)[8], float (&a)
 
 // The forward's epilogue: both sums of a column to a, and their checkpoints.
 struct Gated {
-  static constexpr bool kPairs = true, kRows = false, kJoins = false;
+  static constexpr bool kPairs = true, kRows = false, kJoins = false, kAdds = false;
   Rows out;
   Ckpt c_gate, c_up, c_out;
   uint64_t cols;
@@ -93,6 +93,8 @@ struct Gated {
   __device__ __forceinline__ bool simple() const { return false; }
   __device__ __forceinline__ float load_factor() const { return 1.0f; }
   __device__ __forceinline__ uint64_t row_of(int, uint32_t, uint64_t m) const { return m; }
+  __device__ __forceinline__ bool adds() const { return false; }
+  template <bool>
   __device__ __forceinline__ const Gated& now(uint32_t, uint64_t, float) const { return *this; }
 
   template <typename T>
@@ -180,7 +182,7 @@ struct GradRoom {
 };
 
 // dw takes x^ in 16 bits first where its product fills the chip with whole 256 x 256 tiles:
-// 8192 tokens, 4096 -> 2 x 16384 takes 1.70 + 0.04 ms where the product straight from the
+// 8192 tokens, 4096 -> 2 x 16384 takes 1.96 + 0.02 ms where the product straight from the
 // 8-bit codes, beside their arithmetic, takes 2.20; with fewer tiles, or columns that are
 // not in whole chunks, the latter's splits and edges are better.
 GradRoom grad_room(uint64_t rows, uint64_t cols, uint64_t width) {

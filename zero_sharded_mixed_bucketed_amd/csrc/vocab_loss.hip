@@ -54,8 +54,8 @@ struct Room {
 };
 
 // Bytes of a piece's logits, about (a piece has 256 tokens at least).  Larger pieces
-// add to dW's running sums less often: 8192 tokens x 131072 words at 4096 take PPP ms in
-// two pieces and PPQ ms in one, whose workspace is no larger, as it needs no such sums.
+// add to dW's running sums less often: 8192 tokens x 131072 words at 4096 take 22.4 ms
+// in two pieces and 22.1 in one, whose workspace is no larger, as it needs no such sums.
 constexpr uint64_t kPieceBytes = 6ull << 30;
 constexpr uint64_t kMostRows = 1ull << 22;  // of a piece: a workgroup a row in one launch
 
@@ -203,10 +203,10 @@ struct Part {
 
 // A piece's logits, scaled: the maximum and sum of each wave's columns of a row, from the
 // fp32 sums where they are (a row is then read once less: 4096 x 131072 words, 1060 ->
-// 590 us), and what is wanted of the logits themselves: all (those past the vocabulary
+// 690 us for the pass over them), and what is wanted of the logits themselves: all (those past the vocabulary
 // are -infinity up to `wide`), or each row's target's.
 struct Logits {
-  static constexpr bool kPairs = false, kRows = true, kJoins = false, kOld = false;
+  static constexpr bool kPairs = false, kRows = true, kJoins = false, kOld = false, kAdds = false;
   struct Old {};
   float* z;                 // or nullptr
   uint64_t lead, wide, vocab;
@@ -282,6 +282,8 @@ struct Logits {
     }
   };
 
+  __device__ __forceinline__ bool adds() const { return false; }
+  template <bool>
   __device__ __forceinline__ Now now(uint32_t, uint64_t, float) const { return {z, lead, scale}; }
 
   template <typename T>
