@@ -53,7 +53,14 @@ struct Extents {
   const uint32_t* count;
   uint64_t first;
   int count_k;
+  uint32_t twice;           // 1: each that is counted stands twice
 };
+
+__device__ __forceinline__ uint64_t counted(const Extents& x, uint64_t most) {
+  const uint64_t c = *x.count;
+  const uint64_t left = (c > x.first ? c - x.first : 0) << x.twice;
+  return left < most ? left : most;
+}
 
 // The splits of a product whose rows are counted on the device: as planned for the most
 // rows, or with fewer tiles than that what fills the chip, `fill` workgroups, but not over
@@ -369,10 +376,8 @@ __global__ __launch_bounds__(kMulThreads) void product_kernel(Operand a, Operand
 
   uint64_t m_all = x.m, k_all = x.k;
   if (x.count) {
-    const uint64_t c = *x.count;
-    const uint64_t left = c > x.first ? c - x.first : 0;
     uint64_t& of = x.count_k ? k_all : m_all;
-    of = left < of ? left : of;
+    of = counted(x, of);
   }
   const uint32_t tiles_m = static_cast<uint32_t>((m_all + TM - 1) / TM);
   constexpr int kOutN = E::kPairs ? TN / 2 : TN;            // columns of c a tile
@@ -664,10 +669,8 @@ __global__ __launch_bounds__(kMulThreads, 1) void ring_kernel(Operand a, Operand
   const float by = epilogue.load_factor();
   uint64_t m_all = x.m, k_all = x.k;
   if (x.count) {
-    const uint64_t c = *x.count;
-    const uint64_t left = c > x.first ? c - x.first : 0;
     uint64_t& of = x.count_k ? k_all : m_all;
-    of = left < of ? left : of;
+    of = counted(x, of);
   }
   constexpr int kOutN = E::kPairs ? kRingTile / 2 : kRingTile;
   const uint32_t tiles_m = static_cast<uint32_t>((m_all + kRingTile - 1) / kRingTile);
@@ -861,12 +864,7 @@ __global__ __launch_bounds__(kMulThreads) void slim_kernel(Operand a, Operand b,
   const uint32_t lds0 = static_cast<uint32_t>(
       reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)lds));
 
-  uint64_t m_all = x.m;
-  if (x.count) {
-    const uint64_t c = *x.count;
-    const uint64_t left = c > x.first ? c - x.first : 0;
-    m_all = left < m_all ? left : m_all;
-  }
+  const uint64_t m_all = x.count ? counted(x, x.m) : x.m;
   constexpr int kOutN = E::kPairs ? kSlimCols / 2 : kSlimCols;
   const uint32_t tiles_m = static_cast<uint32_t>((m_all + kMulFrag - 1) / kMulFrag);
   const uint32_t tiles_n = static_cast<uint32_t>((x.n + kOutN - 1) / kOutN);
@@ -881,7 +879,7 @@ __global__ __launch_bounds__(kMulThreads) void slim_kernel(Operand a, Operand b,
   const uint64_t lo = at.split * per < x.k ? at.split * per : x.k;
   const uint64_t hi = lo + per < x.k ? lo + per : x.k;
   const uint32_t stages = static_cast<uint32_t>((hi - lo + kMulDepth - 1) / kMulDepth);
-  const uint32_t lane = threadIdx.x % 64;
+  const uint32_t tail = static_cast<uint32_t>(hi - lo) - (stages - 1) * kMulDepth;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
 
   // Neighbouring tiles begin at different stages, as in the ring.
@@ -893,15 +891,10 @@ __global__ __launch_bounds__(kMulThreads) void slim_kernel(Operand a, Operand b,
     sb.begin(b, n0, lo + turn * static_cast<uint64_t>(kMulDepth), wave);
   };
   const auto load = [&]() __attribute__((always_inline)) {
-    if (loaded >= stages) {                                  // nothing is left
-      sa.cut(0, wave);
-      sb.cut(0, wave);
-    } else if (turn + 1 == stages) {
-      const uint64_t left = hi - lo - turn * static_cast<uint64_t>(kMulDepth);
-      if (left < kMulDepth) {
-        sa.cut(static_cast<uint32_t>(left), wave);
-        sb.cut(static_cast<uint32_t>(left), wave);
-      }
+    const uint32_t some = loaded >= stages ? 0 : turn + 1 == stages ? tail : kMulDepth;
+    if (some < kMulDepth) {
+      sa.cut(some, wave);
+      sb.cut(some, wave);
     }
 #pragma unroll
     for (int q = 0; q < kLoads; ++q) ring_load<0>(sa, sb, fill, q);
@@ -981,6 +974,7 @@ struct Sink {
   float* sums;             // [rows][lead] running sums, or nullptr
   int add, last;           // add what `sums` holds; the result is final
   uint64_t lead;           // cols, rounded up to a chunk
+  uint32_t twice;          // 1: a result's row is the sum of two neighbouring rows of c
 
   template <typename T>
   __device__ __forceinline__ void finish(uint64_t m, uint64_t n, float (&x)[8]) const {
@@ -1039,7 +1033,7 @@ struct Sink {
   struct Old {};
 
   __device__ __forceinline__ void cut(uint32_t splits, uint64_t m_all) {
-    if (splits == 1) partial = nullptr;
+    if (splits == 1 && !twice) partial = nullptr;
     split_size = m_all * lead;
   }
 
@@ -1182,30 +1176,41 @@ struct Sink {
   }
 };
 
-// Adds the splits' partial sums in their order, eight neighbouring columns a thread.
+// Adds the splits' partial sums, and those of rows that stand twice, in their order, eight neighbouring columns a thread.
 template <typename T>
 __global__ __launch_bounds__(kMulThreads) void join_kernel(Sink s, Extents x, uint32_t tile_m,
                                                            uint32_t tiles_n) {
-  uint64_t m_all = x.m;
-  if (x.count && !x.count_k) {
-    const uint64_t c = *x.count;
-    const uint64_t left = c > x.first ? c - x.first : 0;
-    m_all = left < m_all ? left : m_all;
-  }
+  const uint64_t m_all = x.count && !x.count_k ? counted(x, x.m) : x.m;
   const uint32_t tiles = static_cast<uint32_t>((m_all + tile_m - 1) / tile_m) * tiles_n;
   const uint32_t splits = splits_of(x.splits, x.most, x.fill, tiles);
-  if (splits == 1) return;
+  if (splits == 1 && !s.twice) return;
   s.cut(splits, m_all);
   const uint64_t per_row = s.lead / kChunk;
   const uint64_t id = static_cast<uint64_t>(blockIdx.x) * kMulThreads + threadIdx.x;
   const uint64_t m = id / per_row, n = id % per_row * kChunk;
-  if (m >= m_all) return;
+  if (m >= m_all >> s.twice) return;
   f32x4 u = {0.f, 0.f, 0.f, 0.f}, v = u;
-  const float* p = s.partial + m * s.lead + n;
-#pragma unroll 8
-  for (uint32_t i = 0; i < splits; ++i, p += s.split_size) {
-    u += *reinterpret_cast<const f32x4*>(p);
-    v += *reinterpret_cast<const f32x4*>(p + 4);
+  const float* from = s.partial + (m << s.twice) * s.lead + n;
+  // sixteen sums' loads under way together, however many there are
+  constexpr uint32_t kAhead = 16;
+  const uint32_t all = splits << s.twice;
+#pragma unroll 1
+  for (uint32_t i0 = 0; i0 < all; i0 += kAhead) {
+    f32x4 a[kAhead], b[kAhead];
+#pragma unroll
+    for (uint32_t j = 0; j < kAhead; ++j) {
+      const uint32_t i = i0 + j;
+      a[j] = b[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (i >= all) continue;
+      const float* p = from + (i >> s.twice) * s.split_size + (i & s.twice) * s.lead;
+      a[j] = *reinterpret_cast<const f32x4*>(p);
+      b[j] = *reinterpret_cast<const f32x4*>(p + 4);
+    }
+#pragma unroll
+    for (uint32_t j = 0; j < kAhead; ++j) {
+      u += a[j];
+      v += b[j];
+    }
   }
   float sum[8] = {u[0], u[1], u[2], u[3], v[0], v[1], v[2], v[3]};
   s.finish<T>(m, n, sum);
@@ -1336,7 +1341,7 @@ hipError_t run_product(const MulPlan& p, const Operand& a, const Operand& b, Ext
   }
   hipError_t err = hipGetLastError();
   if constexpr (!E::kPairs && E::kJoins) {
-    if (err != hipSuccess || p.most == 1) return err;
+    if (err != hipSuccess || (p.most == 1 && !e.twice)) return err;
     const uint64_t joins = (x.m * (e.lead / kChunk) + kMulThreads - 1) / kMulThreads;
     join_kernel<T><<<static_cast<uint32_t>(joins), kMulThreads, 0, stream>>>(
         e, x, static_cast<uint32_t>(p.tile), static_cast<uint32_t>(p.tiles_n));

@@ -49,6 +49,7 @@ struct Room {
   uint64_t lead_x, lead_z, lead_w;
   uint64_t wide;            // columns of a row of logits: whole chunks, and -infinity
   uint64_t entries;         // of a row: maxima and sums of parts of it
+  uint32_t twice;           // see kFewRows
   uint64_t rows, slots, flags, x, z, stats, ids, sums, partial, bytes;
   MulPlan logits, dx, dw;
 };
@@ -57,6 +58,13 @@ struct Room {
 // add to dW's running sums less often: 8192 tokens x 131072 words at 4096 take 22.4 ms
 // in two pieces and 22.1 in one, whose workspace is no larger, as it needs no such sums.
 constexpr uint64_t kPieceBytes = 6ull << 30;
+// Of few tokens, g's entries keep what their rounding leaves out: of a few values that hold
+// nearly all of a gradient, roundings do not average out.  A token's row of g stands twice,
+// rounded and with those rests, and so does its x; the products are bound by W's memory
+// there (14 tokens x 43264 words at 128, three entries each: relative errors of dx and dw
+// in fp16 3.3e-4 -> 2.1e-4, their own rounding's; 64 tokens x 131072 words at 4096 take 878
+// us, 65 take 840).
+constexpr uint64_t kFewRows = 64;
 constexpr uint64_t kMostRows = 1ull << 22;  // of a piece: a workgroup a row in one launch
 
 Room room_of(uint64_t rows, uint64_t cols, uint64_t vocab, uint32_t top, bool dx, bool dw) {
@@ -79,7 +87,9 @@ Room room_of(uint64_t rows, uint64_t cols, uint64_t vocab, uint32_t top, bool dx
   r.rows = take(rows * 4);
   r.slots = take(rows * 4);
   r.flags = take(rows);
-  r.x = take(r.piece * r.lead_x * 2);
+  r.twice = (dx || dw) && rows <= kFewRows;
+  const uint64_t tokens = r.piece << r.twice;
+  r.x = take(tokens * r.lead_x * 2);
   const bool whole = cols % kChunk == 0;
   r.logits = plan_product(r.piece, vocab, cols, {false, true, true, whole});
   const uint64_t tiles = (vocab + (r.logits.tile == 256 ? 255 : 127)) /
@@ -91,11 +101,13 @@ Room room_of(uint64_t rows, uint64_t cols, uint64_t vocab, uint32_t top, bool dx
   else r.ids = take(r.piece * 8);
   uint64_t partial = 0;
   if (dx) {
-    r.dx = plan_product(r.piece, cols, vocab, {true, true, true, whole});
-    partial = partial_rows(r.dx, r.piece) * r.lead_w * 4;
+    r.dx = plan_product(tokens, cols, vocab, {true, true, true, whole});
+    uint64_t partials = partial_rows(r.dx, tokens);
+    if (r.twice && partials < tokens) partials = tokens;
+    partial = partials * r.lead_w * 4;
   }
   if (dw) {
-    r.dw = plan_product(vocab, cols, r.piece, {true, false, false, true});
+    r.dw = plan_product(vocab, cols, tokens, {true, false, false, true});
     const uint64_t more = partial_rows(r.dw, vocab) * r.lead_w * 4;
     if (more > partial) partial = more;
     if (r.pieces > 1) r.sums = take(vocab * r.lead_w * 4);
@@ -171,7 +183,7 @@ __global__ __launch_bounds__(kPickThreads) void loss_pick_kernel(VocabLaunch a,
 __global__ __launch_bounds__(256) void loss_rows_kernel(VocabLaunch a, const uint32_t* slots,
                                                         uint64_t first, uint64_t most,
                                                         uint16_t* to, uint64_t lead,
-                                                        int32_t* ids) {
+                                                        uint32_t twice, int32_t* ids) {
   const uint64_t t = static_cast<uint64_t>(blockIdx.x) * 4 + threadIdx.x / 64;
   if (t >= a.rows) return;
   const uint32_t slot = __builtin_amdgcn_readfirstlane(slots[t]);
@@ -190,9 +202,12 @@ __global__ __launch_bounds__(256) void loss_rows_kernel(VocabLaunch a, const uin
     ids[slot - first] = id < static_cast<int64_t>(a.vocab) ? static_cast<int32_t>(id) : -1;
   }
   const uint16_t* from = a.x.p + t * a.x.stride;
-  for (uint64_t c = c0; c < lead; c += 512)
-    *reinterpret_cast<u32x4*>(to + (slot - first) * lead + c) =
-        c < a.cols ? load8(from, c, a.cols) : u32x4{0, 0, 0, 0};
+  uint16_t* row = to + ((slot - first) << twice) * lead;
+  for (uint64_t c = c0; c < lead; c += 512) {
+    const u32x4 w = c < a.cols ? load8(from, c, a.cols) : u32x4{0, 0, 0, 0};
+    *reinterpret_cast<u32x4*>(row + c) = w;
+    if (twice) *reinterpret_cast<u32x4*>(row + lead + c) = w;
+  }
 }
 
 __device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
@@ -329,11 +344,13 @@ __device__ __forceinline__ float teacher_at(const VocabLaunch& a, uint64_t t, ui
 }
 
 // One row a workgroup: its maximum and sum from its parts, its loss, and (GRAD) g in place
-// of its logits, 16 bits from the row's begin on.
+// of its logits, 16 bits from the row's begin on (and with `twice` the rests of its entries
+// in the second half).
 template <typename T, bool GRAD>
 __global__ __launch_bounds__(kRowThreads) void loss_row_kernel(
     VocabLaunch a, const Head* head, const uint32_t* rows, uint64_t first, const Part* parts,
-    uint64_t entries, const float* caught, float* z_all, uint64_t lead, uint64_t wide) {
+    uint64_t entries, const float* caught, float* z_all, uint64_t lead, uint64_t wide,
+    uint32_t twice) {
   __shared__ float room[kRowThreads / 64];
   __shared__ int32_t ids[kMaxTop];
   __shared__ float shares[kMaxTop];
@@ -459,13 +476,22 @@ __global__ __launch_bounds__(kRowThreads) void loss_row_kernel(
       }
       if (c < wide) *reinterpret_cast<u32x4*>(g + c) = pack8<T>(x);
     }
+    if (twice) {
+      __syncthreads();                                  // all logits are read
+      for (uint64_t c = tid * kChunk; c < wide; c += kStep)
+        *reinterpret_cast<u32x4*>(g + lead + c) = u32x4{0, 0, 0, 0};
+    }
     __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
       const uint32_t j = tid + i * kRowThreads;
-      if (j < some && ids[j] >= 0 && ids[j] < static_cast<int64_t>(a.vocab))
-        g[ids[j]] = static_cast<uint16_t>(pack16<T>(own[i], 0.0f));
+      if (j >= some || ids[j] < 0 || ids[j] >= static_cast<int64_t>(a.vocab)) continue;
+      const uint16_t near = static_cast<uint16_t>(pack16<T>(own[i], 0.0f));
+      g[ids[j]] = near;
+      if (!twice) continue;
+      const float rest = own[i] - lo16<T>(near);
+      g[lead + ids[j]] = static_cast<uint16_t>(pack16<T>(rest == rest ? rest : 0.0f, 0.0f));
     }
   }
 }
@@ -498,15 +524,17 @@ hipError_t run_loss(const VocabLaunch& a, hipStream_t stream) {
   for (uint64_t p = 0; p < r.pieces; ++p) {
     const uint64_t first = p * r.piece;
     const uint64_t most = a.rows - first < r.piece ? a.rows - first : r.piece;
-    const Operand xs = {x, r.lead_x, most, true};
+    const uint64_t tokens = most << r.twice;
+    const Operand xs = {x, r.lead_x << r.twice, most, true};
     const Operand w_rows = {a.w.p, a.w.stride, a.vocab, false};
     const Operand w_cols = {a.w.p, a.w.stride, a.cols, false};
-    const uint64_t lead_g = 2 * r.lead_z;
+    const uint64_t lead_g = r.twice ? r.lead_z : 2 * r.lead_z;
     const uint16_t* g = reinterpret_cast<const uint16_t*>(z);
     if (a.rows) {
-      loss_rows_kernel<<<waves, 256, 0, stream>>>(a, slots, first, most, x, r.lead_x, ids);
+      loss_rows_kernel<<<waves, 256, 0, stream>>>(a, slots, first, most, x, r.lead_x, r.twice,
+                                                   ids);
       if ((e = hipGetLastError()) != hipSuccess) return e;
-      const Extents ex = {most, a.vocab, a.cols, 1, 1, 0, &head->count, first, 0};
+      const Extents ex = {most, a.vocab, a.cols, 1, 1, 0, &head->count, first, 0, 0};
       const Logits logits = {z, r.lead_z, r.wide, a.vocab, 1.0f / a.tau, parts, r.entries, ids,
                              caught};
       e = run_product<T, true, true>(plan_of(r.logits, most, a.vocab), xs, w_rows, ex, logits,
@@ -515,15 +543,15 @@ hipError_t run_loss(const VocabLaunch& a, hipStream_t stream) {
       const uint32_t grid = static_cast<uint32_t>(most);
       if (dx || dw)
         loss_row_kernel<T, true><<<grid, kRowThreads, 0, stream>>>(
-            a, head, rows, first, parts, r.entries, caught, z, r.lead_z, r.wide);
+            a, head, rows, first, parts, r.entries, caught, z, r.lead_z, r.wide, r.twice);
       else
         loss_row_kernel<T, false><<<grid, kRowThreads, 0, stream>>>(
-            a, head, rows, first, parts, r.entries, caught, z, r.lead_z, r.wide);
+            a, head, rows, first, parts, r.entries, caught, z, r.lead_z, r.wide, r.twice);
       if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     if (dx && a.rows) {
-      const Operand d = {g, lead_g, most, true};
-      const Extents ex = {most, a.cols, a.vocab, 1, 1, 0, &head->count, first, 0};
+      const Operand d = {g, lead_g, tokens, true};
+      const Extents ex = {tokens, a.cols, a.vocab, 1, 1, 0, &head->count, first, 0, r.twice};
       Sink s = {};
       s.out = a.dx.p;
       s.stride = a.dx.stride;
@@ -533,12 +561,14 @@ hipError_t run_loss(const VocabLaunch& a, hipStream_t stream) {
       s.factor = &head->unit;
       s.lead = r.lead_w;
       s.partial = partial;
-      e = run_product<T, true, false>(plan_of(r.dx, most, a.cols), d, w_cols, ex, s, stream);
+      s.twice = r.twice;
+      e = run_product<T, true, false>(plan_of(r.dx, tokens, a.cols), d, w_cols, ex, s, stream);
       if (e != hipSuccess) return e;
     }
     if (dw) {
       const Operand d = {g, lead_g, a.vocab, true}, xc = {x, r.lead_x, a.cols, true};
-      const Extents ex = {a.vocab, a.cols, most, 1, 1, 0, a.rows ? &head->count : nullptr, first, 1};
+      const Extents ex = {a.vocab, a.cols, tokens, 1, 1, 0, a.rows ? &head->count : nullptr, first,
+                          1, r.twice};
       Sink s = {};
       s.out = a.dw;
       s.stride = a.dw_stride;
