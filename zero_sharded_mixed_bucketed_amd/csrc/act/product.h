@@ -607,6 +607,12 @@ struct RingSide {
                  : "memory", "scc", "m0");
   }
 
+  // The descriptor in scalar registers, whatever the compiler made of it.
+  __device__ __forceinline__ void settle() {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) srd[i] = __builtin_amdgcn_readfirstlane(srd[i]);
+  }
+
   __device__ __forceinline__ void next() {
     go_to((static_cast<uint64_t>(srd[1]) << 32 | srd[0]) +
           (FAST ? kMulDepth * 2 : kMulDepth * stride));
@@ -688,7 +694,7 @@ __global__ __launch_bounds__(kMulThreads, 1) void ring_kernel(Operand a, Operand
   A sa;
   B sb;
   uint32_t id = blockIdx.x;
-  int64_t left = 0, rest = 0;
+  int32_t left = 0, rest = 0;      // k is at most 2^25
   uint64_t load_m = 0, load_n = 0, load_k = 0;
   const uint32_t fill0 = lds0 + wave * 1024;
   uint32_t fill = fill0;
@@ -701,8 +707,8 @@ __global__ __launch_bounds__(kMulThreads, 1) void ring_kernel(Operand a, Operand
     // caches, which all tiles would ask together (4096 x 131072 over 4096: 1264 -> 1335
     // TFLOP/s with k fast, 1279 -> 1287 with k slow).
     const uint32_t stages = static_cast<uint32_t>((hi - lo + kMulDepth - 1) / kMulDepth);
-    rest = stages ? static_cast<int64_t>((at.m + at.n) % 8 % stages) * kMulDepth : 0;
-    left = static_cast<int64_t>(hi - lo) - rest;
+    rest = stages ? static_cast<int32_t>((at.m + at.n) % 8 % stages) * kMulDepth : 0;
+    left = static_cast<int32_t>(hi - lo) - rest;
     load_m = static_cast<uint64_t>(at.m) * kRingTile;
     load_n = static_cast<uint64_t>(at.n) * kOutN;
     load_k = lo;
@@ -896,6 +902,8 @@ __global__ __launch_bounds__(kMulThreads) void slim_kernel(Operand a, Operand b,
       sa.cut(some, wave);
       sb.cut(some, wave);
     }
+    sa.settle();
+    sb.settle();
 #pragma unroll
     for (int q = 0; q < kLoads; ++q) ring_load<0>(sa, sb, fill, q);
     fill = fill + kSlimStage < lds0 + kLds ? fill + kSlimStage : lds0 + wave * 1024;
