@@ -611,7 +611,8 @@ uint64_t zero_loss_workspace(uint64_t rows, uint64_t cols, uint64_t vocab, uint3
  * pieces, fp32 sums of dw.  Of up to 64 rows, what the rounding of d leaves out at the
  * targets is kept beside it (16 bits more).  Before its rounding d
  * is divided by the weights' largest power of two and multiplied by 2^14, which fp16's
- * range asks for, and the products multiplied back.
+ * range asks for, and the products multiplied back.  A weight that is not finite makes
+ * its own row's results so, and the dw that it is summed into.
  * A row whose target is negative or whose weight is 0 is left out: its loss and dx are
  * 0, and nothing of it is read into another's result.  A target of vocab or more makes
  * the row's loss NaN and its gradients with it.  targets: id_bytes (4 or 8) wide signed

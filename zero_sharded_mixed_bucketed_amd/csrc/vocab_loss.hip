@@ -32,9 +32,10 @@ constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kLowest = -3.402823466e38f;
 constexpr int kPickThreads = 1024, kRowThreads = 512;
 
-// fp16 holds g as 2^14 g / 2^e, e the least with all weights at most 2^e: |g| 2^-e <= 1
-// leaves the probabilities 28 binary places above its smallest normal value.  bf16
-// needs no such factor and takes the same.
+// fp16 holds g as 2^14 g / 2^e, e the least with all finite weights at most 2^e: |g| 2^-e
+// <= 1 leaves the probabilities 28 binary places above its smallest normal value.  bf16
+// needs no such factor and takes the same.  Weights that are not finite make their own
+// rows so, and have no part in e: they would take the others' range away.
 constexpr int kGradBits = 14;
 
 struct Head {
@@ -133,7 +134,7 @@ __global__ __launch_bounds__(256) void loss_flags_kernel(VocabLaunch a, uint8_t*
 }
 
 // The tokens that have a loss, in their order; each token's place among them; the
-// largest weight's power of two.  One workgroup.
+// largest finite weight's power of two.  One workgroup.
 __global__ __launch_bounds__(kPickThreads) void loss_pick_kernel(VocabLaunch a,
                                                                  const uint8_t* flags,
                                                                  uint32_t* rows, uint32_t* slots,
@@ -149,7 +150,7 @@ __global__ __launch_bounds__(kPickThreads) void loss_pick_kernel(VocabLaunch a,
     if (in && a.weights) {
       const float w = a.weights[t];
       in = w != 0.0f;                                   // NaN is a weight
-      top = fabsf(w) > top || w != w ? fabsf(w) : top;
+      if (fabsf(w) < INFINITY) top = fmaxf(top, fabsf(w));
     }
     const uint64_t votes = __builtin_amdgcn_ballot_w64(in);
     if (lane == 0) counts[wave] = __popcll(votes);
@@ -169,9 +170,9 @@ __global__ __launch_bounds__(kPickThreads) void loss_pick_kernel(VocabLaunch a,
   if (threadIdx.x) return;
   for (uint32_t i = 1; i < kPickThreads / 64; ++i) top = fmaxf(top, tops[i]);
   int e = 0;
-  if (a.weights && top > 0.0f && top < INFINITY) {
-    frexpf(top, &e);                                    // top < 2^e
-    e = e < -100 ? -100 : e > 100 ? 100 : e;
+  if (a.weights && top > 0.0f) {
+    frexpf(top, &e);                                    // top < 2^e, e at most 128
+    e = e < -110 ? -110 : e;                            // 2^(14 - e) is finite
   }
   head->count = before;
   head->held = ldexpf(1.0f, kGradBits - e);
