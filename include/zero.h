@@ -608,8 +608,10 @@ uint64_t zero_loss_workspace(uint64_t rows, uint64_t cols, uint64_t vocab, uint3
  * The logits are never kept: for the loss alone they are not stored at all, and for
  * gradients the workspace holds those of a piece of the tokens, 4 bytes each and about 6
  * GiB at most (or 256 tokens); besides, a copy of a piece's x and, if there are several
- * pieces, fp32 sums of dw.  Of up to 64 rows, what the rounding of d leaves out at the
- * targets is kept beside it (16 bits more).  Before its rounding d
+ * pieces, fp32 sums of dw.  Of up to 64 rows with a loss, among however many, what the
+ * rounding of d leaves out at the targets is kept beside it (16 bits more): a few values
+ * hold nearly all of d, and the fewer they are, the further may their roundings be off
+ * together.  Before its rounding d
  * is divided by the weights' largest power of two and multiplied by 2^14, which fp16's
  * range asks for, and the products multiplied back.  A weight that is not finite makes
  * its own row's results so, and the dw that it is summed into.

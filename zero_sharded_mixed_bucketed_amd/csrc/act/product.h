@@ -53,12 +53,11 @@ struct Extents {
   const uint32_t* count;
   uint64_t first;
   int count_k;
-  uint32_t twice;           // 1: each that is counted stands twice
 };
 
 __device__ __forceinline__ uint64_t counted(const Extents& x, uint64_t most) {
   const uint64_t c = *x.count;
-  const uint64_t left = (c > x.first ? c - x.first : 0) << x.twice;
+  const uint64_t left = c > x.first ? c - x.first : 0;
   return left < most ? left : most;
 }
 
@@ -982,7 +981,9 @@ struct Sink {
   float* sums;             // [rows][lead] running sums, or nullptr
   int add, last;           // add what `sums` holds; the result is final
   uint64_t lead;           // cols, rounded up to a chunk
-  uint32_t twice;          // 1: a result's row is the sum of two neighbouring rows of c
+  const uint32_t* results; // in device memory, or nullptr; where c has more rows than this,
+                           // it has twice as many, and row m + *results is added to row m
+  uint32_t twice;          // whether it has
 
   template <typename T>
   __device__ __forceinline__ void finish(uint64_t m, uint64_t n, float (&x)[8]) const {
@@ -1041,6 +1042,7 @@ struct Sink {
   struct Old {};
 
   __device__ __forceinline__ void cut(uint32_t splits, uint64_t m_all) {
+    twice = results && m_all > *results;
     if (splits == 1 && !twice) partial = nullptr;
     split_size = m_all * lead;
   }
@@ -1184,21 +1186,23 @@ struct Sink {
   }
 };
 
-// Adds the splits' partial sums, and those of rows that stand twice, in their order, eight neighbouring columns a thread.
+// Adds the splits' partial sums, and those of rows that stand twice, in their order, eight
+// neighbouring columns a thread.
 template <typename T>
 __global__ __launch_bounds__(kMulThreads) void join_kernel(Sink s, Extents x, uint32_t tile_m,
                                                            uint32_t tiles_n) {
   const uint64_t m_all = x.count && !x.count_k ? counted(x, x.m) : x.m;
   const uint32_t tiles = static_cast<uint32_t>((m_all + tile_m - 1) / tile_m) * tiles_n;
   const uint32_t splits = splits_of(x.splits, x.most, x.fill, tiles);
-  if (splits == 1 && !s.twice) return;
   s.cut(splits, m_all);
+  if (splits == 1 && !s.twice) return;
+  const uint64_t rows = m_all >> s.twice;
   const uint64_t per_row = s.lead / kChunk;
   const uint64_t id = static_cast<uint64_t>(blockIdx.x) * kMulThreads + threadIdx.x;
   const uint64_t m = id / per_row, n = id % per_row * kChunk;
-  if (m >= m_all >> s.twice) return;
+  if (m >= rows) return;
   f32x4 u = {0.f, 0.f, 0.f, 0.f}, v = u;
-  const float* from = s.partial + (m << s.twice) * s.lead + n;
+  const float* from = s.partial + m * s.lead + n;
   // sixteen sums' loads under way together, however many there are
   constexpr uint32_t kAhead = 16;
   const uint32_t all = splits << s.twice;
@@ -1210,7 +1214,7 @@ __global__ __launch_bounds__(kMulThreads) void join_kernel(Sink s, Extents x, ui
       const uint32_t i = i0 + j;
       a[j] = b[j] = f32x4{0.f, 0.f, 0.f, 0.f};
       if (i >= all) continue;
-      const float* p = from + (i >> s.twice) * s.split_size + (i & s.twice) * s.lead;
+      const float* p = from + (i >> s.twice) * s.split_size + (i & s.twice) * rows * s.lead;
       a[j] = *reinterpret_cast<const f32x4*>(p);
       b[j] = *reinterpret_cast<const f32x4*>(p + 4);
     }
@@ -1349,7 +1353,7 @@ hipError_t run_product(const MulPlan& p, const Operand& a, const Operand& b, Ext
   }
   hipError_t err = hipGetLastError();
   if constexpr (!E::kPairs && E::kJoins) {
-    if (err != hipSuccess || (p.most == 1 && !e.twice)) return err;
+    if (err != hipSuccess || (p.most == 1 && !e.results)) return err;
     const uint64_t joins = (x.m * (e.lead / kChunk) + kMulThreads - 1) / kMulThreads;
     join_kernel<T><<<static_cast<uint32_t>(joins), kMulThreads, 0, stream>>>(
         e, x, static_cast<uint32_t>(p.tile), static_cast<uint32_t>(p.tiles_n));

@@ -135,7 +135,7 @@ template <typename T>
 hipError_t forward(const GatedLaunch& a, hipStream_t stream) {
   const MulPlan p = plan_product(a.rows, 2 * a.width, a.cols, forward_ways(a.cols));
   const Operand x = {a.x.p, a.x.stride, a.rows, false}, w = {a.w.p, a.w.stride, a.width, false};
-  const Extents e = {a.rows, a.width, a.cols, 1, 1, 0, nullptr, 0, 0, 0};
+  const Extents e = {a.rows, a.width, a.cols, 1, 1, 0, nullptr, 0, 0};
   const Gated g = {a.out, a.c_gate, a.c_up, a.c_out, a.width, a.act, a.format};
   return run_product<T, true, true>(p, x, w, e, g, stream);
 }
@@ -228,7 +228,7 @@ hipError_t backward(const GatedGradLaunch& a, hipStream_t stream) {
   }
   if (a.dx.p && a.rows) {
     const Operand d = {slopes, room.lead, a.rows, false}, w = {a.w.p, a.w.stride, a.cols, false};
-    const Extents x = {a.rows, a.cols, 2 * a.width, 1, 1, 0, nullptr, 0, 0, 0};
+    const Extents x = {a.rows, a.cols, 2 * a.width, 1, 1, 0, nullptr, 0, 0};
     Sink s = {};
     s.out = a.dx.p;
     s.stride = a.dx.stride;
@@ -252,7 +252,7 @@ hipError_t backward(const GatedGradLaunch& a, hipStream_t stream) {
     if (e != hipSuccess) return e;
     const Operand d = {slopes, room.lead, 2 * a.width, false};
     const Operand x = {held, room.lead_x, a.cols, false};
-    const Extents by = {2 * a.width, a.cols, a.rows, 1, 1, 0, nullptr, 0, 0, 0};
+    const Extents by = {2 * a.width, a.cols, a.rows, 1, 1, 0, nullptr, 0, 0};
     Sink s = {};
     s.out = a.dw;
     s.stride = a.dw_stride;

@@ -40,6 +40,7 @@ constexpr int kGradBits = 14;
 
 struct Head {
   uint32_t count;           // tokens with a loss
+  uint32_t stand;           // rows of g: as many, or twice (see kFewTokens)
   float held;               // 2^14 / 2^e
   float unit;               // c 2^e / 2^14
 };
@@ -47,10 +48,10 @@ struct Head {
 // The workspace: what lies where.
 struct Room {
   uint64_t piece, pieces;   // tokens of a piece
+  uint64_t least;           // rows that g has room for, however small a piece
   uint64_t lead_x, lead_z, lead_w;
   uint64_t wide;            // columns of a row of logits: whole chunks, and -infinity
   uint64_t entries;         // of a row: maxima and sums of parts of it
-  uint32_t twice;           // see kFewRows
   uint64_t rows, slots, flags, x, z, stats, ids, sums, partial, bytes;
   MulPlan logits, dx, dw;
 };
@@ -59,13 +60,17 @@ struct Room {
 // add to dW's running sums less often: 8192 tokens x 131072 words at 4096 take 22.4 ms
 // in two pieces and 22.1 in one, whose workspace is no larger, as it needs no such sums.
 constexpr uint64_t kPieceBytes = 6ull << 30;
-// Of few tokens, g's entries keep what their rounding leaves out: of a few values that hold
-// nearly all of a gradient, roundings do not average out.  A token's row of g stands twice,
-// rounded and with those rests, and so does its x; the products are bound by W's memory
-// there (14 tokens x 43264 words at 128, three entries each: relative errors of dx and dw
-// in fp16 3.3e-4 -> 2.1e-4, their own rounding's; 64 tokens x 131072 words at 4096 take 878
-// us, 65 take 840).
-constexpr uint64_t kFewRows = 64;
+// Of few tokens with a loss, g's entries keep what their rounding leaves out: a token's row
+// of g stands a second time, as zeros but for those rests, behind all others, and so does its
+// x.  A gradient's entries hold nearly all of it.  Their rounding makes dx's and dw's error
+// 1.4 times that of the results' own rounding, however many tokens there are, but only of
+// many is that what a call gets: the worst of 60 calls is 2.2 times the results' own for one
+// token (fp16, norms relative to 64 bits: 4.6e-4, with rests 2.6e-4), 1.7 for 16, 1.6 for 64
+// (3.4e-4; mean 3.05e-4) and 1.5 for 256, with rests 1.05 for 16 and more.  The rests cost 0-1%
+// up to 32 tokens (131072 words at 4096, fp16: 770 us), 7% at 64 (797 -> 854 us), 13% at 128
+// (903 -> 1011) and 28% at 256 (1131 -> 1450).  It is the tokens with a loss that count,
+// known on the device, not the rows given: 64 tokens of 1024 rows, 933 -> 964 us.
+constexpr uint32_t kFewTokens = 64;
 constexpr uint64_t kMostRows = 1ull << 22;  // of a piece: a workgroup a row in one launch
 
 Room room_of(uint64_t rows, uint64_t cols, uint64_t vocab, uint32_t top, bool dx, bool dw) {
@@ -88,8 +93,8 @@ Room room_of(uint64_t rows, uint64_t cols, uint64_t vocab, uint32_t top, bool dx
   r.rows = take(rows * 4);
   r.slots = take(rows * 4);
   r.flags = take(rows);
-  r.twice = (dx || dw) && rows <= kFewRows;
-  const uint64_t tokens = r.piece << r.twice;
+  if (dx || dw) r.least = 2 * (rows < kFewTokens ? rows : kFewTokens);
+  const uint64_t tokens = r.piece > r.least ? r.piece : r.least;
   r.x = take(tokens * r.lead_x * 2);
   const bool whole = cols % kChunk == 0;
   r.logits = plan_product(r.piece, vocab, cols, {false, true, true, whole});
@@ -98,13 +103,13 @@ Room room_of(uint64_t rows, uint64_t cols, uint64_t vocab, uint32_t top, bool dx
   r.entries = tiles * (r.logits.tile == 32 ? 4 : 2);          // one a wave's columns
   r.stats = take(r.piece * r.entries * 8);
   // cross entropy alone needs the target's logit of each row, not the row
-  if (dx || dw || top) r.z = take(r.piece * r.lead_z * 4);
+  if (dx || dw || top) r.z = take(tokens * r.lead_z * 4);
   else r.ids = take(r.piece * 8);
   uint64_t partial = 0;
   if (dx) {
     r.dx = plan_product(tokens, cols, vocab, {true, true, true, whole});
     uint64_t partials = partial_rows(r.dx, tokens);
-    if (r.twice && partials < tokens) partials = tokens;
+    if (partials < r.least) partials = r.least;
     partial = partials * r.lead_w * 4;
   }
   if (dw) {
@@ -138,7 +143,8 @@ __global__ __launch_bounds__(256) void loss_flags_kernel(VocabLaunch a, uint8_t*
 __global__ __launch_bounds__(kPickThreads) void loss_pick_kernel(VocabLaunch a,
                                                                  const uint8_t* flags,
                                                                  uint32_t* rows, uint32_t* slots,
-                                                                 Head* head, float c) {
+                                                                 Head* head, float c,
+                                                                 uint32_t few) {
   __shared__ uint32_t counts[kPickThreads / 64];
   __shared__ float tops[kPickThreads / 64];
   const uint32_t lane = threadIdx.x % 64, wave = threadIdx.x / 64;
@@ -175,16 +181,17 @@ __global__ __launch_bounds__(kPickThreads) void loss_pick_kernel(VocabLaunch a,
     e = e < -110 ? -110 : e;                            // 2^(14 - e) is finite
   }
   head->count = before;
+  head->stand = before <= few ? 2 * before : before;
   head->held = ldexpf(1.0f, kGradBits - e);
   head->unit = ldexpf(c, e - kGradBits);
 }
 
 // Brings a piece's tokens together: those at places [first, first + most) among the ones
 // with a loss.  The first piece also clears the others' loss and dx.  A wave a token.
-__global__ __launch_bounds__(256) void loss_rows_kernel(VocabLaunch a, const uint32_t* slots,
-                                                        uint64_t first, uint64_t most,
-                                                        uint16_t* to, uint64_t lead,
-                                                        uint32_t twice, int32_t* ids) {
+__global__ __launch_bounds__(256) void loss_rows_kernel(VocabLaunch a, const Head* head,
+                                                        const uint32_t* slots, uint64_t first,
+                                                        uint64_t most, uint16_t* to, uint64_t lead,
+                                                        int32_t* ids) {
   const uint64_t t = static_cast<uint64_t>(blockIdx.x) * 4 + threadIdx.x / 64;
   if (t >= a.rows) return;
   const uint32_t slot = __builtin_amdgcn_readfirstlane(slots[t]);
@@ -203,11 +210,13 @@ __global__ __launch_bounds__(256) void loss_rows_kernel(VocabLaunch a, const uin
     ids[slot - first] = id < static_cast<int64_t>(a.vocab) ? static_cast<int32_t>(id) : -1;
   }
   const uint16_t* from = a.x.p + t * a.x.stride;
-  uint16_t* row = to + ((slot - first) << twice) * lead;
+  const uint32_t count = head->count;
+  const bool twice = head->stand > count;                // first is 0
+  uint16_t* row = to + (slot - first) * lead;
   for (uint64_t c = c0; c < lead; c += 512) {
     const u32x4 w = c < a.cols ? load8(from, c, a.cols) : u32x4{0, 0, 0, 0};
     *reinterpret_cast<u32x4*>(row + c) = w;
-    if (twice) *reinterpret_cast<u32x4*>(row + lead + c) = w;
+    if (twice) *reinterpret_cast<u32x4*>(row + count * lead + c) = w;
   }
 }
 
@@ -345,13 +354,12 @@ __device__ __forceinline__ float teacher_at(const VocabLaunch& a, uint64_t t, ui
 }
 
 // One row a workgroup: its maximum and sum from its parts, its loss, and (GRAD) g in place
-// of its logits, 16 bits from the row's begin on (and with `twice` the rests of its entries
-// in the second half).
+// of its logits, 16 bits from the row's begin on, and where g's rows stand twice the rests
+// of its entries in the row's second place.
 template <typename T, bool GRAD>
 __global__ __launch_bounds__(kRowThreads) void loss_row_kernel(
     VocabLaunch a, const Head* head, const uint32_t* rows, uint64_t first, const Part* parts,
-    uint64_t entries, const float* caught, float* z_all, uint64_t lead, uint64_t wide,
-    uint32_t twice) {
+    uint64_t entries, const float* caught, float* z_all, uint64_t lead, uint64_t wide) {
   __shared__ float room[kRowThreads / 64];
   __shared__ int32_t ids[kMaxTop];
   __shared__ float shares[kMaxTop];
@@ -438,6 +446,8 @@ __global__ __launch_bounds__(kRowThreads) void loss_row_kernel(
   if constexpr (GRAD) {
     const float each = w * head->held / s, held = w * head->held;
     uint16_t* g = reinterpret_cast<uint16_t*>(z);
+    const bool twice = head->stand > head->count;
+    uint16_t* rests = reinterpret_cast<uint16_t*>(z + head->count * lead);
     const uint32_t some = a.top ? a.top : 1;
     // the entries' own values of g, from fp32 logits: an id that stands there twice
     // takes the shares of both
@@ -477,11 +487,9 @@ __global__ __launch_bounds__(kRowThreads) void loss_row_kernel(
       }
       if (c < wide) *reinterpret_cast<u32x4*>(g + c) = pack8<T>(x);
     }
-    if (twice) {
-      __syncthreads();                                  // all logits are read
+    if (twice)
       for (uint64_t c = tid * kChunk; c < wide; c += kStep)
-        *reinterpret_cast<u32x4*>(g + lead + c) = u32x4{0, 0, 0, 0};
-    }
+        *reinterpret_cast<u32x4*>(rests + c) = u32x4{0, 0, 0, 0};
     __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();
 #pragma unroll
@@ -492,7 +500,7 @@ __global__ __launch_bounds__(kRowThreads) void loss_row_kernel(
       g[ids[j]] = near;
       if (!twice) continue;
       const float rest = own[i] - lo16<T>(near);
-      g[lead + ids[j]] = static_cast<uint16_t>(pack16<T>(rest == rest ? rest : 0.0f, 0.0f));
+      rests[ids[j]] = static_cast<uint16_t>(pack16<T>(rest == rest ? rest : 0.0f, 0.0f));
     }
   }
 }
@@ -519,23 +527,23 @@ hipError_t run_loss(const VocabLaunch& a, hipStream_t stream) {
       if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     loss_pick_kernel<<<1, kPickThreads, 0, stream>>>(a, ws + r.flags, rows, slots, head,
-                                                     static_cast<float>(a.scale * a.tau));
+                                                     static_cast<float>(a.scale * a.tau),
+                                                     dx || dw ? kFewTokens : 0);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   for (uint64_t p = 0; p < r.pieces; ++p) {
     const uint64_t first = p * r.piece;
     const uint64_t most = a.rows - first < r.piece ? a.rows - first : r.piece;
-    const uint64_t tokens = most << r.twice;
-    const Operand xs = {x, r.lead_x << r.twice, most, true};
+    const uint64_t tokens = most > r.least ? most : r.least;
+    const Operand xs = {x, r.lead_x, most, true};
     const Operand w_rows = {a.w.p, a.w.stride, a.vocab, false};
     const Operand w_cols = {a.w.p, a.w.stride, a.cols, false};
-    const uint64_t lead_g = r.twice ? r.lead_z : 2 * r.lead_z;
+    const uint64_t lead_g = 2 * r.lead_z;
     const uint16_t* g = reinterpret_cast<const uint16_t*>(z);
     if (a.rows) {
-      loss_rows_kernel<<<waves, 256, 0, stream>>>(a, slots, first, most, x, r.lead_x, r.twice,
-                                                   ids);
+      loss_rows_kernel<<<waves, 256, 0, stream>>>(a, head, slots, first, most, x, r.lead_x, ids);
       if ((e = hipGetLastError()) != hipSuccess) return e;
-      const Extents ex = {most, a.vocab, a.cols, 1, 1, 0, &head->count, first, 0, 0};
+      const Extents ex = {most, a.vocab, a.cols, 1, 1, 0, &head->count, first, 0};
       const Logits logits = {z, r.lead_z, r.wide, a.vocab, 1.0f / a.tau, parts, r.entries, ids,
                              caught};
       e = run_product<T, true, true>(plan_of(r.logits, most, a.vocab), xs, w_rows, ex, logits,
@@ -544,15 +552,15 @@ hipError_t run_loss(const VocabLaunch& a, hipStream_t stream) {
       const uint32_t grid = static_cast<uint32_t>(most);
       if (dx || dw)
         loss_row_kernel<T, true><<<grid, kRowThreads, 0, stream>>>(
-            a, head, rows, first, parts, r.entries, caught, z, r.lead_z, r.wide, r.twice);
+            a, head, rows, first, parts, r.entries, caught, z, r.lead_z, r.wide);
       else
         loss_row_kernel<T, false><<<grid, kRowThreads, 0, stream>>>(
-            a, head, rows, first, parts, r.entries, caught, z, r.lead_z, r.wide, r.twice);
+            a, head, rows, first, parts, r.entries, caught, z, r.lead_z, r.wide);
       if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     if (dx && a.rows) {
       const Operand d = {g, lead_g, tokens, true};
-      const Extents ex = {tokens, a.cols, a.vocab, 1, 1, 0, &head->count, first, 0, r.twice};
+      const Extents ex = {tokens, a.cols, a.vocab, 1, 1, 0, &head->stand, first, 0};
       Sink s = {};
       s.out = a.dx.p;
       s.stride = a.dx.stride;
@@ -562,14 +570,14 @@ hipError_t run_loss(const VocabLaunch& a, hipStream_t stream) {
       s.factor = &head->unit;
       s.lead = r.lead_w;
       s.partial = partial;
-      s.twice = r.twice;
+      s.results = &head->count;
       e = run_product<T, true, false>(plan_of(r.dx, tokens, a.cols), d, w_cols, ex, s, stream);
       if (e != hipSuccess) return e;
     }
     if (dw) {
       const Operand d = {g, lead_g, a.vocab, true}, xc = {x, r.lead_x, a.cols, true};
-      const Extents ex = {a.vocab, a.cols, tokens, 1, 1, 0, a.rows ? &head->count : nullptr, first,
-                          1, r.twice};
+      const Extents ex = {a.vocab, a.cols, tokens, 1, 1, 0, a.rows ? &head->stand : nullptr, first,
+                          1};
       Sink s = {};
       s.out = a.dw;
       s.stride = a.dw_stride;
@@ -601,7 +609,8 @@ uint64_t vocab_workspace(uint64_t rows, uint64_t cols, uint64_t vocab, uint32_t 
 
 bool vocab_fits(uint64_t rows, uint64_t cols, uint64_t vocab, bool dx, bool dw) {
   const Room r = room_of(rows, cols, vocab, 0, dx, dw);
-  return product_fits(r.logits, 0, 0) && (!dx || product_fits(r.dx, r.piece, cols)) &&
+  const uint64_t tokens = r.piece > r.least ? r.piece : r.least;
+  return product_fits(r.logits, 0, 0) && (!dx || product_fits(r.dx, tokens, cols)) &&
          (!dw || product_fits(r.dw, vocab, cols));
 }
 
