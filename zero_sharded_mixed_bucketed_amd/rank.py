@@ -24,7 +24,9 @@ norm_grad and gated_grad write the gradients of a layer's tensors to their flat
 places in the local gradient (stage 1) or in the bucket that is being filled
 (stages 2 and 3), from activations kept in 8 bits (checkpoint; the guide's residual
 states); loss_grad and distill_grad begin the backward with the gradient of the
-projection onto the vocabulary.
+projection onto the vocabulary.  The local gradient is fp16, and so are the
+activations of these calls: with bf16 ones the operators themselves give a gradient in
+bf16 or fp32, which is not what the reduce reads.
 
 This module allocates with torch and calls the library; no arithmetic of the
 path happens here.
@@ -42,6 +44,11 @@ from . import (ACT_SILU, CKPT_INT8, Ckpt, adam_step_shard, block_norm_grad, ckpt
 STAGE_OS = 1
 STAGE_OS_G = 2
 STAGE_OS_G_P = 3
+
+
+def _fp16(name: str, t) -> None:
+    if t.dtype == torch.bfloat16:
+        raise ValueError(f"{name} is bf16, and the local gradient is fp16")
 
 
 class RankState:
@@ -183,6 +190,7 @@ class RankState:
                    **call) -> None:
         """gated_ffn_grad with the gradient of the block's stacked weight (2 dout.shape[1]
         x ckpt_x.cols, at flat index flat_lo) in the local gradient."""
+        _fp16("dout", dout)
         n, k = 2 * dout.shape[1], ckpt_x.cols
         dw = self.grad_slot(flat_lo, n * k, bucket, bucket_offset).view(n, k)
         gated_ffn_grad(dout, ckpt_gate, ckpt_up, w, act, dx=dx, ckpt_x=ckpt_x, dw=dw, **call)
@@ -191,11 +199,13 @@ class RankState:
                   bucket_offset: int = 0, **call) -> None:
         """vocab_loss with the gradient of the projection onto the vocabulary (w's shape,
         at flat index flat_lo) in the local gradient."""
+        _fp16("x", x)
         dw = self.grad_slot(flat_lo, w.numel(), bucket, bucket_offset).view(w.shape)
         vocab_loss(x, w, targets, loss, dx=dx, dw=dw, **call)
 
     def distill_grad(self, flat_lo: int, x, w, ids, logits, loss, dx=None, bucket=None,
                      bucket_offset: int = 0, **call) -> None:
         """distill_loss, likewise."""
+        _fp16("x", x)
         dw = self.grad_slot(flat_lo, w.numel(), bucket, bucket_offset).view(w.shape)
         distill_loss(x, w, ids, logits, loss, dx=dx, dw=dw, **call)
