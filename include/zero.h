@@ -605,10 +605,12 @@ uint64_t zero_loss_workspace(uint64_t rows, uint64_t cols, uint64_t vocab, uint3
  *   loss[t] = weights[t] (log(sum over v of exp z[t][v]) - z[t][y]),  y = targets[t]
  *   d[t][v] = weights[t] (softmax(z[t])[v] - (v == y))       (rounded to dtype)
  *   dx = scale d w;  dw = scale d^T x                        (fp32 sums, one rounding)
- * The logits are never kept: for the loss alone they are not stored at all, and for
- * gradients the workspace holds those of a piece of the tokens, 4 bytes each and about 6
- * GiB at most (or 256 tokens); besides, a copy of a piece's x and, if there are several
- * pieces, fp32 sums of dw.  Of up to 64 rows with a loss, among however many, what the
+ * No logits outlive the call, and the loss alone stores none.  For gradients the workspace
+ * holds those of a piece of the tokens, 4 bytes each: all tokens' where that is up to about
+ * 6 GiB, else 6 GiB (or 256 tokens); besides, a copy of a piece's x and, if there are
+ * several pieces, fp32 sums of dw.  For less memory, call with parts of the rows, all but
+ * the first with `accumulate` and dw in fp32, which adds them up as a call's own pieces.
+ * Of up to 64 rows with a loss, among however many, what the
  * rounding of d leaves out at the targets is kept beside it (16 bits more): a few values
  * hold nearly all of d, and the fewer they are, the further may their roundings be off
  * together.  Before its rounding d
@@ -650,7 +652,8 @@ typedef struct zero_top_logits {
  *   loss[t] = weights[t] tau^2 sum over j of q[t][j] (log q[t][j] - log p[t][i[t][j]])
  *   d[t][v] = weights[t] (p[t][v] - sum over j with i[t][j] == v of q[t][j])
  *   dx = scale tau d w;  dw = scale tau d^T x
- * A row without entries is left out.  An entry of -infinity has no share; an id that
+ * Without gradients too, the workspace holds a piece's logits, from which the entries' are
+ * read.  A row without entries is left out.  An entry of -infinity has no share; an id that
  * stands in a row twice has both shares.  An id of vocab or more, and logits that give
  * no softmax (NaN, +infinity, -infinity alone), make the row's loss NaN and its
  * gradients with it.

@@ -900,14 +900,15 @@ def _loss_arg(x, w, loss, weights, scale, dx, dw, accumulate, workspace, stream,
 def vocab_loss(x, w, targets, loss, weights=None, scale: float = 1.0, dx=None, dw=None,
                accumulate: bool = False, workspace=None, stream=None) -> None:
     """loss = weights . cross entropy of x w^T against targets, and the gradients of
-    scale * sum(loss), without keeping the logits.
+    scale * sum(loss).  The loss alone stores no logits; for gradients the workspace holds
+    those of all rows in fp32, or of as many as make 6 GiB.
 
     x: float16 or bfloat16 [rows, cols], the last hidden states; w: of its type
     [vocab, cols]; targets: contiguous int32 or int64 [rows], negative where a token has
     no loss; loss and weights (or None: ones): float32 [rows].  dx: [rows, cols] of x's
     type, or None; dw: x's type or float32 [vocab, cols], or None, added to with
     `accumulate`.  workspace: uint8 device tensor of loss_workspace bytes, or None to take
-    it from torch's allocator.
+    it from torch's allocator; parts of the rows, their dw accumulated in float32, need less.
     """
     rows = x.shape[0] if isinstance(x, torch.Tensor) and x.dim() == 2 else 0
     if not isinstance(targets, torch.Tensor) or targets.dtype not in _IDS:
@@ -926,7 +927,8 @@ def distill_loss(x, w, ids, logits, loss, temperature: float = 1.0, weights=None
     the gradients of scale * sum(loss).
 
     ids: int32 or int64 [rows, top], negative where a row has fewer entries; logits:
-    float16, bfloat16 or float32 [rows, top]; the rest as vocab_loss.
+    float16, bfloat16 or float32 [rows, top]; the rest as vocab_loss, but that the
+    workspace holds the student's logits without gradients too.
     """
     if not isinstance(ids, torch.Tensor) or ids.dtype not in _IDS:
         raise ValueError("ids must be an int32 or int64 device tensor")

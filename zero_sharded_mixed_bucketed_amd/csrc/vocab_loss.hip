@@ -1,5 +1,5 @@
 // Losses over a vocabulary, from the last hidden states x and the projection W, and
-// their gradients, without keeping the logits z = x W^T / tau:
+// their gradients, with z = x W^T / tau:
 //   cross entropy  l_t = w_t (lse_t - z_ty)
 //   distillation   l_t = w_t tau^2 sum over j of q_tj (log q_tj - (z_tj - lse_t)),
 //                  q_t the softmax of a teacher's top logits / tau
@@ -10,7 +10,8 @@
 // fp32, one pass over each row that replaces them with g in 16 bits, and the two
 // products with it.  That is three products for the three that the definition has;
 // pieces of the vocabulary with all tokens in each would need a fourth (g needs the
-// whole row's sum first).  g is the only value that is rounded on the way: at a
+// whole row's sum first).  Cross entropy alone stores no logits; distillation does for
+// its entries' sake.  g is the only value that is rounded on the way: at a
 // target p - q is formed in fp32 from fp32 logits, so what cancels there is not lost.
 //
 // Tokens without a target are left out of everything: the others are first brought
@@ -58,7 +59,9 @@ struct Room {
 
 // Bytes of a piece's logits, about (a piece has 256 tokens at least).  Larger pieces
 // add to dW's running sums less often: 8192 tokens x 131072 words at 4096 take 22.4 ms
-// in two pieces and 22.1 in one, whose workspace is no larger, as it needs no such sums.
+// in two pieces of 2 GiB with those sums, another 2 GiB, and 22.1 in one of 4 GiB.  Where
+// the sums are smaller (fewer columns, dx alone) one piece takes more memory than two;
+// callers who want less give parts of the rows.
 constexpr uint64_t kPieceBytes = 6ull << 30;
 // Of few tokens with a loss, g's entries keep what their rounding leaves out: a token's row
 // of g stands a second time, as zeros but for those rests, behind all others, and so does its
