@@ -563,6 +563,7 @@ uint64_t zero_gated_ffn_grad_workspace(uint64_t rows, uint64_t cols, uint64_t wi
  * With the held values g and u:
  *   dg = dout . u . act'(g);  du = dout . act(g)     (each rounded to dtype)
  *   dx = dg wg + du wu;  dw = [dg du]^T held(x)      (fp32 sums, one rounding)
+ * In fp16, loss scaling has to keep dg and du above 2^-14, or they lose bits.
  * dw is zero_ckpt_weight_grad's of the rounded dg and du.  rows == 0 gives a dw of 0,
  * or leaves it with `accumulate`.  workspace: 16-byte aligned device memory, written
  * by the call; calls that may run at the same time need one each.  An output must not
