@@ -43,6 +43,10 @@ struct Operand {
   bool padded;   // its fast axis is followed by zeros up to a whole chunk
 };
 
+// In a count: half of what it counts stands a second time, behind the others.  It comes
+// with the count, in one load.
+constexpr uint32_t kTwice = 1u << 31;
+
 // The sizes of a product.  A count in device memory, where there is one, says how
 // many rows of c (or, with count_k, how many k) there are past `first`, at most m
 // (k): the host knows the most only.
@@ -55,9 +59,11 @@ struct Extents {
   int count_k;
 };
 
-__device__ __forceinline__ uint64_t counted(const Extents& x, uint64_t most) {
-  const uint64_t c = *x.count;
+__device__ __forceinline__ uint64_t counted(const Extents& x, uint64_t most, bool* twice) {
+  const uint32_t held = *x.count;
+  const uint64_t c = held & ~kTwice;
   const uint64_t left = c > x.first ? c - x.first : 0;
+  *twice = (held & kTwice) != 0;
   return left < most ? left : most;
 }
 
@@ -374,9 +380,10 @@ __global__ __launch_bounds__(kMulThreads) void product_kernel(Operand a, Operand
   uint16_t* lb = la + 2 * A::kElems;
 
   uint64_t m_all = x.m, k_all = x.k;
+  bool twice = false;
   if (x.count) {
     uint64_t& of = x.count_k ? k_all : m_all;
-    of = counted(x, of);
+    of = counted(x, of, &twice);
   }
   const uint32_t tiles_m = static_cast<uint32_t>((m_all + TM - 1) / TM);
   constexpr int kOutN = E::kPairs ? TN / 2 : TN;            // columns of c a tile
@@ -384,7 +391,7 @@ __global__ __launch_bounds__(kMulThreads) void product_kernel(Operand a, Operand
   const uint32_t splits = splits_of(x.splits, x.most, x.fill, tiles_m * tiles_n);
   const uint32_t wgs = tiles_m * tiles_n * splits;
   if (blockIdx.x >= wgs) return;
-  epilogue.cut(splits, m_all);
+  epilogue.cut(splits, m_all, twice);
   const Spot at = spot_of(blockIdx.x, wgs, tiles_m, tiles_n);
   const uint64_t m0 = static_cast<uint64_t>(at.m) * TM, n0 = static_cast<uint64_t>(at.n) * kOutN;
   const uint64_t per = ((k_all + splits - 1) / splits + kMulDepth - 1) / kMulDepth * kMulDepth;
@@ -673,9 +680,10 @@ __global__ __launch_bounds__(kMulThreads, 1) void ring_kernel(Operand a, Operand
 
   const float by = epilogue.load_factor();
   uint64_t m_all = x.m, k_all = x.k;
+  bool twice = false;
   if (x.count) {
     uint64_t& of = x.count_k ? k_all : m_all;
-    of = counted(x, of);
+    of = counted(x, of, &twice);
   }
   constexpr int kOutN = E::kPairs ? kRingTile / 2 : kRingTile;
   const uint32_t tiles_m = static_cast<uint32_t>((m_all + kRingTile - 1) / kRingTile);
@@ -683,7 +691,7 @@ __global__ __launch_bounds__(kMulThreads, 1) void ring_kernel(Operand a, Operand
   const uint32_t splits = splits_of(x.splits, x.most, x.fill, tiles_m * tiles_n);
   const uint32_t wgs = tiles_m * tiles_n * splits;
   if (blockIdx.x >= wgs) return;
-  epilogue.cut(splits, m_all);
+  epilogue.cut(splits, m_all, twice);
   const uint64_t per = ((k_all + splits - 1) / splits + kMulDepth - 1) / kMulDepth * kMulDepth;
   const uint32_t lane = threadIdx.x % 64;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
@@ -869,14 +877,15 @@ __global__ __launch_bounds__(kMulThreads) void slim_kernel(Operand a, Operand b,
   const uint32_t lds0 = static_cast<uint32_t>(
       reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)lds));
 
-  const uint64_t m_all = x.count ? counted(x, x.m) : x.m;
+  bool twice = false;
+  const uint64_t m_all = x.count ? counted(x, x.m, &twice) : x.m;
   constexpr int kOutN = E::kPairs ? kSlimCols / 2 : kSlimCols;
   const uint32_t tiles_m = static_cast<uint32_t>((m_all + kMulFrag - 1) / kMulFrag);
   const uint32_t tiles_n = static_cast<uint32_t>((x.n + kOutN - 1) / kOutN);
   const uint32_t splits = splits_of(x.splits, x.most, x.fill, tiles_m * tiles_n);
   const uint32_t wgs = tiles_m * tiles_n * splits;
   if (blockIdx.x >= wgs) return;
-  epilogue.cut(splits, m_all);
+  epilogue.cut(splits, m_all, twice);
   const Spot at = spot_of(blockIdx.x, wgs, tiles_m, tiles_n);
   const uint64_t m0 = static_cast<uint64_t>(at.m) * kMulFrag;
   const uint64_t n0 = static_cast<uint64_t>(at.n) * kOutN;
@@ -981,9 +990,8 @@ struct Sink {
   float* sums;             // [rows][lead] running sums, or nullptr
   int add, last;           // add what `sums` holds; the result is final
   uint64_t lead;           // cols, rounded up to a chunk
-  const uint32_t* results; // in device memory, or nullptr; where c has more rows than this,
-                           // it has twice as many, and row m + *results is added to row m
-  uint32_t twice;          // whether it has
+  uint32_t twice;          // 1: rows of c may stand twice (Extents): row m and the row half
+                           // of them further on are added up
 
   template <typename T>
   __device__ __forceinline__ void finish(uint64_t m, uint64_t n, float (&x)[8]) const {
@@ -1041,8 +1049,8 @@ struct Sink {
   struct Row {};
   struct Old {};
 
-  __device__ __forceinline__ void cut(uint32_t splits, uint64_t m_all) {
-    twice = results && m_all > *results;
+  __device__ __forceinline__ void cut(uint32_t splits, uint64_t m_all, bool stand_twice) {
+    twice = twice && stand_twice;
     if (splits == 1 && !twice) partial = nullptr;
     split_size = m_all * lead;
   }
@@ -1191,10 +1199,11 @@ struct Sink {
 template <typename T>
 __global__ __launch_bounds__(kMulThreads) void join_kernel(Sink s, Extents x, uint32_t tile_m,
                                                            uint32_t tiles_n) {
-  const uint64_t m_all = x.count && !x.count_k ? counted(x, x.m) : x.m;
+  bool twice = false;
+  const uint64_t m_all = x.count && !x.count_k ? counted(x, x.m, &twice) : x.m;
   const uint32_t tiles = static_cast<uint32_t>((m_all + tile_m - 1) / tile_m) * tiles_n;
   const uint32_t splits = splits_of(x.splits, x.most, x.fill, tiles);
-  s.cut(splits, m_all);
+  s.cut(splits, m_all, twice);
   if (splits == 1 && !s.twice) return;
   const uint64_t rows = m_all >> s.twice;
   const uint64_t per_row = s.lead / kChunk;
@@ -1353,7 +1362,7 @@ hipError_t run_product(const MulPlan& p, const Operand& a, const Operand& b, Ext
   }
   hipError_t err = hipGetLastError();
   if constexpr (!E::kPairs && E::kJoins) {
-    if (err != hipSuccess || (p.most == 1 && !e.results)) return err;
+    if (err != hipSuccess || (p.most == 1 && !e.twice)) return err;
     const uint64_t joins = (x.m * (e.lead / kChunk) + kMulThreads - 1) / kMulThreads;
     join_kernel<T><<<static_cast<uint32_t>(joins), kMulThreads, 0, stream>>>(
         e, x, static_cast<uint32_t>(p.tile), static_cast<uint32_t>(p.tiles_n));

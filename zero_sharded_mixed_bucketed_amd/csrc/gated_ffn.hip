@@ -88,7 +88,7 @@ struct Gated {
   struct Row {};
   struct Old {};
 
-  __device__ __forceinline__ void cut(uint32_t, uint64_t) {}
+  __device__ __forceinline__ void cut(uint32_t, uint64_t, bool) {}
   __device__ __forceinline__ bool stores() const { return true; }
   __device__ __forceinline__ bool simple() const { return false; }
   __device__ __forceinline__ float load_factor() const { return 1.0f; }

@@ -41,7 +41,7 @@ constexpr int kGradBits = 14;
 
 struct Head {
   uint32_t count;           // tokens with a loss
-  uint32_t stand;           // rows of g: as many, or twice (see kFewTokens)
+  uint32_t stand;           // rows of g: as many, or twice with kTwice (see kFewTokens)
   float held;               // 2^14 / 2^e
   float unit;               // c 2^e / 2^14
 };
@@ -184,7 +184,7 @@ __global__ __launch_bounds__(kPickThreads) void loss_pick_kernel(VocabLaunch a,
     e = e < -110 ? -110 : e;                            // 2^(14 - e) is finite
   }
   head->count = before;
-  head->stand = before <= few ? 2 * before : before;
+  head->stand = before <= few ? 2 * before | kTwice : before;
   head->held = ldexpf(1.0f, kGradBits - e);
   head->unit = ldexpf(c, e - kGradBits);
 }
@@ -197,6 +197,7 @@ __global__ __launch_bounds__(256) void loss_rows_kernel(VocabLaunch a, const Hea
                                                         int32_t* ids) {
   const uint64_t t = static_cast<uint64_t>(blockIdx.x) * 4 + threadIdx.x / 64;
   if (t >= a.rows) return;
+  const uint32_t count = head->count, stand = head->stand;
   const uint32_t slot = __builtin_amdgcn_readfirstlane(slots[t]);
   const uint64_t c0 = threadIdx.x % 64 * kChunk;
   if (slot == UINT32_MAX) {
@@ -213,8 +214,7 @@ __global__ __launch_bounds__(256) void loss_rows_kernel(VocabLaunch a, const Hea
     ids[slot - first] = id < static_cast<int64_t>(a.vocab) ? static_cast<int32_t>(id) : -1;
   }
   const uint16_t* from = a.x.p + t * a.x.stride;
-  const uint32_t count = head->count;
-  const bool twice = head->stand > count;                // first is 0
+  const bool twice = (stand & kTwice) != 0;              // first is 0
   uint16_t* row = to + (slot - first) * lead;
   for (uint64_t c = c0; c < lead; c += 512) {
     const u32x4 w = c < a.cols ? load8(from, c, a.cols) : u32x4{0, 0, 0, 0};
@@ -231,8 +231,8 @@ struct Part {
 
 // A piece's logits, scaled: the maximum and sum of each wave's columns of a row, from the
 // fp32 sums where they are (a row is then read once less: 4096 x 131072 words, 1060 ->
-// 690 us for the pass over them), and what is wanted of the logits themselves: all (those past the vocabulary
-// are -infinity up to `wide`), or each row's target's.
+// 690 us for the pass over them), and what is wanted of the logits themselves: all (those
+// past the vocabulary are -infinity up to `wide`), or each row's target's.
 struct Logits {
   static constexpr bool kPairs = false, kRows = true, kJoins = false, kOld = false, kAdds = false;
   struct Old {};
@@ -244,7 +244,7 @@ struct Logits {
   const int32_t* ids;       // of the targets, without z
   float* caught;
 
-  __device__ __forceinline__ void cut(uint32_t, uint64_t) {}
+  __device__ __forceinline__ void cut(uint32_t, uint64_t, bool) {}
   __device__ __forceinline__ bool stores() const { return z != nullptr; }
   __device__ __forceinline__ float load_factor() const { return 1.0f; }
   __device__ __forceinline__ uint64_t row_of(int, uint32_t, uint64_t m) const { return m; }
@@ -449,7 +449,7 @@ __global__ __launch_bounds__(kRowThreads) void loss_row_kernel(
   if constexpr (GRAD) {
     const float each = w * head->held / s, held = w * head->held;
     uint16_t* g = reinterpret_cast<uint16_t*>(z);
-    const bool twice = head->stand > head->count;
+    const bool twice = (head->stand & kTwice) != 0;
     uint16_t* rests = reinterpret_cast<uint16_t*>(z + head->count * lead);
     const uint32_t some = a.top ? a.top : 1;
     // the entries' own values of g, from fp32 logits: an id that stands there twice
@@ -573,7 +573,7 @@ hipError_t run_loss(const VocabLaunch& a, hipStream_t stream) {
       s.factor = &head->unit;
       s.lead = r.lead_w;
       s.partial = partial;
-      s.results = &head->count;
+      s.twice = 1;
       e = run_product<T, true, false>(plan_of(r.dx, tokens, a.cols), d, w_cols, ex, s, stream);
       if (e != hipSuccess) return e;
     }
